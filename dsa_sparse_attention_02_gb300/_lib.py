@@ -27,6 +27,9 @@ EXPORTED = (
     "dsa_decode_step_hist", "dsa_decode_step_hist_workspace_size",
     "dsa_cache_append", "dsa_cache_append_workspace_size",
     "dsa_indexer_prepare", "dsa_indexer_prepare_workspace_size", "dsa_stage_copy",
+    "dsa_gqa_append", "dsa_gqa_append_workspace_size", "dsa_gqa_attend", "dsa_gqa_attend_workspace_size",
+    "dsa_block_select", "dsa_block_select_workspace_size",
+    "dsa_gqa_attend_blocks", "dsa_gqa_attend_blocks_workspace_size",
     "dsa_get_error", "dsa_clear_error", "dsa_wait_probe", "dsa_status_string", "dsa_last_error", "dsa_abi_version",
 )
 
@@ -60,6 +63,12 @@ class dsa_step_args_t(C.Structure):
                 ("out", C.c_void_p), ("lse", C.c_void_p)]
 
 
+class dsa_gqa_cache_t(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("Hkv", C.c_int32), ("D", C.c_int32),
+                ("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("k_mean", C.c_void_p), ("k_mean_scale", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -74,6 +83,7 @@ def load(path: str = LIB_PATH):
     P, I32, I64, SZ, F = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
     G = C.POINTER(dsa_geom_t)
     S = C.POINTER(dsa_step_args_t)
+    K = C.POINTER(dsa_gqa_cache_t)
     sig = {
         "dsa_indexer_scores": (C.c_int, [G, C.c_int, I32, P, P, P, P, P, P, I64, P, SZ, P]),
         "dsa_indexer_scores_workspace_size": (SZ, [G]),
@@ -94,6 +104,14 @@ def load(path: str = LIB_PATH):
         "dsa_indexer_prepare": (C.c_int, [G, I32, I32, P, P, P, P, P, P, F, P, P, P, P, P, SZ, P]),
         "dsa_indexer_prepare_workspace_size": (SZ, [G]),
         "dsa_stage_copy": (C.c_int, [P, P, SZ, P]),
+        "dsa_gqa_append": (C.c_int, [G, K, P, I64, P, I64, I32, P, I64, P, I32, P, P, P, SZ, P]),
+        "dsa_gqa_append_workspace_size": (SZ, [G, K]),
+        "dsa_gqa_attend": (C.c_int, [G, K, I32, P, I64, F, P, P, P, SZ, P]),
+        "dsa_gqa_attend_workspace_size": (SZ, [G, K, I32]),
+        "dsa_block_select": (C.c_int, [G, K, I32, P, I64, I32, I32, I32, P, P, SZ, P]),
+        "dsa_block_select_workspace_size": (SZ, [G, K, I32]),
+        "dsa_gqa_attend_blocks": (C.c_int, [G, K, I32, P, I64, P, I32, F, P, P, P, SZ, P]),
+        "dsa_gqa_attend_blocks_workspace_size": (SZ, [G, K, I32, I32]),
         "dsa_get_error": (C.c_int, [P, P]),
         "dsa_clear_error": (C.c_int, [P, P]),
         "dsa_wait_probe": (C.c_int, [P, SZ, C.c_uint32, P]),
@@ -288,6 +306,140 @@ def dsa_decode_step_hist(args: dsa_step_args_t, ws: torch.Tensor, stream=None):
     """dsa_decode_step with the top-k's first radix digit counted by the indexer."""
     st = load().dsa_decode_step_hist(C.byref(args), _dptr(ws), ws.numel(), _stream(stream))
     _check(st, "dsa_decode_step_hist")
+
+
+class GqaCache:
+    """Handle of a grouped-query cache: codes k, v [P, Hkv, 64, D] (torch.float8_e4m3fn or
+    torch.int8), their scales [P, Hkv] fp32 and, for dsa_block_select, the blocks' key
+    means [P, Hkv, D] int8 with scales [P, Hkv] fp32."""
+
+    def __init__(self, k, v, k_scale, v_scale, k_mean=None, k_mean_scale=None):
+        kinds = {torch.float8_e4m3fn: DSA_E4M3, torch.int8: DSA_I8}
+        if k.dtype not in kinds or k.dim() != 4 or k.shape[2] != 64:
+            raise TypeError("k must be a [P, Hkv, 64, D] tensor of float8_e4m3fn or int8 codes")
+        P, Hkv, _, D = k.shape
+        like = {"k": (k, k.dtype, (P, Hkv, 64, D)), "v": (v, k.dtype, (P, Hkv, 64, D)),
+                "k_scale": (k_scale, torch.float32, (P, Hkv)), "v_scale": (v_scale, torch.float32, (P, Hkv)),
+                "k_mean": (k_mean, torch.int8, (P, Hkv, D)), "k_mean_scale": (k_mean_scale, torch.float32, (P, Hkv))}
+        if (k_mean is None) != (k_mean_scale is None):
+            raise TypeError("k_mean and k_mean_scale go together")
+        for name, (t, dtype, shape) in like.items():
+            if t is None and name in ("k_mean", "k_mean_scale"):
+                continue
+            if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+            if t.device != k.device:
+                raise TypeError(f"{name} is on {t.device}, k on {k.device}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k_mean, self.k_mean_scale = k_mean, k_mean_scale
+        self.Hkv, self.D, self.num_pages, self.device = int(Hkv), int(D), int(P), k.device
+        self.c = dsa_gqa_cache_t(kinds[k.dtype], self.Hkv, self.D, _dptr(k), _dptr(v), _dptr(k_scale), _dptr(v_scale),
+                                 _dptr(k_mean), _dptr(k_mean_scale))
+
+    @property
+    def ref(self):
+        return C.byref(self.c)
+
+
+def _gqa_call(geom: Geometry, cache: GqaCache, ws, stream):
+    """Checks common to the grouped-query calls; the stream to enqueue on."""
+    if cache.num_pages < geom.num_pages:
+        raise ValueError(f"the cache has {cache.num_pages} pages, the geometry {geom.num_pages}")
+    if cache.device.index != torch.cuda.current_device() or geom.seq_lens.device != cache.device or ws.device != cache.device:
+        raise ValueError(f"cache on {cache.device}, geometry on {geom.seq_lens.device}, workspace on {ws.device}: "
+                         f"all must be on the current device, cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def _heads(name, t, geom, cache, heads=None, dtype=torch.bfloat16, strided=True):
+    """Address and token stride of a [T, heads, D] tensor (heads of a token side by side)."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != geom.T or t.shape[2] != cache.D or (heads and t.shape[1] != heads):
+        raise TypeError(f"{name} must be a {dtype} tensor of shape [{geom.T}, {heads or 'H'}, {cache.D}]")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != cache.D and t.shape[1] > 1) or (not strided and not t.is_contiguous()):
+        raise TypeError(f"{name}: " + ("each token's heads must lie side by side" if strided else "must be contiguous"))
+    return _dptr(t), (s0 if t.shape[0] > 1 else t.shape[1] * cache.D)
+
+
+def _plain(name, t, dtype, shape, cache):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return _dptr(t)
+
+
+def dsa_gqa_append_workspace_size(geom: Geometry, cache: GqaCache) -> int:
+    return int(load().dsa_gqa_append_workspace_size(geom.ref, cache.ref))
+
+
+def dsa_gqa_append(geom: Geometry, cache: GqaCache, k_new, v_new, q_in=None, q_out=None, rope_dim: int = 0,
+                   rope_cos=None, rope_sin=None, ws=None, stream=None):
+    """Rotates the new tokens' keys (and queries into q_out), quantises keys and values
+    into the cache's blocks and refreshes the blocks' means."""
+    st = _gqa_call(geom, cache, ws, stream)
+    k, ks = _heads("k_new", k_new, geom, cache, cache.Hkv)
+    v, vs = _heads("v_new", v_new, geom, cache, cache.Hkv)
+    H, q, qs, qo = 0, None, 0, None
+    if q_in is not None:
+        H = int(q_in.shape[1])
+        q, qs = _heads("q_in", q_in, geom, cache)
+        qo, _ = _heads("q_out", q_out, geom, cache, H, strided=False)
+    cos = sin = None
+    if rope_dim:
+        table = (geom.max_seq_len, rope_dim // 2)
+        cos, sin = (_plain(n, t, torch.float32, table, cache) for n, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)))
+    _check(load().dsa_gqa_append(geom.ref, cache.ref, k, ks, v, vs, H, q, qs, qo, int(rope_dim), cos, sin, _dptr(ws),
+                                 ws.numel(), st), "dsa_gqa_append")
+
+
+def dsa_gqa_attend_workspace_size(geom: Geometry, cache: GqaCache, H: int) -> int:
+    return int(load().dsa_gqa_attend_workspace_size(geom.ref, cache.ref, int(H)))
+
+
+def dsa_gqa_attend(geom: Geometry, cache: GqaCache, q, sm_scale: float, out, lse, ws, stream=None):
+    """Causal grouped-query attention of q [T, H, D] over the whole context into out
+    [T, H, D] bf16 and lse [T, H] fp32 (or None)."""
+    st = _gqa_call(geom, cache, ws, stream)
+    H = int(q.shape[1])
+    qp, qs = _heads("q", q, geom, cache)
+    o, _ = _heads("out", out, geom, cache, H, strided=False)
+    le = None if lse is None else _plain("lse", lse, torch.float32, (geom.T, H), cache)
+    _check(load().dsa_gqa_attend(geom.ref, cache.ref, H, qp, qs, float(sm_scale), o, le, _dptr(ws), ws.numel(), st),
+           "dsa_gqa_attend")
+
+
+def dsa_block_select_workspace_size(geom: Geometry, cache: GqaCache, n_sel: int) -> int:
+    return int(load().dsa_block_select_workspace_size(geom.ref, cache.ref, int(n_sel)))
+
+
+def dsa_block_select(geom: Geometry, cache: GqaCache, q, n_sel: int, n_first: int, n_last: int, blocks, ws, stream=None):
+    """The n_sel blocks of each (token, key head) that score best by their means, the first
+    n_first and last n_last visible ones always among them, into blocks [T, Hkv, n_sel]."""
+    st = _gqa_call(geom, cache, ws, stream)
+    H = int(q.shape[1])
+    qp, qs = _heads("q", q, geom, cache)
+    bp = _plain("blocks", blocks, torch.int32, (geom.T, cache.Hkv, int(n_sel)), cache)
+    _check(load().dsa_block_select(geom.ref, cache.ref, H, qp, qs, int(n_sel), int(n_first), int(n_last), bp, _dptr(ws),
+                                   ws.numel(), st), "dsa_block_select")
+
+
+def dsa_gqa_attend_blocks_workspace_size(geom: Geometry, cache: GqaCache, H: int, n_sel: int) -> int:
+    return int(load().dsa_gqa_attend_blocks_workspace_size(geom.ref, cache.ref, int(H), int(n_sel)))
+
+
+def dsa_gqa_attend_blocks(geom: Geometry, cache: GqaCache, q, blocks, sm_scale: float, out, lse, ws, stream=None):
+    """dsa_gqa_attend over the listed blocks [T, Hkv, n_sel] of each (token, key head)."""
+    st = _gqa_call(geom, cache, ws, stream)
+    H, n = int(q.shape[1]), int(blocks.shape[-1])
+    qp, qs = _heads("q", q, geom, cache)
+    bp = _plain("blocks", blocks, torch.int32, (geom.T, cache.Hkv, n), cache)
+    o, _ = _heads("out", out, geom, cache, H, strided=False)
+    le = None if lse is None else _plain("lse", lse, torch.float32, (geom.T, H), cache)
+    _check(load().dsa_gqa_attend_blocks(geom.ref, cache.ref, H, qp, qs, bp, n, float(sm_scale), o, le, _dptr(ws),
+                                        ws.numel(), st), "dsa_gqa_attend_blocks")
 
 
 def dsa_stage_copy(dst, src, nbytes: int, stream=None):

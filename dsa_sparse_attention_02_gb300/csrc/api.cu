@@ -68,12 +68,13 @@ bool encode_mla_q_map(CUtensorMap* map_q, const void* q, int T, int H) {
 
 namespace {
 
-constexpr size_t kHeaderBytes = 256;
 constexpr int kMaxTopk = 16384;
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int kv_format_of(dsa_dtype_t dt) { return dt == DSA_E4M3 ? kKvE4m3 : dt == DSA_I8 ? kKvInt8 : kKvBf16; }
+
+}  // namespace
+
+namespace dsa {
 
 int num_sms() {
   static int cache[64] = {0};
@@ -85,10 +86,6 @@ int num_sms() {
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
-
-}  // namespace
-
-namespace dsa {
 
 dsa_status_t check_geom(const dsa_geom_t* g) {
   if (!g) return DSA_ERR_INVALID_ARG;
@@ -150,10 +147,6 @@ dsa_status_t resolve_outputs(const dsa_geom_t* g, int H, void* out, float* lse, 
   return DSA_OK;
 }
 
-}  // namespace dsa
-
-namespace {
-
 GeomDev to_dev(const dsa_geom_t* g) {
   GeomDev d;
   d.B = g->B; d.T = g->T; d.max_seq_len = g->max_seq_len; d.num_pages = g->num_pages; d.bt_stride = g->bt_stride;
@@ -161,11 +154,15 @@ GeomDev to_dev(const dsa_geom_t* g) {
   return d;
 }
 
-dsa_status_t from_cuda(cudaError_t e, const char* what = "kernel launch") {
+dsa_status_t from_cuda(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return DSA_OK;
   set_last_error(what, cudaGetErrorString(e));
   return DSA_ERR_CUDA;
 }
+
+}  // namespace dsa
+
+namespace {
 
 // ---------------------------------------------------------------- indexer
 dsa_status_t check_indexer(const dsa_geom_t* g, dsa_dtype_t dt, int Hi, const void* q_idx, const float* q_scale,

@@ -136,7 +136,68 @@ struct PrepArgs {
 };
 cudaError_t indexer_prep_launch(const PrepArgs& A, cudaStream_t st);
 
+// ---- grouped-query attention over an 8-bit paged cache (gqa_*.cu; entry points in gqa_api.cu)
+struct GqaCacheDev {
+  bool i8;                      // int8 codes (else e4m3)
+  int Hkv, D;
+  uint8_t* k;                   // [P, Hkv, 64, D]
+  uint8_t* v;
+  float* k_scale;               // [P, Hkv]
+  float* v_scale;
+  int8_t* k_mean;               // [P, Hkv, D] or null
+  float* k_mean_scale;          // [P, Hkv] or null
+};
+struct GqaAppendArgs {
+  GeomDev g;
+  GqaCacheDev c;
+  const __nv_bfloat16* k_new;   // token t at t * k_stride
+  const __nv_bfloat16* v_new;
+  const __nv_bfloat16* q_in;    // or null
+  __nv_bfloat16* q_out;         // [T, G * Hkv, D]
+  int64_t k_stride, v_stride, q_stride;
+  int G;                        // query heads per key head
+  int parts;                    // blocks of threads per (block, key head): the query heads are spread over them
+  int rope_dim;
+  const float* rope_cos;
+  const float* rope_sin;
+  int* err;
+};
+cudaError_t gqa_append_launch(const GqaAppendArgs& A, cudaStream_t st);
+struct GqaSelectArgs {
+  GeomDev g;
+  GqaCacheDev c;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int G;
+  int n_sel, n_first, n_last;
+  int* blocks;                  // [T, Hkv, n_sel]
+  int* err;
+};
+cudaError_t gqa_select_launch(const GqaSelectArgs& A, int num_sms, cudaStream_t st);
+struct GqaAttendArgs {
+  GeomDev g;
+  GqaCacheDev c;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  int G;
+  float scale_log2;             // sm_scale * log2(e)
+  const int* blocks;            // [T, Hkv, n_sel], or null: the whole context
+  int n_sel;
+  __nv_bfloat16* out;           // [T, G * Hkv, D]
+  float* lse;                   // [T, G * Hkv] or null
+  void* scratch;
+  int* err;
+};
+size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int Hkv, int D, int G, int n_sel, int num_sms);
+cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st);
+
 // ---- host helpers defined in api.cu
+constexpr size_t kHeaderBytes = 256;   // workspace header: the error word comes first
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int num_sms();                         // of the current device
+GeomDev to_dev(const dsa_geom_t* g);
+dsa_status_t from_cuda(cudaError_t e, const char* what = "kernel launch");
 // Host-side argument checks shared by every entry point that takes these arguments.
 dsa_status_t check_geom(const dsa_geom_t* g);
 dsa_status_t check_attend(const dsa_geom_t* g, dsa_dtype_t dt, int H, const void* q, const void* kv, const int* idx,

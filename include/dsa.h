@@ -362,6 +362,123 @@ dsa_status_t dsa_decode_step_bounded(const dsa_step_args_t* args, size_t score_b
                                      size_t ws_bytes, void* stream);
 size_t dsa_decode_step_bounded_workspace_size(const dsa_step_args_t* args, size_t score_budget_bytes);
 
+/*
+ * Grouped-query attention over a paged 8-bit cache: the operators below serve layers
+ * with keys and values by head (drafting heads, grouped-query layers) beside the latent
+ * ones, on the same requests, positions and block tables (dsa_geom_t).
+ *
+ * A block is one page of one key head: 64 tokens of D values. Its keys share one fp32
+ * scale, its values another; key d of the block's token i is code * k_scale. A block's
+ * keys may also have an int8 mean, which dsa_block_select scores.
+ *
+ * New tokens and queries are flattened as everywhere (token t of request b at position
+ * seq_lens[b] - n_b + j). Beside the common conventions, in these operators:
+ *   - rows t >= cu_q[B] (padding behind the last request's tokens) are left as they were;
+ *   - a token at a negative position (a padding request whose seq_lens is below its new
+ *     tokens, e.g. 0) sees no key and is not stored; this is not an error;
+ *   - a request with seq_lens > max_seq_len, or with cu_q decreasing or above T, sets
+ *     DSA_ERR_BAD_INDEX; its tokens are treated as at negative positions where they lie
+ *     in [0, T), as are tokens below cu_q[0];
+ *   - a page id out of range sets DSA_ERR_BAD_INDEX; its tokens are not stored, and are
+ *     seen by no query.
+ */
+typedef struct {
+  dsa_dtype_t dtype;    /* DSA_E4M3 or DSA_I8: the codes of k and v                           */
+  int32_t Hkv;          /* key heads, 1..128                                                  */
+  int32_t D;            /* head size, 64 or 128                                               */
+  void* k;              /* device [num_pages, Hkv, 64, D] codes, 16-byte aligned              */
+  void* v;              /* the same of the values                                             */
+  float* k_scale;       /* device [num_pages, Hkv], finite, > 0 for blocks that hold tokens   */
+  float* v_scale;
+  int8_t* k_mean;       /* device [num_pages, Hkv, D] or NULL, 16-byte aligned                */
+  float* k_mean_scale;  /* device [num_pages, Hkv], NULL exactly if k_mean is                 */
+} dsa_gqa_cache_t;
+
+/*
+ * dsa_gqa_append -- rotates the new tokens' keys (and queries), quantises keys and
+ *   values into their blocks and refreshes the blocks' means, in one launch.
+ *   k_new, v_new bf16, token t's head h at t*stride + h*D (strides in elements, multiples
+ *     of 8, >= Hkv*D: slices of one fused projection's output are taken as they are).
+ *   q_in, q_out: bf16 queries, q_in with a stride of its own (>= H*D), q_out [T, H, D]
+ *     contiguous: q_out = bf16(rotated q_in). Both NULL: keys and values alone (H is then
+ *     ignored). H = g*Hkv, 1 <= g <= 16. q_out overlaps no input.
+ *   Rotation on the first rope_dim values (0, or a multiple of 8 up to D), for
+ *     i < r = rope_dim/2, with cos/sin from rope_cos, rope_sin [max_seq_len, r] fp32 at
+ *     the token's position: y_i = x_i*cos_i - x_{i+r}*sin_i, y_{i+r} = x_{i+r}*cos_i +
+ *     x_i*sin_i, in fp32, the products and the sum each rounded; the rest pass through.
+ *     rope_dim 0: no rotation, the tables are NULL or ignored.
+ *   For each block that receives tokens, with amax the largest finite magnitude among its
+ *     new values, qmax 448 (e4m3) or 127 (int8), and s_old its scale if it held tokens of
+ *     the request before the first new one, else 0:
+ *     s = max(s_old, amax / qmax, 2^-100); if s > s_old the older codes become
+ *     round(code * (s_old / s)); new codes are round(y / s). Quotients and products in
+ *     fp32, rounding to nearest even, saturating at +-qmax; a NaN becomes the e4m3 NaN
+ *     code, or int8 0.
+ *   With k_mean: over the block's n tokens of the request, m = the sum of its key codes
+ *     (exact in fp32; a NaN code counts as 0), u = max|m| / 127: k_mean = round(m / u)
+ *     (0 if u is 0), k_mean_scale = u * s / n.
+ *   No other token's codes and no other block's scale or mean change. Two requests of a
+ *   call must not append to the same page.
+ *   ws: 256 bytes (the header).
+ */
+dsa_status_t dsa_gqa_append(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, const void* k_new,
+                            int64_t k_stride, const void* v_new, int64_t v_stride, int32_t H, const void* q_in,
+                            int64_t q_stride, void* q_out, int32_t rope_dim, const float* rope_cos,
+                            const float* rope_sin, void* ws, size_t ws_bytes, void* stream);
+size_t dsa_gqa_append_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache);
+
+/*
+ * dsa_gqa_attend -- causal grouped-query attention over the whole context.
+ *   q bf16, token t's head h at t*q_stride + h*D (q_stride in elements, a multiple of 8,
+ *     >= H*D), 16-byte aligned; head h reads key head h / g, g = H / Hkv, 1 <= g <= 16.
+ *   z_s = sm_scale * q . k_s over the keys s <= pos(t):
+ *     out [T, H, D] bf16 = sum_s softmax(z)_s * v_s; lse [T, H] fp32 (or NULL) =
+ *     ln(sum_s exp(z_s)). A row that sees no key gives out = 0 and lse = -inf. What lies
+ *     in a key or value that a row does not see (NaN codes, pages of other requests) does
+ *     not reach it. out overlaps no input; out 16-byte aligned.
+ *   sm_scale finite and >= 0.
+ */
+dsa_status_t dsa_gqa_attend(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H, const void* q,
+                            int64_t q_stride, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                            void* stream);
+size_t dsa_gqa_attend_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H);
+
+/*
+ * dsa_block_select -- the blocks each query token and key head should attend to, by a
+ *   score of the blocks' means (the pooled-key selection of lmdeploy "glm5.3-flash
+ *   support", Capacity improvement, in a form of its own).
+ *   a = round(qs / (max|qs| / 127)) with qs the sum of the group's g queries (fp32, added
+ *   in head order; a is 0 if qs is), score[c] = (a . k_mean[c]) * k_mean_scale[c]: a whole
+ *   number, exact, times the scale in fp32, so selections do not depend on the order of
+ *   the sums. A NaN in qs counts as 0 in a; a NaN score ranks below every number.
+ *   Of the nv = pos(t)/64 + 1 blocks the token sees, the first n_first and the last n_last
+ *   rank above all others; the n_sel highest are taken, ties to the lower block.
+ *   blocks [T, Hkv, n_sel] int32: their numbers within the request, ascending, then -1.
+ *   1 <= n_last, 0 <= n_first, n_first + n_last <= n_sel <= 1024: the newest block is
+ *   always taken, so the mean of a block that is not yet full is never compared (n_last
+ *   counts back from the token's own block). q as for dsa_gqa_attend. cache->k_mean must
+ *   be given; k, v and their scales are not read. max_seq_len <= 2,097,152.
+ *   ws: 256 bytes (the header).
+ */
+dsa_status_t dsa_block_select(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H, const void* q,
+                              int64_t q_stride, int32_t n_sel, int32_t n_first, int32_t n_last, int32_t* blocks,
+                              void* ws, size_t ws_bytes, void* stream);
+size_t dsa_block_select_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t n_sel);
+
+/*
+ * dsa_gqa_attend_blocks -- dsa_gqa_attend over listed blocks only: query token t's heads
+ *   of key head h see the keys s <= pos(t) of the blocks blocks[t, h, :].
+ *   blocks [T, Hkv, n_sel] int32 as dsa_block_select writes them: ascending, then -1;
+ *     1 <= n_sel <= 32768. An entry that does not follow a smaller one (or the start of
+ *     the list) is skipped and sets DSA_ERR_BAD_INDEX, -1 and blocks past the token's own
+ *     are skipped. A list without a visible block gives out = 0, lse = -inf.
+ */
+dsa_status_t dsa_gqa_attend_blocks(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H, const void* q,
+                                   int64_t q_stride, const int32_t* blocks, int32_t n_sel, float sm_scale, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, void* stream);
+size_t dsa_gqa_attend_blocks_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H,
+                                            int32_t n_sel);
+
 /* Synchronizes `stream`, reads the device error word of `ws` (DSA_OK if none)
  * and clears it. Returns DSA_ERR_CUDA if the stream itself reports an error. */
 dsa_status_t dsa_get_error(void* ws, void* stream);
