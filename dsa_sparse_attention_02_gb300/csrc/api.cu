@@ -59,6 +59,25 @@ bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ba
   return true;
 }
 
+bool encode_code_tiles(CUtensorMap* m, const void* base, int D, uint64_t tiles) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) { set_last_error("cudaGetDriverEntryPointByVersion", "cuTensorMapEncodeTiled unavailable"); return false; }
+  cuuint64_t dims[3] = {(cuuint64_t)D, 64, tiles};
+  cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * 64};
+  cuuint32_t box[3] = {(cuuint32_t)D, 64, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[96];
+    snprintf(buf, sizeof(buf), "CUresult %d (%llu tiles of 64 x %d)", (int)r, (unsigned long long)tiles, D);
+    set_last_error("cuTensorMapEncodeTiled", buf);
+    return false;
+  }
+  return true;
+}
+
 bool encode_mla_q_map(CUtensorMap* map_q, const void* q, int T, int H) {
   const uint32_t box_rows = H < 16 ? (uint32_t)H : 16u;
   return encode_tensor_map_2d(map_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, 576, (uint64_t)T * H, 1152, 64, box_rows);

@@ -68,6 +68,10 @@ dsa_status_t attend(const dsa_geom_t* g, const dsa_gqa_cache_t* c, int H, const 
   if (s == DSA_OK) s = check_cache(c);
   if (s != DSA_OK) return s;
   if (!heads_ok(c, H) || !std::isfinite(sm_scale) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
+  if ((int64_t)g->num_pages * c->Hkv > INT32_MAX) {
+    set_last_error("grouped-query attention", "num_pages * Hkv above 2^31 - 1");
+    return DSA_ERR_UNSUPPORTED;
+  }
   if (!ws_ok(ws, ws_bytes, attend_ws(g, c, H, n_sel))) return DSA_ERR_WORKSPACE;
   if (g->T == 0) return DSA_OK;
   if (!has_codes(c) || !rows_ok(q, q_stride, (int64_t)H * c->D) || !out || !aligned16(out) || (lse && !aligned4(lse)))

@@ -208,6 +208,9 @@ dsa_status_t check_attend(const dsa_geom_t* g, dsa_dtype_t dt, int H, const void
 dsa_status_t resolve_outputs(const dsa_geom_t* g, int H, void* out, float* lse, void** dout, float** dlse);
 bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t cols,
                           uint64_t rows, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows);
+// Codes [tiles, 64, D] bytes in boxes of one tile, with the swizzle of D-byte rows (64 or
+// 128): 16-byte chunk i of row r lies at chunk i ^ (r & 7) (128), i ^ ((r >> 1) & 3) (64).
+bool encode_code_tiles(CUtensorMap* m, const void* base, int D, uint64_t tiles);
 void set_last_error(const char* what, const char* detail);
 
 }  // namespace dsa

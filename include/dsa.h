@@ -378,7 +378,7 @@ size_t dsa_decode_step_bounded_workspace_size(const dsa_step_args_t* args, size_
  *     tokens, e.g. 0) sees no key and is not stored; this is not an error;
  *   - a request with seq_lens > max_seq_len, or with cu_q decreasing or above T, sets
  *     DSA_ERR_BAD_INDEX; its tokens are treated as at negative positions where they lie
- *     in [0, T), as are tokens below cu_q[0];
+ *     in [0, T);
  *   - a page id out of range sets DSA_ERR_BAD_INDEX; its tokens are not stored, and are
  *     seen by no query.
  */
@@ -436,7 +436,7 @@ size_t dsa_gqa_append_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache
  *     ln(sum_s exp(z_s)). A row that sees no key gives out = 0 and lse = -inf. What lies
  *     in a key or value that a row does not see (NaN codes, pages of other requests) does
  *     not reach it. out overlaps no input; out 16-byte aligned.
- *   sm_scale finite and >= 0.
+ *   sm_scale finite and >= 0. num_pages * Hkv < 2^31.
  */
 dsa_status_t dsa_gqa_attend(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H, const void* q,
                             int64_t q_stride, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,

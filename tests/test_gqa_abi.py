@@ -76,6 +76,7 @@ def test_attend_refusals(lib):
                dict(sm=float("inf")), dict(sm=-0.5), dict(out=None), dict(out=8), dict(lse=18)):
         assert call(**kw) == INV, kw
     assert call(wb=lib.dsa_gqa_attend_workspace_size(ref(geom()), ref(cache()), 8) - 1) == WSP
+    assert call(g=geom(num_pages=1 << 24), c=cache(Hkv=128), H=128) == UNS
 
 
 def test_attend_blocks_refusals(lib):
