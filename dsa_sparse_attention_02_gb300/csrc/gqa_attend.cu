@@ -10,12 +10,13 @@
 // leaves partial results that a second kernel merges. A producer warp brings units through
 // a ring of TMA stages; four warps compute straight from the codes:
 //
-//   * 16 query rows x 16 keys per warp and step on mma.sync m16n8k16 (f16, fp32 sums).
-//     tcgen05 would take its operands from shared memory or TMEM, i.e. a write and a second
-//     read of every key and value converted to 16 bits; here the codes go from shared
-//     memory to registers once, are converted there, and are fragments already. The order
-//     of the summation index is free, so a lane's fragments are D/4 consecutive bytes of a
-//     key, and a value pair's halves are put side by side by one byte permute.
+//   * 16 keys x 8 query rows per step on mma.sync m16n8k16 (f16, fp32 sums), the keys (and
+//     the values' columns) as the 16 rows of A, so that a group of up to 8 heads wastes
+//     nothing. tcgen05 would take its operands from shared memory or TMEM, i.e. a write and
+//     a second read of every key and value converted to 16 bits; here the codes go from
+//     shared memory to registers once, are converted there, and are fragments already. The
+//     order of the summation index is free, so a lane's fragments are D/4 consecutive bytes
+//     of a key, and a value pair's halves are put side by side by one byte permute.
 //   * both 8-bit types are exact in f16. Queries are scaled by a power of two per row (so
 //     that bf16's range fits f16) and are exact to 2^-38 of the row's largest value.
 //   * the block's key scale multiplies the scores. Its value scale enters the exponent: with
@@ -34,8 +35,6 @@ namespace {
 
 constexpr int kConsumers = 4;               // computing warps; one more brings the units
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kStages = 4;
-constexpr int kCtasPerSm = 2;
 constexpr float kNone = -3.0e38f;           // running maximum before the first key
 
 // What a unit's stage says to the computing warps.
@@ -82,11 +81,18 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
     lo = *reinterpret_cast<const uint32_t*>(&x);
     hi = *reinterpret_cast<const uint32_t*>(&y);
   } else {
-    const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-    const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    lo = (uint32_t)x.x | ((uint32_t)x.y << 16);
-    hi = (uint32_t)y.x | ((uint32_t)y.y << 16);
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
+}
+
+// An 8x8 matrix of 16-bit values, a row per four lanes and two values per lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -97,6 +103,22 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
+}
+
+// The A fragments of a slice's values, 16 columns at a time: take(tile, a0, a1, a2, a3).
+template <int D, bool I8, typename F>
+__device__ __forceinline__ void value_tiles(const uint32_t (&v)[4][D / 32], F take) {
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t sel = e ? 0x7362u : 0x5140u;
+      uint32_t a0, a1, a2, a3;
+      codes_f16<I8>(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
+      codes_f16<I8>(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
+      take(2 * w + e, a0, a1, a2, a3);
+    }
+  }
 }
 
 // Requests as the items see them: tokens [q0, q0 + n), items of `units` units each.
@@ -118,22 +140,26 @@ __device__ __forceinline__ Request request_of(const GqaAttendArgs& A, int b, int
   return r;
 }
 
-template <int D, bool I8, int MT>
+// A warp has NT tiles of 8 query rows; MT warps share a unit's keys, each with rows of its own.
+template <int D, int NT, int MT>
 struct Shape {
+  static constexpr int kRows = 8 * NT * MT;
   static constexpr int kTile = kPage * D;                        // bytes of a unit's keys (and of its values)
-  static constexpr int kAcc = D / 2;                             // fp32 sums per lane
+  static constexpr int kAcc = NT * D / 4;                        // fp32 sums per lane
   static constexpr int kGroups = kConsumers / MT;                // warps that share a row tile, each with its keys
   static constexpr int kMergeBufs = (kGroups - 1) * MT;
-  static constexpr int kMergeFloats = (kAcc + 4) * 32;
+  static constexpr int kMergeFloats = (kAcc + 4 * NT) * 32;
+  static constexpr int kCtas = NT == 1 ? 3 : 2;                  // per SM
+  static constexpr int kStages = NT == 1 ? 3 : 4;
   static constexpr size_t kSmem = (size_t)kStages * 2 * kTile + (size_t)kMergeBufs * kMergeFloats * 4 + 1024;
 };
 
-template <int D, bool I8, int MT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int D, bool I8, int NT, int MT>
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
     gqa_rows_kernel(const GqaAttendArgs A, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, float* o_part, float* ml_part, Cut* cuts) {
-  using S = Shape<D, I8, MT>;
-  constexpr int kRows = 16 * MT;
+  using S = Shape<D, NT, MT>;
+  constexpr int kRows = S::kRows, kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kStages], s_empty[kStages], s_meet;
   __shared__ Unit s_unit[kStages];
@@ -352,16 +378,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 
   // -------------------------------------------------------------- computing warps
-  constexpr int kSteps = D / 16;                 // k16 steps of a score
-  constexpr int kWords = D / 16;                 // words of a lane's D/4 key bytes
-  constexpr int kTiles = D / 8;                  // n8 tiles of the output
+  constexpr int kSteps = D / 16;                 // k16 steps of a score = words of a lane's D/4 key bytes
+  constexpr int kTiles = D / 16;                 // 16-column tiles of the output
+  constexpr int kVw = D / 32;                    // words of a lane's D/8 bytes of a value
   const int m = warp % MT, group = warp / MT;
   const int q = lane & 3, lrow = lane >> 2;
   const int G = A.G, H = A.G * A.c.Hkv;
-  uint32_t qf[kSteps][4];
-  float o[kTiles][4];
-  float M[2], l[2], rowf[2];
-  int tok[2];                                    // token of the lane's two rows, or far below any limit
+  uint32_t qf[NT][kSteps][2];
+  float o[NT][kTiles][4];                        // [.][j]: columns lrow*D/8 + 2j (0, 1) and + 1 (2, 3) of rows 2q, 2q+1
+  float M[NT][2], l[NT][2], rowf[NT][2];         // of rows 8i + 2q and + 1
+  int tok[NT][2];                                // their tokens, or far below any limit
   int tok_lo = 0, tok_hi = 0;                    // of the warp's rows (tok_hi < 0: none)
   int stage = 0;
   uint32_t phase = 0, met = 0;
@@ -378,39 +404,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (!mbar_wait(smem_u32(&s_full[stage]), phase, abort, A.err)) break;
     const Unit x = s_unit[stage];
     if (x.flags & kFirst) {
-      const int r0 = x.row0 + m * 16, rows = x.n * G;
+      const int r0 = x.row0 + m * 8 * NT, rows = x.n * G;
       tok_lo = r0 / G;
-      tok_hi = r0 < rows ? min(x.n - 1, (r0 + 15) / G) : -1;
+      tok_hi = r0 < rows ? min(x.n - 1, (r0 + 8 * NT - 1) / G) : -1;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int row = r0 + lrow + 8 * s;
+      for (int i = 0; i < NT; ++i) {
+        const int row = r0 + 8 * i + lrow;
         const bool valid = row < rows;
         const int t = valid ? row / G : 0;
-        tok[s] = valid ? t : -(1 << 30);
-        M[s] = kNone;
-        l[s] = 0.f;
         const uint4* src = reinterpret_cast<const uint4*>(
             A.q + (int64_t)(x.q0 + t) * A.q_stride + (int64_t)(x.h * G + (valid ? row - t * G : 0)) * D + q * (D / 4));
         uint32_t w[D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 v = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        for (int k = 0; k < D / 32; ++k) {
+          const uint4 v = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+          w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
         }
         float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+        for (int k = 0; k < D / 8; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
         // the row times 2^(14 - e), e the exponent of its largest value (none for infinities)
         const int e = min(max((int)(__float_as_uint(big) >> 23), 15), 254);
         const float up = __uint_as_float((uint32_t)(268 - e) << 23);
-        rowf[s] = __uint_as_float((uint32_t)(e - 14) << 23);
+        const float down = __uint_as_float((uint32_t)(e - 14) << 23);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) qf[i >> 1][(i & 1) * 2 + s] = pack_f16(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+        for (int k = 0; k < D / 8; ++k) qf[i][k >> 1][k & 1] = pack_f16(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int mine = r0 + 8 * i + 2 * q + h;
+          rowf[i][h] = __shfl_sync(0xffffffffu, down, 4 * (2 * q + h));
+          tok[i][h] = mine < rows ? mine / G : -(1 << 30);
+          M[i][h] = kNone;
+          l[i][h] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     }
     const uint32_t kt = smem_u32(smem + stage * 2 * S::kTile), vt = kt + S::kTile;
     const int seen = (x.flags & kVoid) ? -1 : min(x.rel + tok_hi, kPage - 1);   // last key any row of the warp sees
@@ -419,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int sub = 0; sub < MT; ++sub) {
       const int ts = (group * MT + sub) * 16;
       if (tok_hi < 0 || ts > seen) break;
-      // ---- scores
-      float s[2][4] = {};
+      // ---- scores: s[i][0..3] are key lrow (0, 1) and lrow + 8 (2, 3) with rows 2q, 2q+1
+      float s[NT][4] = {};
       {
-        uint32_t kw[2][kWords];
+        uint32_t kw[2][kSteps];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t row = kt + (ts + 8 * j + lrow) * D;
@@ -436,105 +467,103 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
         }
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i)
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a0, a1, a2, a3;
+          codes_f16<I8>(kw[0][k], a0, a2);
+          codes_f16<I8>(kw[1][k], a1, a3);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t b0, b1;
-            codes_f16<I8>(kw[j][i], b0, b1);
-            mma16816(s[j], qf[i][0], qf[i][1], qf[i][2], qf[i][3], b0, b1);
-          }
+          for (int i = 0; i < NT; ++i) mma16816(s[i], a0, a1, a2, a3, qf[i][k][0], qf[i][k][1]);
+        }
       }
-      // ---- values (read early: their latency passes under the softmax). vw[i]: token
-      // 2q + (i & 1) + 8 * (i >> 1) of the slice, D/8 bytes from column (D/8) * lrow
-      uint32_t vw[4][D / 32];
+      // ---- values (read early: their latency passes under the softmax). vw[k]: token
+      // 2q + (k & 1) + 8 * (k >> 1) of the slice, D/8 bytes from column (D/8) * lrow
+      uint32_t vw[4][kVw];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tk = ts + 2 * q + (i & 1) + 8 * (i >> 1);
+      for (int k = 0; k < 4; ++k) {
+        const int tk = ts + 2 * q + (k & 1) + 8 * (k >> 1);
         if constexpr (D == 128) {
           const uint4 a = lds128(vt + tk * D + ((lrow ^ (tk & 7)) << 4));
-          vw[i][0] = a.x, vw[i][1] = a.y, vw[i][2] = a.z, vw[i][3] = a.w;
+          vw[k][0] = a.x, vw[k][1] = a.y, vw[k][2] = a.z, vw[k][3] = a.w;
         } else {
           const uint2 a = lds64(vt + tk * D + (((lrow >> 1) ^ ((tk >> 1) & 3)) << 4) + (lrow & 1) * 8);
-          vw[i][0] = a.x, vw[i][1] = a.y;
+          vw[k][0] = a.x, vw[k][1] = a.y;
         }
       }
       // ---- softmax
-      float p[2][4];                              // [row half][token 2q, 2q+1, 2q+8, 2q+9]
       bool grew = false;
-      float keep[2];
+      float keep[NT][2];
+      uint32_t pb[NT][2];                         // weights, f16: rows by lane group, keys 2q, 2q+1 (0) and + 8 (1)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float f = x.kf * rowf[h];
-        p[h][0] = s[0][2 * h] * f, p[h][1] = s[0][2 * h + 1] * f;
-        p[h][2] = s[1][2 * h] * f, p[h][3] = s[1][2 * h + 1] * f;
-        if (!whole) {
-          const int lim = x.rel + tok[h] - ts;
+      for (int i = 0; i < NT; ++i) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (2 * q + (i & 1) + 8 * (i >> 1) > lim) p[h][i] = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+          const float f = x.kf * rowf[i][h];
+          float z0 = s[i][h] * f, z1 = s[i][2 + h] * f;
+          if (!whole) {
+            const int lim = x.rel + tok[i][h] - ts;
+            if (lrow > lim) z0 = -INFINITY;
+            if (lrow + 8 > lim) z1 = -INFINITY;
+          }
+          float mx = fmaxf(z0, z1);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float Mn = fmaxf(M[i][h], mx + x.lv);
+          grew |= Mn > M[i][h];
+          keep[i][h] = ex2(M[i][h] - Mn);
+          M[i][h] = Mn;
+          const float ref = Mn - x.lv;
+          z0 = ex2(z0 - ref);
+          z1 = ex2(z1 - ref);
+          l[i][h] = l[i][h] * keep[i][h] + (z0 + z1) * x.ivs;
+          s[i][h] = z0, s[i][2 + h] = z1;
         }
-        float mx = fmaxf(fmaxf(p[h][0], p[h][1]), fmaxf(p[h][2], p[h][3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float Mn = fmaxf(M[h], mx + x.lv);
-        grew |= Mn > M[h];
-        keep[h] = ex2(M[h] - Mn);
-        M[h] = Mn;
-        const float ref = Mn - x.lv;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[h][i] = ex2(p[h][i] - ref);
-        l[h] = l[h] * keep[h] + ((p[h][0] + p[h][1]) + (p[h][2] + p[h][3])) * x.ivs;
+        pb[i][0] = transpose8(pack_f16(s[i][0], s[i][1]));
+        pb[i][1] = transpose8(pack_f16(s[i][2], s[i][3]));
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) o[j][0] *= keep[0], o[j][1] *= keep[0], o[j][2] *= keep[1], o[j][3] *= keep[1];
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+            o[i][j][0] *= keep[i][0], o[i][j][1] *= keep[i][1], o[i][j][2] *= keep[i][0], o[i][j][3] *= keep[i][1];
       }
       // ---- values times weights
-      const uint32_t a0 = pack_f16(p[0][0], p[0][1]), a1 = pack_f16(p[1][0], p[1][1]);
-      const uint32_t a2 = pack_f16(p[0][2], p[0][3]), a3 = pack_f16(p[1][2], p[1][3]);
       bool apart = false;                         // a NaN value that only some rows may meet
       if (!whole) {
         bool nan = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool out = ts + 2 * q + (i & 1) + 8 * (i >> 1) > seen;
+        for (int k = 0; k < 4; ++k) {
+          const bool out = ts + 2 * q + (k & 1) + 8 * (k >> 1) > seen;
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            if (out) vw[i][w] = 0u;
-            if (!I8) nan |= __vcmpeq4(vw[i][w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+          for (int w = 0; w < kVw; ++w) {
+            if (out) vw[k][w] = 0u;
+            if (!I8) nan |= __vcmpeq4(vw[k][w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
           }
         }
         apart = !I8 && __any_sync(0xffffffffu, nan);
       }
-      auto product = [&](const uint32_t (&v)[4][D / 32], auto&& take) {
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t sel = e ? 0x7362u : 0x5140u;
-            uint32_t x0, x1, y0, y1;
-            codes_f16<I8>(__byte_perm(v[0][w], v[1][w], sel), x0, x1);
-            codes_f16<I8>(__byte_perm(v[2][w], v[3][w], sel), y0, y1);
-            take(4 * w + 2 * e, x0, y0);
-            take(4 * w + 2 * e + 1, x1, y1);
-          }
-        }
-      };
       if (!apart) {
-        product(vw, [&](int j, uint32_t b0, uint32_t b1) { mma16816(o[j], a0, a1, a2, a3, b0, b1); });
+        value_tiles<D, I8>(vw, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) mma16816(o[i][j], a0, a1, a2, a3, pb[i][0], pb[i][1]);
+        });
       } else {
         for (int t = tok_lo; t <= tok_hi; ++t) {
-          uint32_t v[4][D / 32];
+          uint32_t v[4][kVw];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w)
-              v[i][w] = ts + 2 * q + (i & 1) + 8 * (i >> 1) > x.rel + t ? 0u : vw[i][w];
-          product(v, [&](int j, uint32_t b0, uint32_t b1) {
-            float c[4] = {o[j][0], o[j][1], o[j][2], o[j][3]};
-            mma16816(c, a0, a1, a2, a3, b0, b1);
-            if (tok[0] == t) o[j][0] = c[0], o[j][1] = c[1];
-            if (tok[1] == t) o[j][2] = c[2], o[j][3] = c[3];
+            for (int w = 0; w < kVw; ++w)
+              v[k][w] = ts + 2 * q + (k & 1) + 8 * (k >> 1) > x.rel + t ? 0u : vw[k][w];
+          value_tiles<D, I8>(v, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              float c[4] = {o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]};
+              mma16816(c, a0, a1, a2, a3, pb[i][0], pb[i][1]);
+              if (tok[i][0] == t) o[i][j][0] = c[0], o[i][j][2] = c[2];
+              if (tok[i][1] == t) o[i][j][1] = c[1], o[i][j][3] = c[3];
+            }
           });
         }
       }
@@ -546,74 +575,81 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     // ---- end of the run's part of the item: the sums of the warps that shared its rows
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    }
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 4);
+        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 8);
+        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 16);
+      }
     if (S::kGroups > 1) {
       if (!meet()) break;                         // the last merge has been read
       if (group > 0) {
         float* buf = merge + ((group - 1) * MT + m) * S::kMergeFloats + lane;
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
+        for (int i = 0; i < NT; ++i) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) buf[(4 * j + i) * 32] = o[j][i];
-        buf[S::kAcc * 32] = M[0], buf[(S::kAcc + 1) * 32] = M[1];
-        buf[(S::kAcc + 2) * 32] = l[0], buf[(S::kAcc + 3) * 32] = l[1];
+          for (int j = 0; j < 4 * kTiles; ++j) buf[(i * 4 * kTiles + j) * 32] = o[i][j >> 2][j & 3];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            buf[(S::kAcc + 4 * i + h) * 32] = M[i][h];
+            buf[(S::kAcc + 4 * i + 2 + h) * 32] = l[i][h];
+          }
+        }
       }
       if (!meet()) break;
       if (group > 0) continue;
 #pragma unroll 1
       for (int gr = 1; gr < S::kGroups; ++gr) {
         const float* buf = merge + ((gr - 1) * MT + m) * S::kMergeFloats + lane;
-        float mine[2], other[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float Mo = buf[(S::kAcc + h) * 32], Mn = fmaxf(M[h], Mo);
-          mine[h] = ex2(M[h] - Mn);
-          other[h] = ex2(Mo - Mn);
-          l[h] = l[h] * mine[h] + buf[(S::kAcc + 2 + h) * 32] * other[h];
-          M[h] = Mn;
+        for (int i = 0; i < NT; ++i) {
+          float mine[2], other[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float Mo = buf[(S::kAcc + 4 * i + h) * 32], Mn = fmaxf(M[i][h], Mo);
+            mine[h] = ex2(M[i][h] - Mn);
+            other[h] = ex2(Mo - Mn);
+            l[i][h] = l[i][h] * mine[h] + buf[(S::kAcc + 4 * i + 2 + h) * 32] * other[h];
+            M[i][h] = Mn;
+          }
+#pragma unroll
+          for (int j = 0; j < 4 * kTiles; ++j)
+            o[i][j >> 2][j & 3] = o[i][j >> 2][j & 3] * mine[j & 1] + buf[(i * 4 * kTiles + j) * 32] * other[j & 1];
         }
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] = o[j][i] * mine[i >> 1] + buf[(4 * j + i) * 32] * other[i >> 1];
       }
     }
-    // a lane holds columns q*D/4 .. of its rows: first half in o[.][0], second in o[.][1]
+    // a lane holds columns lrow*D/8 .. of its rows
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (tok[h] < 0) continue;
-      const int row = x.row0 + m * 16 + lrow + 8 * h, head = x.h * G + row % G;
-      if (x.slot < 0) {
-        const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
-        const int64_t at = (int64_t)(x.q0 + tok[h]) * H + head;
-        uint4* dst = reinterpret_cast<uint4*>(A.out + at * D + q * (D / 4));
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+      for (int h = 0; h < 2; ++h) {
+        if (tok[i][h] < 0) continue;
+        const int r = m * 8 * NT + 8 * i + 2 * q + h;                 // row of the item's tile
+        auto col = [&](int d) { return o[i][d >> 1][2 * (d & 1) + h]; };
+        if (x.slot < 0) {
+          const float inv = l[i][h] == 0.f ? 0.f : 1.f / l[i][h];
+          const int64_t at = (int64_t)(x.q0 + tok[i][h]) * H + x.h * G + (x.row0 + r - tok[i][h] * G);
+          uint4* dst = reinterpret_cast<uint4*>(A.out + at * D + lrow * (D / 8));
 #pragma unroll
-          for (int j = 0; j < kTiles; j += 8) {
+          for (int d = 0; d < D / 8; d += 8) {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(o[j + 2 * i][2 * h + e] * inv, o[j + 2 * i + 1][2 * h + e] * inv);
-              w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(col(d + 2 * k) * inv, col(d + 2 * k + 1) * inv);
+              w[k] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            dst[e * (kTiles / 8) + j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[d / 8] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        if (A.lse && q == 0) A.lse[at] = l[h] == 0.f ? -INFINITY : (M[h] + log2f(l[h])) * 0.6931471805599453f;
-      } else {
-        const int64_t at = (int64_t)x.slot * kRows + m * 16 + lrow + 8 * h;
-        float4* dst = reinterpret_cast<float4*>(o_part + at * D + q * (D / 4));
+          if (A.lse && lrow == 0) A.lse[at] = l[i][h] == 0.f ? -INFINITY : (M[i][h] + log2f(l[i][h])) * 0.6931471805599453f;
+        } else {
+          const int64_t at = (int64_t)x.slot * kRows + r;
+          float4* dst = reinterpret_cast<float4*>(o_part + at * D + lrow * (D / 8));
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int j = 0; j < kTiles; j += 4)
-            dst[e * (kTiles / 4) + j / 4] = make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e], o[j + 3][2 * h + e]);
-        if (q == 0) *reinterpret_cast<float2*>(ml_part + at * 2) = make_float2(M[h], l[h]);
+          for (int d = 0; d < D / 8; d += 4) dst[d / 4] = make_float4(col(d), col(d + 1), col(d + 2), col(d + 3));
+          if (lrow == 0) *reinterpret_cast<float2*>(ml_part + at * 2) = make_float2(M[i][h], l[i][h]);
+        }
       }
-    }
   }
 }
 
@@ -686,27 +722,28 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
-// Row tiles of 16 query rows (tokens x heads of a key head) per warp; a request with more
-// rows has its keys converted once for up to four such tiles.
-int row_tiles(int T, int B, int G, bool listed) {
-  if (listed) return 1;
-  const int64_t rows = ((int64_t)T + B - 1) / B * G;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+// Query rows (tokens x heads of a key head) that meet a unit together. Up to 16 rows: every
+// warp has them all and a quarter of the keys. More: a unit's codes are converted by two or
+// four warps, each for 16 of the rows.
+int rows_per_item(int T, int B, int G, bool listed) {
+  const int64_t rows = listed ? G : ((int64_t)T + B - 1) / B * G;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-int rows_grid(int num_sms) { return kCtasPerSm * num_sms; }
+int rows_grid(int rows, int num_sms) { return (rows == 8 ? Shape<128, 1, 1>::kCtas : Shape<128, 2, 1>::kCtas) * num_sms; }
 
-template <int D, bool I8, int MT>
+template <int D, bool I8, int NT, int MT>
 cudaError_t launch(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
-  using S = Shape<D, I8, MT>;
-  const int grid = rows_grid(num_sms), rows = 16 * MT;
+  using S = Shape<D, NT, MT>;
+  constexpr int rows = S::kRows;
+  const int grid = rows_grid(rows, num_sms);
   uint8_t* p = reinterpret_cast<uint8_t*>(A.scratch);
   Cut* cuts = reinterpret_cast<Cut*>(p);
   p += align_up(sizeof(Cut) * grid, 256);
   float* ml = reinterpret_cast<float*>(p);
   p += align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256);
   float* o = reinterpret_cast<float*>(p);
-  auto kern = gqa_rows_kernel<D, I8, MT>;
+  auto kern = gqa_rows_kernel<D, I8, NT, MT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, S::kSmem, st>>>(A, mk, mv, o, ml, cuts);
@@ -725,18 +762,19 @@ cudaError_t launch(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensor
 }
 
 template <int D, bool I8>
-cudaError_t launch_mt(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
-  switch (row_tiles(A.g.T, A.g.B, A.G, A.blocks != nullptr)) {
-    case 1: return launch<D, I8, 1>(A, mk, mv, num_sms, st);
-    case 2: return launch<D, I8, 2>(A, mk, mv, num_sms, st);
-    default: return launch<D, I8, 4>(A, mk, mv, num_sms, st);
+cudaError_t launch_rows(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
+  switch (rows_per_item(A.g.T, A.g.B, A.G, A.blocks != nullptr)) {
+    case 8: return launch<D, I8, 1, 1>(A, mk, mv, num_sms, st);
+    case 16: return launch<D, I8, 2, 1>(A, mk, mv, num_sms, st);
+    case 32: return launch<D, I8, 2, 2>(A, mk, mv, num_sms, st);
+    default: return launch<D, I8, 2, 4>(A, mk, mv, num_sms, st);
   }
 }
 
 }  // namespace
 
 size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int, int D, int G, int n_sel, int num_sms) {
-  const int grid = rows_grid(num_sms), rows = 16 * row_tiles(g->T, g->B, G, n_sel > 0);
+  const int rows = rows_per_item(g->T, g->B, G, n_sel > 0), grid = rows_grid(rows, num_sms);
   return align_up(sizeof(Cut) * grid, 256) + align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256) +
          (size_t)2 * grid * rows * D * sizeof(float);
 }
@@ -746,8 +784,8 @@ cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t 
   const uint64_t tiles = (uint64_t)A.g.num_pages * A.c.Hkv;
   if (!encode_code_tiles(&mk, A.c.k, A.c.D, tiles) || !encode_code_tiles(&mv, A.c.v, A.c.D, tiles))
     return cudaErrorInvalidValue;
-  if (A.c.D == 128) return A.c.i8 ? launch_mt<128, true>(A, mk, mv, num_sms, st) : launch_mt<128, false>(A, mk, mv, num_sms, st);
-  return A.c.i8 ? launch_mt<64, true>(A, mk, mv, num_sms, st) : launch_mt<64, false>(A, mk, mv, num_sms, st);
+  if (A.c.D == 128) return A.c.i8 ? launch_rows<128, true>(A, mk, mv, num_sms, st) : launch_rows<128, false>(A, mk, mv, num_sms, st);
+  return A.c.i8 ? launch_rows<64, true>(A, mk, mv, num_sms, st) : launch_rows<64, false>(A, mk, mv, num_sms, st);
 }
 
 }  // namespace dsa
