@@ -35,59 +35,14 @@ namespace {
 
 constexpr int kConsumers = 4;               // computing warps; one more brings the units
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr float kNone = -3.0e38f;           // running maximum before the first key
 
-// What a unit's stage says to the computing warps.
-struct __align__(16) Unit {
-  float kf;       // k_scale * sm_scale * log2(e)
-  float lv, ivs;  // log2(v_scale), 1 / v_scale
-  int flags;
-  int q0, n;      // the request's first token and its number of tokens (listed blocks: the token, 1)
-  int row0, h;    // first row of the tile (row r: token r / G, head r % G of key head h)
-  int rel;        // position of token 0, less the block's first position
-  int slot;       // partial slot, or -1: the item ends in its outputs
-  int pad[2];
-};
-enum : int { kFirst = 1, kLast = 2, kVoid = 4 };   // first / last unit of the run's part of an item; nothing to see
 
-// Merge order of an item that was cut: block of threads c holds its first part in `slot`,
-// the next `follow` ones each a part in their slot 0.
-struct __align__(16) Cut { int follow, slot, q0, n, row0, h, pad[2]; };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// f16 pairs of a word's four codes: (byte 0, byte 1) and (byte 2, byte 3).
-template <bool I8>
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (I8) {
-    // 0x64xx is 1024 + xx in f16; with the sign bit flipped xx is code + 128
-    const uint32_t u = w ^ 0x80808080u, bias = 0x64806480u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&bias));
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
-}
-
 // An 8x8 matrix of 16-bit values, a row per four lanes and two values per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
@@ -157,7 +112,7 @@ struct Shape {
 template <int D, bool I8, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
     gqa_rows_kernel(const GqaAttendArgs A, const __grid_constant__ CUtensorMap map_k,
-                    const __grid_constant__ CUtensorMap map_v, float* o_part, float* ml_part, Cut* cuts) {
+                    const __grid_constant__ CUtensorMap map_v, const GqaParts parts) {
   using S = Shape<D, NT, MT>;
   constexpr int kRows = S::kRows, kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -179,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
     s_abort = 0;
     mbar_init(smem_u32(&s_meet), kConsumers);
     fence_mbar_init();
-    cuts[blockIdx.x].follow = 0;
+    parts.cuts[blockIdx.x].follow = 0;
   }
   // This block's run [s_begin, s_end) of all units. Whole contexts: the request it starts in
   // and where that request's units begin.
@@ -339,11 +294,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
           k.follow = (int)split_owner(item_end - 1, total, grid) - (int)blockIdx.x;
           k.slot = x.slot;
           k.q0 = x.q0, k.n = x.n, k.row0 = x.row0, k.h = x.h;
-          cuts[blockIdx.x] = k;
+          parts.cuts[blockIdx.x] = k;
         }
       }
       for (int i = 0; i < cnt; ++i) {
-        ok = mbar_wait(smem_u32(&s_empty[stage]), phase ^ 1u, abort, A.err);
+        ok = warp_wait(&s_empty[stage], phase ^ 1u, abort, A.err);
         if (!ok) break;
         if (lane == i) {
           s_unit[stage] = x;
@@ -395,13 +350,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
   auto meet = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s_meet));
-    const bool all = mbar_wait(smem_u32(&s_meet), met, abort, A.err);
+    const bool all = warp_wait(&s_meet, met, abort, A.err);
     met ^= 1u;
     return all;
   };
 
   for (int64_t u = begin; u < end; ++u) {
-    if (!mbar_wait(smem_u32(&s_full[stage]), phase, abort, A.err)) break;
+    if (!warp_wait(&s_full[stage], phase, abort, A.err)) break;
     const Unit x = s_unit[stage];
     if (x.flags & kFirst) {
       const int r0 = x.row0 + m * 8 * NT, rows = x.n * G;
@@ -644,10 +599,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
           if (A.lse && lrow == 0) A.lse[at] = l[i][h] == 0.f ? -INFINITY : (M[i][h] + log2f(l[i][h])) * 0.6931471805599453f;
         } else {
           const int64_t at = (int64_t)x.slot * kRows + r;
-          float4* dst = reinterpret_cast<float4*>(o_part + at * D + lrow * (D / 8));
+          float4* dst = reinterpret_cast<float4*>(parts.o + at * D + lrow * (D / 8));
 #pragma unroll
           for (int d = 0; d < D / 8; d += 4) dst[d / 4] = make_float4(col(d), col(d + 1), col(d + 2), col(d + 3));
-          if (lrow == 0) *reinterpret_cast<float2*>(ml_part + at * 2) = make_float2(M[i][h], l[i][h]);
+          if (lrow == 0) *reinterpret_cast<float2*>(parts.ml + at * 2) = make_float2(M[i][h], l[i][h]);
         }
       }
   }
@@ -660,15 +615,15 @@ constexpr int kMergeWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-    gqa_merge_kernel(const GqaAttendArgs A, int rows, const float* o_part, const float* ml_part, const Cut* cuts) {
+    gqa_merge_kernel(const GqaAttendArgs A, const GqaParts s) {
   constexpr int V = D / 32;
   __shared__ float s_o[kMergeWarps][D];
   __shared__ float s_ml[kMergeWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
-  const Cut k = cuts[blockIdx.x];
+  const Cut k = s.cuts[blockIdx.x];
   if (k.follow <= 0) return;
-  const int parts = k.follow + 1, H = A.G * A.c.Hkv;
+  const int rows = s.rows, parts = k.follow + 1, H = A.G * A.c.Hkv;
   const bool many = parts > 2 * kMergeWarps;
   const int first = many ? warp : 0, step = many ? kMergeWarps : 1;
   for (int i = many ? 0 : warp; i < kMergeWarps; i += many ? 1 : kMergeWarps) {
@@ -678,13 +633,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     for (int p = first; p < parts; p += step) {
       const int64_t slot = p == 0 ? k.slot : 2 * (int64_t)(blockIdx.x + p);
       const int64_t at = slot * rows + r;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(ml_part + at * 2));
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(s.ml + at * 2));
       float v[V];
       if constexpr (V == 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(o_part + at * D) + lane);
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(s.o + at * D) + lane);
         v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
       } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(o_part + at * D) + lane);
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(s.o + at * D) + lane);
         v[0] = f.x, v[1] = f.y;
       }
       const float Mn = fmaxf(M, ml.x), a = ex2(M - Mn), b = ex2(ml.x - Mn);
@@ -724,10 +679,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 
 // Query rows (tokens x heads of a key head) that meet a unit together. Up to 16 rows: every
 // warp has them all and a quarter of the keys. More: a unit's codes are converted by two or
-// four warps, each for 16 of the rows.
+// four warps, each for 16 of the rows. Above 64: gqa_tiles.cu.
 int rows_per_item(int T, int B, int G, bool listed) {
   const int64_t rows = listed ? G : ((int64_t)T + B - 1) / B * G;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kGqaTileRows;
 }
 
 int rows_grid(int rows, int num_sms) { return (rows == 8 ? Shape<128, 1, 1>::kCtas : Shape<128, 2, 1>::kCtas) * num_sms; }
@@ -737,28 +692,14 @@ cudaError_t launch(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensor
   using S = Shape<D, NT, MT>;
   constexpr int rows = S::kRows;
   const int grid = rows_grid(rows, num_sms);
-  uint8_t* p = reinterpret_cast<uint8_t*>(A.scratch);
-  Cut* cuts = reinterpret_cast<Cut*>(p);
-  p += align_up(sizeof(Cut) * grid, 256);
-  float* ml = reinterpret_cast<float*>(p);
-  p += align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256);
-  float* o = reinterpret_cast<float*>(p);
+  const GqaParts s = gqa_parts(A.scratch, grid, rows);
   auto kern = gqa_rows_kernel<D, I8, NT, MT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, S::kSmem, st>>>(A, mk, mv, o, ml, cuts);
+  kern<<<grid, kThreads, S::kSmem, st>>>(A, mk, mv, s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, rows / kMergeWarps);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gqa_merge_kernel<D>, A, rows, (const float*)o, (const float*)ml, (const Cut*)cuts);
+  return gqa_merge_launch(A, s, grid, st);
 }
 
 template <int D, bool I8>
@@ -773,13 +714,26 @@ cudaError_t launch_rows(const GqaAttendArgs& A, const CUtensorMap& mk, const CUt
 
 }  // namespace
 
+cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, s.rows / kMergeWarps);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return A.c.D == 128 ? cudaLaunchKernelEx(&cfg, gqa_merge_kernel<128>, A, s) : cudaLaunchKernelEx(&cfg, gqa_merge_kernel<64>, A, s);
+}
+
 size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int, int D, int G, int n_sel, int num_sms) {
-  const int rows = rows_per_item(g->T, g->B, G, n_sel > 0), grid = rows_grid(rows, num_sms);
-  return align_up(sizeof(Cut) * grid, 256) + align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256) +
-         (size_t)2 * grid * rows * D * sizeof(float);
+  const int rows = rows_per_item(g->T, g->B, G, n_sel > 0);
+  return rows > 64 ? gqa_parts_bytes(num_sms, kGqaTileRows, D) : gqa_parts_bytes(rows_grid(rows, num_sms), rows, D);
 }
 
 cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st) {
+  if (rows_per_item(A.g.T, A.g.B, A.G, A.blocks != nullptr) > 64) return gqa_tiles_launch(A, num_sms, st);
   CUtensorMap mk, mv;
   const uint64_t tiles = (uint64_t)A.g.num_pages * A.c.Hkv;
   if (!encode_code_tiles(&mk, A.c.k, A.c.D, tiles) || !encode_code_tiles(&mv, A.c.v, A.c.D, tiles))

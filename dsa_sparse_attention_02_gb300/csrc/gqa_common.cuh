@@ -43,4 +43,85 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// ---- attention: runs of units (gqa_attend.cu, gqa_tiles.cu)
+constexpr float kNone = -3.0e38f;           // running maximum before the first key
+
+// What a unit's stage says to the computing warps.
+struct __align__(16) Unit {
+  float kf;       // k_scale * sm_scale * log2(e)
+  float lv, ivs;  // log2(v_scale), 1 / v_scale
+  int flags;
+  int q0, n;      // the request's first token and its number of tokens (listed blocks: the token, 1)
+  int row0, h;    // first row of the tile (row r: token r / G, head r % G of key head h)
+  int rel;        // position of token 0, less the block's first position
+  int slot;       // partial slot, or -1: the item ends in its outputs
+  int c;          // the block's number in the request
+  int pad;
+};
+enum : int { kFirst = 1, kLast = 2, kVoid = 4 };   // first / last unit of the run's part of an item; nothing to see
+
+// Merge order of an item that was cut: block of threads c holds its first part in `slot`,
+// the next `follow` ones each a part in their slot 0.
+struct __align__(16) Cut { int follow, slot, q0, n, row0, h, pad[2]; };
+
+// A bounded wait by a whole warp: all lanes go on, or all give up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort, err));
+}
+
+// Partial results of cut items, in the workspace: two slots a block of threads, `rows` rows each.
+struct GqaParts {
+  int rows;
+  Cut* cuts;      // one per block of threads
+  float* ml;      // [2 * grid, rows, 2] running maximum (log2 units) and sum
+  float* o;       // [2 * grid, rows, D]
+};
+inline size_t gqa_parts_bytes(int grid, int rows, int D) {
+  return align_up(sizeof(Cut) * grid, 256) + align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256) +
+         (size_t)2 * grid * rows * D * sizeof(float);
+}
+inline GqaParts gqa_parts(void* scratch, int grid, int rows) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(scratch);
+  GqaParts s;
+  s.rows = rows;
+  s.cuts = reinterpret_cast<Cut*>(p);
+  p += align_up(sizeof(Cut) * grid, 256);
+  s.ml = reinterpret_cast<float*>(p);
+  s.o = reinterpret_cast<float*>(p + align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256));
+  return s;
+}
+cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int grid, cudaStream_t st);
+
+// Rows of an item in the kernel for many query rows (gqa_tiles.cu).
+constexpr int kGqaTileRows = 256;
+cudaError_t gqa_tiles_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st);
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// f16 pairs of a word's four codes: (byte 0, byte 1) and (byte 2, byte 3).
+template <bool I8>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (I8) {
+    // 0x64xx is 1024 + xx in f16; with the sign bit flipped xx is code + 128
+    const uint32_t u = w ^ 0x80808080u, bias = 0x64806480u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&bias));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
 }  // namespace dsa

@@ -228,7 +228,7 @@ def test_attend(lens, new, H, Hkv, D, dtype):
     check_attend(Dev(c), D ** -0.5)
 
 
-@pytest.mark.parametrize("new", [1, 4, 40])
+@pytest.mark.parametrize("new", [1, 4, 40, 200])
 def test_attend_empty_rows_and_padding(new):
     """Requests of length 0 (with a token, as padded batches have), of fewer keys than new
     tokens, and without new tokens."""
