@@ -64,9 +64,15 @@ enum : int { kFirst = 1, kLast = 2, kVoid = 4 };   // first / last unit of the r
 // the next `follow` ones each a part in their slot 0.
 struct __align__(16) Cut { int follow, slot, q0, n, row0, h, pad[2]; };
 
-// A bounded wait by a whole warp: all lanes go on, or all give up.
+// A bounded wait by a whole warp: all lanes go on, or all give up. The waiting loop stays
+// out of line: the roles of a block together outgrow the instruction caches, and a phase
+// that is already complete should cost a few instructions.
+static __device__ __noinline__ bool warp_wait_loop(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort, err));
+  const uint32_t a = smem_u32(bar);
+  return __all_sync(0xffffffffu, mbar_try_wait(a, parity)) || warp_wait_loop(a, parity, abort, err);
 }
 
 // Partial results of cut items, in the workspace: two slots a block of threads, `rows` rows each.

@@ -106,7 +106,7 @@ template <int D, bool I8>
 __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendArgs A, const GqaParts parts) {
   using S = TileShape<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_kfull[kStages], s_vfull[kStages], s_empty[kStages];
+  __shared__ uint64_t s_full[kStages], s_empty[kStages];
   __shared__ uint64_t s_sfull[2], s_pfull[2], s_odone[2], s_qfull[2], s_drain;
   __shared__ Unit s_unit[kStages];
   __shared__ int s_nan[I8 ? 1 : kNanSlots][D];
@@ -119,8 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
 
   if (tid == 32 * kMmaWarp) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&s_kfull[i]), kConvWarps);
-      mbar_init(smem_u32(&s_vfull[i]), kConvWarps);
+      mbar_init(smem_u32(&s_full[i]), kConvWarps);
       mbar_init(smem_u32(&s_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -327,9 +326,6 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       uint8_t* kd = smem + (size_t)stage * 2 * S::kOperand;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) put(kd, i, kr[i]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s_kfull[stage]));
       if (n + 1 < count) {
         if (++at == cnt) batch(begin + n + 1);
         t_next = __shfl_sync(0xffffffffu, page_tile, at);
@@ -358,68 +354,86 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       for (int i = 0; i < kLoads; ++i) put(kd + S::kOperand, i, vr[i]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s_vfull[stage]));
+      if (lane == 0) mbar_arrive(smem_u32(&s_full[stage]));
       if (n + 1 < count) fetch(A.c.v, t_next, vr);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = make_idesc(128, kPage, kFmtF16, kFmtF16, 0, 0);
-      constexpr uint32_t idesc_o = make_idesc(128, D, kFmtF16, kFmtF16, 0, 1);
-      const uint64_t dk = smem_desc(smem_u32(smem), 0, 1024, kSwizzle128B);
-      const uint64_t dv = smem_desc(smem_u32(smem + S::kOperand), S::kAtom, 1024, kSwizzle128B);
-      int seg = -1;
-      bool ok = true;
-      auto scores = [&](int i, int n, bool first) {
-        if (first && !mbar_wait(smem_u32(&s_qfull[i]), seg & 1, abort, A.err)) return false;
-        tc_fence_after();
-        const uint64_t kd = desc_add(dk, (n % kStages) * 2 * S::kOperand);
-        const uint32_t t = tmem + i * kTileCols;
+    // The whole warp runs the loop, so that descriptors and addresses are uniform values (an
+    // MMA takes them from uniform registers); one lane issues. All 512 columns are this
+    // block's: tensor memory starts at column 0.
+    constexpr uint32_t idesc_s = make_idesc(128, kPage, kFmtF16, kFmtF16, 0, 0);
+    constexpr uint32_t idesc_o = make_idesc(128, D, kFmtF16, kFmtF16, 0, 1);
+    const uint64_t dk = smem_desc(smem_u32(smem), 0, 1024, kSwizzle128B);
+    const uint64_t dv = smem_desc(smem_u32(smem) + S::kOperand, S::kAtom, 1024, kSwizzle128B);
+    const bool issuer = elect_one();
+    uint32_t qphase = 1, first = 0;               // first: unit n begins a segment
+    int stage = 0;                                // of unit n + 1
+    uint32_t phase = 0;
+    uint64_t kd = dk, vd = dv, vd_next = dv;      // unit n + 1's keys, unit n's and n + 1's values
+    bool ok = tmem == 0;
+    if (!ok) {
+      *abort = 1;
+      record_error(A.err, kDevTimeout);
+    }
+    auto scores = [&](int i, bool with_q) {
+      if (with_q && !warp_wait(&s_qfull[i], qphase, abort, A.err)) return false;
+      tc_fence_after();
+      if (issuer) {
+        const uint32_t t = i * kTileCols;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           mma_f16_ts(t, t + kQCol + 8 * k, desc_add(kd, (k >> 2) * S::kAtom + (k & 3) * 32), idesc_s, k != 0);
         mma_commit(smem_u32(&s_sfull[i]));
-        return true;
-      };
-      auto values = [&](int i, int n, bool first) {
-        if (!mbar_wait(smem_u32(&s_pfull[i]), n & 1, abort, A.err)) return false;
-        tc_fence_after();
-        const uint64_t vd = desc_add(dv, (n % kStages) * 2 * S::kOperand);
-        const uint32_t t = tmem + i * kTileCols;
+      }
+      return true;
+    };
+    auto values = [&](int i, int n) {
+      if (!warp_wait(&s_pfull[i], n & 1, abort, A.err)) return false;
+      tc_fence_after();
+      if (issuer) {
+        const uint32_t t = i * kTileCols;
 #pragma unroll
         for (int k = 0; k < kPage / 16; ++k)
-          mma_f16_ts(t + kOCol, t + 8 * k, desc_add(vd, k * 2048), idesc_o, !first || k != 0);
+          mma_f16_ts(t + kOCol, t + 8 * k, desc_add(vd, k * 2048), idesc_o, k != 0 ? 1u : first ^ 1u);
         mma_commit(smem_u32(&s_odone[i]));
-        return true;
-      };
-      bool first = false;                          // unit n begins a segment
-      for (int n = -1; n < count && ok; ++n) {
-        // unit n's values and unit n + 1's scores, tile by tile
-        bool next_first = false;
-        if (n >= 0) ok = mbar_wait(smem_u32(&s_vfull[n % kStages]), (n / kStages) & 1, abort, A.err);
-        if (ok && n + 1 < count) {
-          ok = mbar_wait(smem_u32(&s_kfull[(n + 1) % kStages]), ((n + 1) / kStages) & 1, abort, A.err);
-          next_first = ok && (s_unit[(n + 1) % kStages].flags & kFirst);
-        }
-        if (!ok) break;
-        if (next_first) {
-          // the tiles' new queries come after their outputs: both tiles' values first
-          if (n >= 0) {
-            ok = values(0, n, first) && values(1, n, first);
-            if (ok) mma_commit(smem_u32(&s_empty[n % kStages]));
-          }
-          ++seg;
-          ok = ok && scores(0, n + 1, true) && scores(1, n + 1, true);
-        } else {
-          for (int i = 0; i < 2 && ok; ++i) {
-            ok = values(i, n, first);
-            if (ok && i == 1) mma_commit(smem_u32(&s_empty[n % kStages]));
-            if (ok && n + 1 < count) ok = scores(i, n + 1, false);
-          }
-        }
-        first = next_first;
       }
-      // Everything issued has finished before tensor and shared memory are given back.
+      return true;
+    };
+    for (int n = -1; n < count && ok; ++n) {
+      // unit n's values and unit n + 1's scores, tile by tile
+      uint32_t next_first = 0;
+      const int last_stage = stage == 0 ? kStages - 1 : stage - 1;
+      const bool more = n + 1 < count;
+      if (more) {
+        ok = warp_wait(&s_full[stage], phase, abort, A.err);
+        next_first = ok && (s_unit[stage].flags & kFirst) ? 1u : 0u;
+        kd = desc_add(dk, stage * 2 * S::kOperand);
+        vd_next = desc_add(dv, stage * 2 * S::kOperand);
+      }
+      if (!ok) break;
+      if (__any_sync(0xffffffffu, next_first)) {
+        // the tiles' new queries come after their outputs: both tiles' values first
+        if (n >= 0) {
+          ok = values(0, n) && values(1, n);
+          if (ok && issuer) mma_commit(smem_u32(&s_empty[last_stage]));
+        }
+        qphase ^= 1u;
+        ok = ok && scores(0, true) && scores(1, true);
+      } else {
+        ok = values(0, n);
+        if (ok && more) ok = scores(0, false);
+        if (ok) ok = values(1, n);
+        if (ok && issuer) mma_commit(smem_u32(&s_empty[last_stage]));
+        if (ok && more) ok = scores(1, false);
+      }
+      first = next_first;
+      vd = vd_next;
+      if (++stage == kStages) stage = 0, phase ^= 1u;
+    }
+    // Everything issued has finished before tensor and shared memory are given back.
+    __syncwarp();
+    if (issuer) {
       mma_commit(smem_u32(&s_drain));
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(smem_u32(&s_drain), 0)) {
@@ -442,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
     bool valid = false;
     for (int n = 0; n < count; ++n) {
       const int stage = n % kStages;
-      if (!warp_wait(&s_kfull[stage], (n / kStages) & 1, abort, A.err)) break;
+      if (!warp_wait(&s_full[stage], (n / kStages) & 1, abort, A.err)) break;
       const Unit x = s_unit[stage];
       if (x.flags & kFirst) {
         ++seg;
@@ -536,8 +550,6 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       l += ((a[0] + a[1]) + (a[2] + a[3])) * x.ivs;
       tmem_st_wait();
       tc_fence_before();
-      // the converters' NaN notes of the segment (waited for while the stage is still this unit's)
-      if (!I8 && (x.flags & kLast) && !warp_wait(&s_vfull[stage], (n / kStages) & 1, abort, A.err)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s_pfull[i]));
       if (!(x.flags & kLast)) continue;
