@@ -6,11 +6,13 @@
 // (128 x D x 64) per tile, f16 operands with fp32 sums. The tensor cores bound it: 4 * 64 *
 // 256 * D operations per block, at D = 128 about 1,000 clocks of an SM.
 //
-//   * tensor memory holds, per tile, S (64 columns; P, packed f16, takes the place of the S
-//     it comes from), Q (D/2 columns) and O (D columns): with two tiles of D = 128 all 512.
-//     With Q and P as the A operands from tensor memory, the MMAs read only K and V from
-//     shared memory (64 B a clock or less of the SM's 128), which leaves room for the writes
-//     of the converted codes (from shared memory, Q would be read again for every block).
+//   * tensor memory holds, per tile, two S of 64 columns (P, packed f16, takes the place of
+//     the S it comes from) and O (D columns): with two tiles of D = 128 all 512. So the next
+//     block's scores are computed while this one's softmax runs, and the softmax of a tile
+//     never waits for its own products. P is the A operand from tensor memory; Q is read from
+//     shared memory. (With Q in tensor memory and one S per tile the MMAs read half as much
+//     shared memory, but each block went through softmax, product and scores one after the
+//     other: 1,950 clocks a block.)
 //   * four warps convert the codes of each block to f16 (exact) once for all 256 rows, into
 //     a ring of 128-byte-swizzled stages: K row by row (K-major), V row by row as well (read
 //     MN-major). Their loads run one block ahead in registers.
@@ -18,7 +20,8 @@
 //     cores do tile 1's products, and the other way round. The block's value scale is part
 //     of the exponent, as in gqa_attend.cu; the reference maximum M moves only when a score
 //     passes it by more than 2^8 (P stays below 256), and only then O is rescaled.
-//   * one thread issues all MMAs.
+//   * one thread per tile issues its MMAs (each costs the issuer some 40 clocks: with one thread
+//     for both tiles the tensor cores waited for it).
 // Items (request, key head, 256 rows) have as many units as blocks their last token sees;
 // all units are laid end to end and cut into equal runs, one per SM, so that the causal
 // triangle and ragged requests leave no SM idle; cut items are merged afterwards.
@@ -33,19 +36,21 @@ namespace dsa {
 namespace {
 
 constexpr int kConvWarp0 = 8, kConvWarps = 4;   // warps 0-3 and 4-7: the softmax of tile 0 and 1
-constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
-constexpr int kStages = 5;
+constexpr int kMmaWarp = 12;                    // and 13: the products of tile 0 and 1
+constexpr int kThreads = 14 * 32;
+constexpr int kStages = 4;
 constexpr int kNanSlots = 16;               // segments whose NaN notes are alive: converters run at most kStages units ahead
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTileCols = 256, kQCol = 64, kOCol = 128;   // of a tile: S / P at 0
+constexpr uint32_t kTileCols = 256, kSCols = 64, kOCol = 128;   // of a tile: S / P at 0 and 64
 constexpr float kRescale = 8.f;
 
 template <int D>
 struct TileShape {
   static constexpr int kAtom = kPage * 128;              // 64 rows x 64 f16
   static constexpr int kOperand = kPage * D * 2;         // K or V of a block
-  static constexpr size_t kSmem = (size_t)kStages * 2 * kOperand + 1024;
+  static constexpr int kQAtom = 128 * 128;               // 128 rows x 64 f16
+  static constexpr int kQTile = D / 64 * kQAtom;
+  static constexpr size_t kSmem = 2 * kQTile + (size_t)kStages * 2 * kOperand + 1024;
 };
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -107,28 +112,32 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
   using S = TileShape<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kStages], s_empty[kStages];
-  __shared__ uint64_t s_sfull[2], s_pfull[2], s_odone[2], s_qfull[2], s_drain;
+  __shared__ uint64_t s_sfull[2][2], s_pfull[2][2],   // [tile][S buffer]
+       s_odone[2], s_qfull[2], s_drain[2];
   __shared__ Unit s_unit[kStages];
   __shared__ int s_nan[I8 ? 1 : kNanSlots][D];
   __shared__ int64_t s_begin, s_end, s_base, s_total;
   __shared__ int s_req, s_grid, s_abort;
   __shared__ uint32_t s_tmem;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* q_smem = smem + (size_t)kStages * 2 * S::kOperand;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
 
   if (tid == 32 * kMmaWarp) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&s_full[i]), kConvWarps);
-      mbar_init(smem_u32(&s_empty[i]), 1);
+      mbar_init(smem_u32(&s_empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s_sfull[i]), 1);
-      mbar_init(smem_u32(&s_pfull[i]), 4);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(smem_u32(&s_sfull[i][k]), 1);
+        mbar_init(smem_u32(&s_pfull[i][k]), 4);
+      }
       mbar_init(smem_u32(&s_odone[i]), 1);
       mbar_init(smem_u32(&s_qfull[i]), 4);
+      mbar_init(smem_u32(&s_drain[i]), 1);
     }
-    mbar_init(smem_u32(&s_drain), 1);
     s_abort = 0;
     fence_mbar_init();
     parts.cuts[blockIdx.x].follow = 0;
@@ -357,86 +366,81 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       if (lane == 0) mbar_arrive(smem_u32(&s_full[stage]));
       if (n + 1 < count) fetch(A.c.v, t_next, vr);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     // The whole warp runs the loop, so that descriptors and addresses are uniform values (an
     // MMA takes them from uniform registers); one lane issues. All 512 columns are this
     // block's: tensor memory starts at column 0.
     constexpr uint32_t idesc_s = make_idesc(128, kPage, kFmtF16, kFmtF16, 0, 0);
     constexpr uint32_t idesc_o = make_idesc(128, D, kFmtF16, kFmtF16, 0, 1);
+    const int i = warp - kMmaWarp;                // tile
+    const uint32_t tcol = i * kTileCols;
     const uint64_t dk = smem_desc(smem_u32(smem), 0, 1024, kSwizzle128B);
     const uint64_t dv = smem_desc(smem_u32(smem) + S::kOperand, S::kAtom, 1024, kSwizzle128B);
     const bool issuer = elect_one();
-    uint32_t qphase = 1, first = 0;               // first: unit n begins a segment
-    int stage = 0;                                // of unit n + 1
+    uint32_t qphase = 0, fresh = 0;               // fresh: unit n begins a segment
+    int stage = 0, before = 0;                    // of units n + 1 and n
     uint32_t phase = 0;
-    uint64_t kd = dk, vd = dv, vd_next = dv;      // unit n + 1's keys, unit n's and n + 1's values
     bool ok = tmem == 0;
     if (!ok) {
       *abort = 1;
       record_error(A.err, kDevTimeout);
     }
-    auto scores = [&](int i, bool with_q) {
-      if (with_q && !warp_wait(&s_qfull[i], qphase, abort, A.err)) return false;
+    const uint64_t dq = smem_desc(smem_u32(q_smem) + i * S::kQTile, 0, 1024, kSwizzle128B);
+    auto scores = [&](int n) {                    // of unit n, in `stage`
       tc_fence_after();
       if (issuer) {
-        const uint32_t t = i * kTileCols;
+        const uint64_t kd = desc_add(dk, stage * 2 * S::kOperand);
+        const uint32_t d = tcol + (n & 1) * kSCols;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_f16_ts(t, t + kQCol + 8 * k, desc_add(kd, (k >> 2) * S::kAtom + (k & 3) * 32), idesc_s, k != 0);
-        mma_commit(smem_u32(&s_sfull[i]));
+          mma_f16_ss(d, desc_add(dq, (k >> 2) * S::kQAtom + (k & 3) * 32), desc_add(kd, (k >> 2) * S::kAtom + (k & 3) * 32),
+                     idesc_s, k != 0);
+        mma_commit(smem_u32(&s_sfull[i][n & 1]));
       }
-      return true;
     };
-    auto values = [&](int i, int n) {
-      if (!warp_wait(&s_pfull[i], n & 1, abort, A.err)) return false;
-      tc_fence_after();
-      if (issuer) {
-        const uint32_t t = i * kTileCols;
+    for (int n = -1; n < count; ++n) {
+      // unit n + 1's scores, then unit n's values; where n + 1 begins a segment, its queries
+      // come after unit n's outputs, so the other way round
+      uint32_t next = 0;
+      if (n + 1 < count) {
+        ok = ok && warp_wait(&s_full[stage], phase, abort, A.err);
+        if (!ok) break;
+        next = s_unit[stage].flags & kFirst;
+        static_assert(kFirst == 1, "next is a flag and an operand");
+        next = __any_sync(0xffffffffu, next) ? 1u : 0u;
+        if (!next) scores(n + 1);
+      }
+      if (n >= 0) {
+        ok = warp_wait(&s_pfull[i][n & 1], (n >> 1) & 1, abort, A.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (issuer) {
+          const uint64_t vd = desc_add(dv, before * 2 * S::kOperand);
+          const uint32_t p = tcol + (n & 1) * kSCols;
 #pragma unroll
-        for (int k = 0; k < kPage / 16; ++k)
-          mma_f16_ts(t + kOCol, t + 8 * k, desc_add(vd, k * 2048), idesc_o, k != 0 ? 1u : first ^ 1u);
-        mma_commit(smem_u32(&s_odone[i]));
-      }
-      return true;
-    };
-    for (int n = -1; n < count && ok; ++n) {
-      // unit n's values and unit n + 1's scores, tile by tile
-      uint32_t next_first = 0;
-      const int last_stage = stage == 0 ? kStages - 1 : stage - 1;
-      const bool more = n + 1 < count;
-      if (more) {
-        ok = warp_wait(&s_full[stage], phase, abort, A.err);
-        next_first = ok && (s_unit[stage].flags & kFirst) ? 1u : 0u;
-        kd = desc_add(dk, stage * 2 * S::kOperand);
-        vd_next = desc_add(dv, stage * 2 * S::kOperand);
-      }
-      if (!ok) break;
-      if (__any_sync(0xffffffffu, next_first)) {
-        // the tiles' new queries come after their outputs: both tiles' values first
-        if (n >= 0) {
-          ok = values(0, n) && values(1, n);
-          if (ok && issuer) mma_commit(smem_u32(&s_empty[last_stage]));
+          for (int k = 0; k < kPage / 16; ++k)
+            mma_f16_ts(tcol + kOCol, p + 8 * k, desc_add(vd, k * 2048), idesc_o, k != 0 ? 1u : fresh ^ 1u);
+          mma_commit(smem_u32(&s_odone[i]));
+          mma_commit(smem_u32(&s_empty[before]));
         }
-        qphase ^= 1u;
-        ok = ok && scores(0, true) && scores(1, true);
-      } else {
-        ok = values(0, n);
-        if (ok && more) ok = scores(0, false);
-        if (ok) ok = values(1, n);
-        if (ok && issuer) mma_commit(smem_u32(&s_empty[last_stage]));
-        if (ok && more) ok = scores(1, false);
       }
-      first = next_first;
-      vd = vd_next;
+      if (next) {
+        ok = warp_wait(&s_qfull[i], qphase, abort, A.err);
+        qphase ^= 1u;
+        if (!ok) break;
+        scores(n + 1);
+      }
+      fresh = next;
+      before = stage;
       if (++stage == kStages) stage = 0, phase ^= 1u;
     }
     // Everything issued has finished before tensor and shared memory are given back.
     __syncwarp();
     if (issuer) {
-      mma_commit(smem_u32(&s_drain));
+      mma_commit(smem_u32(&s_drain[i]));
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&s_drain), 0)) {
+      while (!mbar_try_wait(smem_u32(&s_drain[i]), 0)) {
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
           *abort = 1;
           record_error(A.err, kDevTimeout);
@@ -477,29 +481,23 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
         const int e = min(max((int)(__float_as_uint(big) >> 23), 15), 254);
         const float up = __uint_as_float((uint32_t)(268 - e) << 23);
         rowf = __uint_as_float((uint32_t)(e - 14) << 23);
-#pragma unroll 1
-        for (int k = 0; k < D / 2; k += 32) {
-          uint32_t p[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 v = valid ? __ldg(src + k / 4 + j) : make_uint4(0, 0, 0, 0);
-            p[4 * j] = pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up);
-            p[4 * j + 1] = pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up);
-            p[4 * j + 2] = pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up);
-            p[4 * j + 3] = pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up);
-          }
-          __syncwarp();
-          tmem_st32(tile + kQCol + k, p);
+        uint8_t* mine = q_smem + i * S::kQTile + (r_in & 127) * 128;
+#pragma unroll 4
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 v = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(mine + (k >> 3) * S::kQAtom + (((k & 7) ^ (r_in & 7)) << 4)) =
+              make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                         pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
         }
-        tmem_st_wait();
-        tc_fence_before();
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_qfull[i]));
       }
-      if (!warp_wait(&s_sfull[i], n & 1, abort, A.err)) break;
+      if (!warp_wait(&s_sfull[i][n & 1], (n >> 1) & 1, abort, A.err)) break;
       tc_fence_after();
       float s[64];
-      tmem_ld64(tile, s);
+      const uint32_t sp = tile + (n & 1) * kSCols;
+      tmem_ld64(sp, s);
       tmem_ld_wait();
       if (x.rel + tok_lo < kPage - 1 || (x.flags & kVoid)) {   // some row of the warp does not see every key
         const int lim = (x.flags & kVoid) ? -1 : x.rel + tok;
@@ -546,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
         p[k / 2] = pack_f16(s[k], s[k + 1]);
         p[k / 2 + 1] = pack_f16(s[k + 2], s[k + 3]);
       }
-      tmem_st32(tile, p);
+      tmem_st32(sp, p);
       l += ((a[0] + a[1]) + (a[2] + a[3])) * x.ivs;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&s_pfull[i]));
+      if (lane == 0) mbar_arrive(smem_u32(&s_pfull[i][n & 1]));
       if (!(x.flags & kLast)) continue;
 
       // ---- the segment's outputs, or its part
