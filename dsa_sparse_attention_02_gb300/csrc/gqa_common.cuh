@@ -51,9 +51,10 @@ struct __align__(16) Unit {
   float kf;       // k_scale * sm_scale * log2(e)
   float lv, ivs;  // log2(v_scale), 1 / v_scale
   int flags;
-  int q0, n;      // the request's first token and its number of tokens (listed blocks: the token, 1)
-  int row0, h;    // first row of the tile (row r: token r / G, head r % G of key head h)
   int rel;        // position of token 0, less the block's first position
+  int q0, n;      // the request's first token and its number of tokens (listed blocks: the token, 1)
+  int row0;       // first row of the tile (row r: token r / G, head r % G of key head h)
+  int h;
   int slot;       // partial slot, or -1: the item ends in its outputs
   int c;          // the block's number in the request
   int pad;
@@ -105,6 +106,11 @@ cudaError_t gqa_tiles_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t s
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -458,19 +458,31 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
     float M = kNone, l = 0.f, rowf = 1.f;
     int tok = 0, tok_lo = 0, seg = -1;
     bool valid = false;
-    for (int n = 0; n < count; ++n) {
-      const int stage = n % kStages;
-      if (!warp_wait(&s_full[stage], (n / kStages) & 1, abort, A.err)) break;
-      const Unit x = s_unit[stage];
+    // Of the next unit what every row needs (the rest is read where a segment begins or
+    // ends): fetched while this one's exponentials run.
+    struct Short { float kf, lv, ivs; int flags, rel; } x, x_next;
+    int stage = 0;
+    uint32_t phase = 0;
+    auto peek = [&](Short& s) {
+      if (!warp_wait(&s_full[stage], phase, abort, A.err)) return false;
+      const Unit* u = &s_unit[stage];
+      s = Short{u->kf, u->lv, u->ivs, u->flags, u->rel};
+      return true;
+    };
+    bool ok = peek(x_next);
+    for (int n = 0; n < count && ok; ++n) {
+      x = x_next;
+      const Unit& unit = s_unit[stage];
       if (x.flags & kFirst) {
         ++seg;
-        const int row = x.row0 + r_in;
-        valid = row < x.n * G;
+        const struct { int q0, n, row0, h; } u = {unit.q0, unit.n, unit.row0, unit.h};
+        const int row = u.row0 + r_in;
+        valid = row < u.n * G;
         tok = valid ? row / G : -(1 << 30);
-        tok_lo = (x.row0 + 128 * i + 32 * (warp & 3)) / G;        // of the warp's rows
+        tok_lo = (u.row0 + 128 * i + 32 * (warp & 3)) / G;        // of the warp's rows
         M = kNone, l = 0.f;
         const uint4* src = reinterpret_cast<const uint4*>(
-            A.q + (int64_t)(x.q0 + (valid ? tok : 0)) * A.q_stride + (int64_t)(x.h * G + (valid ? row - tok * G : 0)) * D);
+            A.q + (int64_t)(u.q0 + (valid ? tok : 0)) * A.q_stride + (int64_t)(u.h * G + (valid ? row - tok * G : 0)) * D);
         float big = 0.f;
 #pragma unroll 4
         for (int k = 0; k < D / 8; ++k) {
@@ -507,7 +519,12 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       }
       float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int k = 4; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
+      for (int k = 4; k < 60; k += 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m4[j] = max3(m4[j], s[k + 2 * j], s[k + 2 * j + 1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], s[60 + j]);
       // (a scale of 0 would make masked scores NaN)
       const float f = fmaxf(x.kf * rowf, 1.17549435e-38f);
       const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f + x.lv;
@@ -531,6 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
         }
       }
       const float ref = x.lv - M;
+      struct { int q0, row0, h, slot, c; } end{};   // (read before the stage may be given back)
+      if (x.flags & kLast) end = {unit.q0, unit.row0, unit.h, unit.slot, unit.c};
+      if (n + 1 < count) {
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+        ok = peek(x_next);
+        if (!ok) break;
+      }
       float a[4] = {};
       uint32_t p[32];
 #pragma unroll
@@ -555,11 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       // ---- the segment's outputs, or its part
       if (!warp_wait(&s_odone[i], n & 1, abort, A.err)) break;
       tc_fence_after();
-      const int pos = x.rel + tok + x.c * kPage;
+      const int pos = x.rel + tok + end.c * kPage;
       const bool none = l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
-      const int64_t at = valid ? (int64_t)(x.q0 + tok) * H + x.h * G + (x.row0 + r_in - tok * G) : 0;
-      const int64_t part = (int64_t)x.slot * kGqaTileRows + r_in;
+      const int64_t at = valid ? (int64_t)(end.q0 + tok) * H + end.h * G + (end.row0 + r_in - tok * G) : 0;
+      const int64_t part = (int64_t)end.slot * kGqaTileRows + r_in;
 #pragma unroll 1
       for (int k = 0; k < D; k += 16) {
         float v[16];
@@ -571,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
             if (!none && pos >= s_nan[seg % kNanSlots][k + j]) v[j] = NAN;
         }
         if (!valid) {
-        } else if (x.slot < 0) {
+        } else if (end.slot < 0) {
           uint32_t w[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -590,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       }
       tc_fence_before();
       if (valid) {
-        if (x.slot >= 0) *reinterpret_cast<float2*>(parts.ml + part * 2) = make_float2(M, l);
+        if (end.slot >= 0) *reinterpret_cast<float2*>(parts.ml + part * 2) = make_float2(M, l);
         else if (A.lse) A.lse[at] = none ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
       }
     }
