@@ -16,6 +16,9 @@
 //   * four warps convert the codes of each block to f16 (exact) once for all 256 rows, into
 //     a ring of 128-byte-swizzled stages: K row by row (K-major), V row by row as well (read
 //     MN-major). Their loads run one block ahead in registers.
+//     At D = 128 column d of a row goes to atom (d/8) % 2, 16-byte chunk d/16: the eight lanes
+//     that load a row's 128 bytes of codes then store to eight different bank groups. Q is
+//     laid out the same way, and the outputs' columns come out of O in that order.
 //   * eight warps do the softmax, one thread per row: while tile 0's four work, the tensor
 //     cores do tile 1's products, and the other way round. The block's value scale is part
 //     of the exponent, as in gqa_attend.cu; the reference maximum M moves only when a score
@@ -296,25 +299,26 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       }
       at = 0;
     };
-    // a thread's share of a tensor's codes: kLoads pieces of 16, piece i at row
-    // ct/4 + 32 * (i & 1), columns 64 * (i >> 1) + 16 * (ct & 3)
-    constexpr int kLoads = D / 32;
-    const int prow = ct >> 2, pch = ct & 3;
+    // a thread's share of a tensor's codes: kLoads pieces of 16, piece i in row prow + kStep * i
+    constexpr int kLoads = D / 32, kLanes = D / 16, kStep = 32 * kConvWarps / kLanes;
+    const int prow = ct / kLanes, pch = ct % kLanes;
     uint4 kr[kLoads], vr[kLoads];
     auto fetch = [&](const uint8_t* base, int t, uint4 (&dst)[kLoads]) {
-      const uint4* src = reinterpret_cast<const uint4*>(base + (int64_t)t * (kPage * D));
+      const uint4* src = reinterpret_cast<const uint4*>(base + (int64_t)t * (kPage * D)) + ct;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) dst[i] = __ldg(src + (prow + 32 * (i & 1)) * (D / 16) + 4 * (i >> 1) + pch);
+      for (int i = 0; i < kLoads; ++i) dst[i] = __ldg(src + i * 32 * kConvWarps);
     };
     auto put = [&](uint8_t* dst, int i, const uint4& v) {
-      const int row = prow + 32 * (i & 1);
+      const int row = prow + kStep * i;
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t f[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) codes_f16<I8>(w[k], f[2 * k], f[2 * k + 1]);
-      uint8_t* line = dst + (i >> 1) * S::kAtom + row * 128;
-      *reinterpret_cast<uint4*>(line + (((2 * pch) ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<uint4*>(line + (((2 * pch + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+      uint8_t* line = dst + row * 128;
+      uint8_t* lo = D == 128 ? line + ((pch ^ (row & 7)) << 4) : line + (((2 * pch) ^ (row & 7)) << 4);
+      uint8_t* hi = D == 128 ? lo + S::kAtom : line + (((2 * pch + 1) ^ (row & 7)) << 4);
+      *reinterpret_cast<uint4*>(lo) = make_uint4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<uint4*>(hi) = make_uint4(f[4], f[5], f[6], f[7]);
     };
     batch(begin);
     int t_next = __shfl_sync(0xffffffffu, page_tile, 0);
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       if (!my_whole) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int row = prow + 32 * (i & 1);
+          const int row = prow + kStep * i;
           if (row > my_seen) vr[i] = make_uint4(0, 0, 0, 0);
           if (!I8) {
             uint32_t* w = &vr[i].x;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
               if (bad) {
                 w[k] &= ~bad;
                 for (int e = 0; e < 4; ++e)
-                  if ((bad >> (8 * e)) & 1u) atomicMin(&s_nan[seg % kNanSlots][64 * (i >> 1) + 16 * pch + 4 * k + e], my_c * kPage + row);
+                  if ((bad >> (8 * e)) & 1u) atomicMin(&s_nan[seg % kNanSlots][16 * pch + 4 * k + e], my_c * kPage + row);
               }
             }
           }
@@ -497,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
 #pragma unroll 4
         for (int k = 0; k < D / 8; ++k) {
           const uint4 v = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(mine + (k >> 3) * S::kQAtom + (((k & 7) ^ (r_in & 7)) << 4)) =
+          const int atom = D == 128 ? k & 1 : 0, chunk = D == 128 ? k >> 1 : k;
+          *reinterpret_cast<uint4*>(mine + atom * S::kQAtom + ((chunk ^ (r_in & 7)) << 4)) =
               make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
                          pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
         }
@@ -585,30 +590,40 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       const int64_t at = valid ? (int64_t)(end.q0 + tok) * H + end.h * G + (end.row0 + r_in - tok * G) : 0;
       const int64_t part = (int64_t)end.slot * kGqaTileRows + r_in;
 #pragma unroll 1
-      for (int k = 0; k < D; k += 16) {
-        float v[16];
-        tmem_ld16(tile + kOCol + k, v);
-        tmem_ld_wait();
+      for (int k = 0; k < D; k += 32) {            // columns k .. k + 31
+        float v[32];
+        {
+          float a[16], b[16];
+          tmem_ld16(tile + kOCol + (D == 128 ? k / 2 : k), a);
+          tmem_ld16(tile + kOCol + (D == 128 ? 64 + k / 2 : k + 16), b);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = D == 128 ? ((j >> 3) & 1 ? b[(j & 7) + 8 * (j >> 4)] : a[(j & 7) + 8 * (j >> 4)]) : (j < 16 ? a[j] : b[j - 16]);
+        }
         if (!I8) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < 32; ++j)
             if (!none && pos >= s_nan[seg % kNanSlots][k + j]) v[j] = NAN;
         }
         if (!valid) {
         } else if (end.slot < 0) {
-          uint32_t w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 o = __floats2bfloat162_rn(none ? 0.f : v[2 * j] * inv, none ? 0.f : v[2 * j + 1] * inv);
-            w[j] = *reinterpret_cast<const uint32_t*>(&o);
-          }
           uint4* dst = reinterpret_cast<uint4*>(A.out + at * D + k);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 o =
+                  __floats2bfloat162_rn(none ? 0.f : v[j + 2 * e] * inv, none ? 0.f : v[j + 2 * e + 1] * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&o);
+            }
+            dst[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         } else {
           float4* dst = reinterpret_cast<float4*>(parts.o + part * D + k);
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) dst[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         }
         __syncwarp();
       }
