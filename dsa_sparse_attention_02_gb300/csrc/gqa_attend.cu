@@ -3,12 +3,13 @@
 // dsa_gqa_attend and dsa_gqa_attend_blocks in include/dsa.h).
 //
 // A block (64 keys and values of one head, 2 * 64 * D bytes) is the unit of work; the time
-// goes into bringing units from HBM (D = 128: 16 KB, which the tensor cores multiply with
-// up to 64 query rows in less time than the SM's share of the bandwidth needs to load it).
-// So the units of all (request, key head, row tile) items are laid end to end and cut into
-// equal runs, one per block of threads (two of those per SM); an item that crosses a cut
-// leaves partial results that a second kernel merges. A producer warp brings units through
-// a ring of TMA stages; four warps compute straight from the codes:
+// goes into bringing units from HBM (D = 128: 16 KB, which an SM's share of the bandwidth
+// takes about 700 clocks to load). So the units of all (request, key head, row tile) items
+// are laid end to end and cut into equal runs, and every run belongs to one warp, or a team
+// of two or four warps where an item has more than 16 query rows. The warps of an SM work
+// without meeting: each team brings its units' keys and values through a ring of its own by
+// TMA and keeps its rows' sums in registers. An item that crosses a cut leaves partial results
+// that a second kernel merges.
 //
 //   * 16 keys x 8 query rows per step on mma.sync m16n8k16 (f16, fp32 sums), the keys (and
 //     the values' columns) as the 16 rows of A, so that a group of up to 8 heads wastes
@@ -32,10 +33,6 @@
 namespace dsa {
 
 namespace {
-
-constexpr int kConsumers = 4;               // computing warps; one more brings the units
-constexpr int kThreads = 32 * (kConsumers + 1);
-
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -95,248 +92,211 @@ __device__ __forceinline__ Request request_of(const GqaAttendArgs& A, int b, int
   return r;
 }
 
-// A warp has NT tiles of 8 query rows; MT warps share a unit's keys, each with rows of its own.
+// A warp has NT tiles of 8 query rows; a team of MT warps shares its units, each with rows of
+// its own. The team's ring holds halves (a unit's keys, or its values) in turn.
 template <int D, int NT, int MT>
 struct Shape {
+  static constexpr int kWarps = 8;                               // one block of threads per SM
   static constexpr int kRows = 8 * NT * MT;
-  static constexpr int kTile = kPage * D;                        // bytes of a unit's keys (and of its values)
-  static constexpr int kAcc = NT * D / 4;                        // fp32 sums per lane
-  static constexpr int kGroups = kConsumers / MT;                // warps that share a row tile, each with its keys
-  static constexpr int kMergeBufs = (kGroups - 1) * MT;
-  static constexpr int kMergeFloats = (kAcc + 4 * NT) * 32;
-  static constexpr int kCtas = NT == 1 ? 3 : 2;                  // per SM
-  static constexpr int kStages = NT == 1 ? 3 : 4;
-  static constexpr size_t kSmem = (size_t)kStages * 2 * kTile + (size_t)kMergeBufs * kMergeFloats * 4 + 1024;
+  static constexpr int kTeams = kWarps / MT;
+  static constexpr int kHalf = kPage * D;                        // bytes
+  static constexpr int kRing = 3 * MT * (128 / D);               // halves
+  // Halves that a lead warp stays behind with new loads, so that it does not wait for the
+  // others to have read the slot.
+  static constexpr int kLag = MT == 1 ? 0 : 2;
+  static constexpr size_t kSmem = (size_t)kTeams * kRing * kHalf + 1024;
 };
 
 template <int D, bool I8, int NT, int MT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
+__global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
     gqa_rows_kernel(const GqaAttendArgs A, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const GqaParts parts) {
   using S = Shape<D, NT, MT>;
-  constexpr int kRows = S::kRows, kStages = S::kStages;
+  constexpr int kRows = S::kRows, kRing = S::kRing, kAhead = S::kRing - S::kLag;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_full[kStages], s_empty[kStages], s_meet;
-  __shared__ Unit s_unit[kStages];
-  __shared__ int64_t s_begin, s_end, s_base, s_total;
-  __shared__ int s_req, s_grid, s_abort;
+  __shared__ uint64_t s_full[S::kTeams][kRing], s_empty[S::kTeams][kRing];
+  __shared__ int s_abort;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* merge = reinterpret_cast<float*>(smem + kStages * 2 * S::kTile);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int team = warp / MT, m = warp % MT;
+  const int run = team * gridDim.x + blockIdx.x, runs = S::kTeams * gridDim.x;   // teams of an SM far apart
   const bool listed = A.blocks != nullptr;
   griddep_launch_dependents();
-
-  if (tid == 32) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_empty[i]), kConsumers);
+  if (tid == 0) {
+    for (int i = 0; i < S::kTeams * kRing; ++i) {
+      mbar_init(smem_u32(&s_full[0][0] + i), 1);
+      mbar_init(smem_u32(&s_empty[0][0] + i), MT);
     }
     s_abort = 0;
-    mbar_init(smem_u32(&s_meet), kConsumers);
     fence_mbar_init();
-    parts.cuts[blockIdx.x].follow = 0;
   }
-  // This block's run [s_begin, s_end) of all units. Whole contexts: the request it starts in
-  // and where that request's units begin.
-  if (warp == 0) {
-    int64_t total = 0;
-    if (listed) {
-      total = (int64_t)A.g.T * A.c.Hkv * A.n_sel;
-    } else {
-      for (int b0 = 0; b0 < A.g.B; b0 += 32) {
-        int64_t w = 0;
-        if (b0 + lane < A.g.B) {
-          const Request r = request_of(A, b0 + lane, kRows);
-          w = (int64_t)A.c.Hkv * r.tiles * r.units;
-          if (r.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
-        }
-        total += w;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
-    const int grid = (int)min((int64_t)gridDim.x, total);
-    int64_t begin = 0, end = 0;
-    if ((int)blockIdx.x < grid) {
-      begin = split_begin(blockIdx.x, total, grid);
-      end = split_begin(blockIdx.x + 1, total, grid);
-    }
-    int req = 0;
-    int64_t base = 0;
-    if (!listed && begin < end) {
-      for (int b0 = 0; b0 < A.g.B; b0 += 32) {
-        int64_t w = 0;
-        if (b0 + lane < A.g.B) {
-          const Request r = request_of(A, b0 + lane, kRows);
-          w = (int64_t)A.c.Hkv * r.tiles * r.units;
-        }
-        int64_t upto = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += v;
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, base + upto > begin);
-        if (m) {
-          const int l = __ffs(m) - 1;
-          req = b0 + l;
-          base += __shfl_sync(0xffffffffu, upto - w, l);
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
-    if (lane == 0) {
-      s_begin = begin, s_end = end, s_base = base, s_total = total;
-      s_req = req, s_grid = grid;
-    }
-  }
+  if (m == 0 && lane == 0) parts.cuts[run].follow = 0;
   __syncthreads();
-  const int64_t begin = s_begin, end = s_end;
-  if (begin >= end) return;
+
+  // ---- the run [begin, end) of all units; whole contexts: the request it starts in and where
+  // that request's units begin
+  int64_t total = 0, begin = 0, end = 0, base = 0;
+  int req = 0;
+  if (listed) {
+    total = (int64_t)A.g.T * A.c.Hkv * A.n_sel;
+  } else {
+    for (int b0 = 0; b0 < A.g.B; b0 += 32) {
+      if (b0 + lane < A.g.B) {
+        const Request r = request_of(A, b0 + lane, kRows);
+        total += (int64_t)A.c.Hkv * r.tiles * r.units;
+        if (r.bad && run == 0 && m == 0) record_error(A.err, kDevBadIndex);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  const int used = (int)min((int64_t)runs, (total + A.min_run - 1) / A.min_run);
+  if (run >= used) return;
+  begin = split_begin(run, total, used);
+  end = split_begin(run + 1, total, used);
+  if (!listed) {
+    for (int b0 = 0; b0 < A.g.B; b0 += 32) {
+      int64_t w = 0;
+      if (b0 + lane < A.g.B) {
+        const Request r = request_of(A, b0 + lane, kRows);
+        w = (int64_t)A.c.Hkv * r.tiles * r.units;
+      }
+      int64_t upto = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const unsigned mask = __ballot_sync(0xffffffffu, base + upto > begin);
+      if (mask) {
+        const int l = __ffs(mask) - 1;
+        req = b0 + l;
+        base += __shfl_sync(0xffffffffu, upto - w, l);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
   volatile int* abort = &s_abort;
 
-  if (warp == kConsumers) {
-    // ------------------------------------------------------------ producer
-    int stage = 0;
-    uint32_t phase = 0;
-    int64_t u = begin, base = s_base;
-    int b = s_req;
-    Request r{};
-    if (!listed) r = request_of(A, b, kRows);
-    const int grid = s_grid;
-    const int64_t total = s_total;
-    bool ok = true;
-    while (u < end && ok) {
-      // up to 32 units at a time, one per lane
-      int cnt;
-      int64_t item_begin = 0, item_end = 0;      // of the lane's unit
-      int c = 0, bb = b;
-      bool sees = false;
-      Unit x{};
-      if (!listed) {
-        const int64_t mine = (int64_t)A.c.Hkv * r.tiles * r.units;
-        if (u >= base + mine) {                  // next request with tokens
-          base += mine;
-          r = request_of(A, ++b, kRows);
-          continue;
-        }
-        cnt = (int)min((int64_t)32, min(end, base + mine) - u);
-        if (lane < cnt) {
-          const int64_t o = u + lane - base;
-          const int64_t item = o / r.units;
-          c = (int)(o - item * r.units);
-          item_begin = base + item * r.units;
-          item_end = item_begin + r.units;
-          x.h = (int)(item / r.tiles);
-          x.row0 = (int)(item % r.tiles) * kRows;
-          x.q0 = r.q0;
-          x.n = r.n;
-          x.rel = r.len - r.n - c * kPage;
-          // the tile's last token
-          const int last = min(r.n - 1, (x.row0 + kRows - 1) / A.G);
-          sees = c * kPage < r.len && x.rel + last >= 0;
-        }
-      } else {
-        cnt = (int)min((int64_t)32, end - u);
-        if (lane < cnt) {
-          const int64_t item = (u + lane) / A.n_sel;
-          const int i = (int)(u + lane - item * A.n_sel);
-          item_begin = item * A.n_sel;
-          item_end = item_begin + A.n_sel;
-          const int t = (int)(item / A.c.Hkv);
-          x.h = (int)(item % A.c.Hkv);
-          x.q0 = t;
-          const bool real = t < __ldg(A.g.cu_q + A.g.B);
-          x.n = real ? 1 : 0;                    // no rows: a padding token's outputs stay
-          const QueryInfo qi = query_info(A.g, t);
-          bb = qi.b;
-          const bool bad = real && (t < __ldg(A.g.cu_q + bb) || t >= __ldg(A.g.cu_q + bb + 1) ||
-                                    __ldg(A.g.cu_q + bb + 1) > A.g.T || qi.len > A.g.max_seq_len);
-          if (bad) record_error(A.err, kDevBadIndex);
-          if (real && !bad && qi.pos >= 0 && qi.pos < qi.len) {
-            const int* list = A.blocks + item * A.n_sel;
-            c = __ldg(list + i);
-            sees = c >= 0 && c <= (qi.pos >> 6);
-            if (sees && i > 0) {
-              const int before = __ldg(list + i - 1);
-              if (before < 0 || before >= c) {
-                record_error(A.err, kDevBadIndex);
-                sees = false;
-              }
-            }
-            x.rel = qi.pos - c * kPage;
-          }
-        }
+  // ---- units, up to 32 at a time, one per lane; a batch stays within a request
+  struct Lane {
+    float kf, lv, ivs;          // k_scale * sm_scale * log2(e); log2(v_scale), 1 / v_scale
+    int flags, rel;             // position of token 0, less the block's first position
+    int q0, n, row0, h, slot, tile;
+  };
+  int64_t bu = begin;           // the next batch's first unit
+  Request r{};
+  if (!listed) r = request_of(A, req, kRows);
+  auto batch = [&](Lane& x) {
+    x = Lane{};
+    int64_t item_begin = 0, item_end = 0;
+    int c = 0, bb = req, cnt;
+    bool sees = false;
+    if (!listed) {
+      int64_t mine = (int64_t)A.c.Hkv * r.tiles * r.units;
+      while (bu >= base + mine) {                // the next request with tokens
+        base += mine;
+        r = request_of(A, ++req, kRows);
+        mine = (int64_t)A.c.Hkv * r.tiles * r.units;
       }
-      int tile = 0;
+      bb = req;
+      cnt = (int)min((int64_t)32, min(end, base + mine) - bu);
       if (lane < cnt) {
-        if (sees) {
-          const int page = gqa_page(A.g, bb, c);
-          if (page < 0) {
-            record_error(A.err, kDevBadIndex);
-            sees = false;
-          } else {
-            tile = page * A.c.Hkv + x.h;
-            const float vs = __ldg(A.c.v_scale + tile);
-            x.kf = __ldg(A.c.k_scale + tile) * A.scale_log2;
-            x.lv = log2f(vs);
-            x.ivs = 1.f / vs;
-          }
-        }
-        const int64_t at = u + lane;
-        const bool first = at == item_begin || at == begin, last = at + 1 == item_end || at + 1 == end;
-        x.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (sees ? 0 : kVoid);
-        const bool cut = item_begin < begin || item_end > end;
-        x.slot = !cut ? -1 : 2 * (int)blockIdx.x + (max(item_begin, begin) == begin ? 0 : 1);
-        if (last && cut && item_begin >= begin) {   // this block merges the item
-          Cut k{};
-          k.follow = (int)split_owner(item_end - 1, total, grid) - (int)blockIdx.x;
-          k.slot = x.slot;
-          k.q0 = x.q0, k.n = x.n, k.row0 = x.row0, k.h = x.h;
-          parts.cuts[blockIdx.x] = k;
-        }
+        const int64_t o = bu + lane - base, item = o / r.units;
+        c = (int)(o - item * r.units);
+        item_begin = base + item * r.units;
+        item_end = item_begin + r.units;
+        x.h = (int)(item / r.tiles);
+        x.row0 = (int)(item % r.tiles) * kRows;
+        x.q0 = r.q0;
+        x.n = r.n;
+        x.rel = r.len - r.n - c * kPage;
+        const int last = min(r.n - 1, (x.row0 + kRows - 1) / A.G);    // the tile's last token
+        sees = c * kPage < r.len && x.rel + last >= 0;
       }
-      for (int i = 0; i < cnt; ++i) {
-        ok = warp_wait(&s_empty[stage], phase ^ 1u, abort, A.err);
-        if (!ok) break;
-        if (lane == i) {
-          s_unit[stage] = x;
-          const uint32_t bar = smem_u32(&s_full[stage]);
-          if (sees) {
-            const uint32_t dst = smem_u32(smem + stage * 2 * S::kTile);
-            mbar_arrive_expect_tx(bar, 2 * S::kTile);
-            tma_load_3d(dst, &map_k, bar, 0, 0, tile);
-            tma_load_3d(dst + S::kTile, &map_v, bar, 0, 0, tile);
-          } else {
-            mbar_arrive(bar);
+    } else {
+      cnt = (int)min((int64_t)32, end - bu);
+      if (lane < cnt) {
+        const int64_t item = (bu + lane) / A.n_sel;
+        const int i = (int)(bu + lane - item * A.n_sel);
+        item_begin = item * A.n_sel;
+        item_end = item_begin + A.n_sel;
+        const int t = (int)(item / A.c.Hkv);
+        x.h = (int)(item % A.c.Hkv);
+        x.q0 = t;
+        const bool real = t < __ldg(A.g.cu_q + A.g.B);
+        x.n = real ? 1 : 0;                      // no rows: a padding token's outputs stay
+        const QueryInfo qi = query_info(A.g, t);
+        bb = qi.b;
+        const bool bad = real && (t < __ldg(A.g.cu_q + bb) || t >= __ldg(A.g.cu_q + bb + 1) ||
+                                  __ldg(A.g.cu_q + bb + 1) > A.g.T || qi.len > A.g.max_seq_len);
+        if (bad) record_error(A.err, kDevBadIndex);
+        if (real && !bad && qi.pos >= 0 && qi.pos < qi.len) {
+          const int* list = A.blocks + item * A.n_sel;
+          c = __ldg(list + i);
+          sees = c >= 0 && c <= (qi.pos >> 6);
+          if (sees && i > 0) {
+            const int before = __ldg(list + i - 1);
+            if (before < 0 || before >= c) {
+              record_error(A.err, kDevBadIndex);
+              sees = false;
+            }
           }
-        }
-        __syncwarp();
-        if (++stage == kStages) stage = 0, phase ^= 1u;
-      }
-      u += cnt;
-    }
-    if (!ok) {
-      // Gave up: copies still in flight must land before the shared memory is given back
-      // (each stage's last phase; one that was never filled counts as complete).
-      if (lane == 0) {
-        const uint64_t t0 = globaltimer_ns();
-        for (int i = 0; i < kStages; ++i) {
-          const uint32_t par = i < stage ? phase : phase ^ 1u;
-          while (!mbar_test_wait(smem_u32(&s_full[i]), par) && globaltimer_ns() - t0 < kWaitLimitNs) {
-          }
+          x.rel = qi.pos - c * kPage;
         }
       }
     }
-    return;
-  }
+    if (lane < cnt) {
+      if (sees) {
+        const int page = gqa_page(A.g, bb, c);
+        if (page < 0) {
+          record_error(A.err, kDevBadIndex);
+          sees = false;
+        } else {
+          x.tile = page * A.c.Hkv + x.h;
+          const float vs = __ldg(A.c.v_scale + x.tile);
+          x.kf = __ldg(A.c.k_scale + x.tile) * A.scale_log2;
+          x.lv = log2f(vs);
+          x.ivs = 1.f / vs;
+        }
+      }
+      const int64_t at = bu + lane;
+      const bool first = at == item_begin || at == begin, last = at + 1 == item_end || at + 1 == end;
+      x.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (sees ? 0 : kVoid);
+      const bool cut = item_begin < begin || item_end > end;
+      x.slot = !cut ? -1 : 2 * run + (max(item_begin, begin) == begin ? 0 : 1);
+      if (m == 0 && last && cut && item_begin >= begin) {   // the item's merge goes by this run's index
+        Cut k{};
+        k.follow = (int)split_owner(item_end - 1, total, used) - run;
+        k.slot = x.slot;
+        k.q0 = x.q0, k.n = x.n, k.row0 = x.row0, k.h = x.h;
+        parts.cuts[run] = k;
+      }
+    }
+    __syncwarp();
+    bu += cnt;
+    return cnt;
+  };
 
-  // -------------------------------------------------------------- computing warps
+  // ---- loads: half j (unit j / 2's keys or values) goes to ring slot j % kRing
+  uint8_t* ring = smem + (size_t)team * kRing * S::kHalf;
+  uint64_t* full = s_full[team];
+  uint64_t* empty = s_empty[team];
+  Lane x, y;                                     // the batch of the unit at work, and the next one
+  int cnt = batch(x), at = 0;                    // lane of the unit at work
+  int ycnt = 0, lat = 0;                         // lane of the next load, in x, or in y if ycnt
+  int lslot = 0;
+  uint32_t lphase = 1;
+  int64_t left = 2 * (end - begin);              // halves to load
+  int ahead = 0;                                 // halves loaded and not yet read
+  bool lvalues = false;
+
+  // ---- computing
   constexpr int kSteps = D / 16;                 // k16 steps of a score = words of a lane's D/4 key bytes
   constexpr int kTiles = D / 16;                 // 16-column tiles of the output
   constexpr int kVw = D / 32;                    // words of a lane's D/8 bytes of a value
-  const int m = warp % MT, group = warp / MT;
+  constexpr int kSlices = kPage / 16, kPair = NT == 1 ? 4 : 2;
   const int q = lane & 3, lrow = lane >> 2;
   const int G = A.G, H = A.G * A.c.Hkv;
   uint32_t qf[NT][kSteps][2];
@@ -344,362 +304,421 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, MT>::kCtas)
   float M[NT][2], l[NT][2], rowf[NT][2];         // of rows 8i + 2q and + 1
   int tok[NT][2];                                // their tokens, or far below any limit
   int tok_lo = 0, tok_hi = 0;                    // of the warp's rows (tok_hi < 0: none)
-  int stage = 0;
-  uint32_t phase = 0, met = 0;
-  // All computing warps meet here (a bounded wait: a warp that gave up does not come).
-  auto meet = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s_meet));
-    const bool all = warp_wait(&s_meet, met, abort, A.err);
-    met ^= 1u;
-    return all;
-  };
+  uint32_t pb[kSlices][NT][2];                   // weights, f16: rows by lane group, keys 2q, 2q+1 (0) and + 8 (1)
+  int flags = 0, rel = 0, seen = 0;
+  bool some = false, whole = false, values = false, ok = true;
+  int slot = 0;
+  uint32_t phase = 0;
 
-  for (int64_t u = begin; u < end; ++u) {
-    if (!warp_wait(&s_full[stage], phase, abort, A.err)) break;
-    const Unit x = s_unit[stage];
-    if (x.flags & kFirst) {
-      const int r0 = x.row0 + m * 8 * NT, rows = x.n * G;
-      tok_lo = r0 / G;
-      tok_hi = r0 < rows ? min(x.n - 1, (r0 + 8 * NT - 1) / G) : -1;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int row = r0 + 8 * i + lrow;
-        const bool valid = row < rows;
-        const int t = valid ? row / G : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            A.q + (int64_t)(x.q0 + t) * A.q_stride + (int64_t)(x.h * G + (valid ? row - t * G : 0)) * D + q * (D / 4));
-        uint32_t w[D / 8];
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint4 v = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-          w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
-        }
-        float big = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // the row times 2^(14 - e), e the exponent of its largest value (none for infinities)
-        const int e = min(max((int)(__float_as_uint(big) >> 23), 15), 254);
-        const float up = __uint_as_float((uint32_t)(268 - e) << 23);
-        const float down = __uint_as_float((uint32_t)(e - 14) << 23);
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) qf[i][k >> 1][k & 1] = pack_f16(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int mine = r0 + 8 * i + 2 * q + h;
-          rowf[i][h] = __shfl_sync(0xffffffffu, down, 4 * (2 * q + h));
-          tok[i][h] = mine < rows ? mine / G : -(1 << 30);
-          M[i][h] = kNone;
-          l[i][h] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
-      }
-    }
-    const uint32_t kt = smem_u32(smem + stage * 2 * S::kTile), vt = kt + S::kTile;
-    const int seen = (x.flags & kVoid) ? -1 : min(x.rel + tok_hi, kPage - 1);   // last key any row of the warp sees
-    const bool whole = x.rel + tok_lo >= kPage - 1;                             // every row sees every key
+  // Each turn loads ahead, then works on one half.
 #pragma unroll 1
-    for (int sub = 0; sub < MT; ++sub) {
-      const int ts = (group * MT + sub) * 16;
-      if (tok_hi < 0 || ts > seen) break;
-      // ---- scores: s[i][0..3] are key lrow (0, 1) and lrow + 8 (2, 3) with rows 2q, 2q+1
-      float s[NT][4] = {};
-      {
-        uint32_t kw[2][kSteps];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t row = kt + (ts + 8 * j + lrow) * D;
-          if constexpr (D == 128) {
-            const uint4 a = lds128(row + (((2 * q) ^ lrow) << 4)), b = lds128(row + (((2 * q + 1) ^ lrow) << 4));
-            kw[j][0] = a.x, kw[j][1] = a.y, kw[j][2] = a.z, kw[j][3] = a.w;
-            kw[j][4] = b.x, kw[j][5] = b.y, kw[j][6] = b.z, kw[j][7] = b.w;
+  for (int64_t todo = 2 * (end - begin); todo > 0; --todo) {
+    // up to kAhead halves ahead, but not past the batch after the one at work
+    while (left > 0 && ahead < kAhead) {
+      if (!lvalues && lat == (ycnt ? ycnt : cnt)) {
+        if (ycnt) break;
+        ycnt = batch(y);
+        lat = 0;
+      }
+      const int fl = ycnt ? y.flags : x.flags, ti = ycnt ? y.tile : x.tile;
+      const bool load = !(__shfl_sync(0xffffffffu, fl, lat) & kVoid);
+      const int tile = __shfl_sync(0xffffffffu, ti, lat);
+      if (m == 0) {
+        if (MT > 1) {
+          ok = warp_wait(&empty[lslot], lphase, abort, A.err);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&full[lslot]);
+          if (load) {
+            mbar_arrive_expect_tx(bar, S::kHalf);
+            tma_load_3d(smem_u32(ring + lslot * S::kHalf), lvalues ? &map_v : &map_k, bar, 0, 0, tile);
           } else {
-            const uint4 a = lds128(row + ((q ^ ((lrow >> 1) & 3)) << 4));
-            kw[j][0] = a.x, kw[j][1] = a.y, kw[j][2] = a.z, kw[j][3] = a.w;
+            mbar_arrive(bar);
           }
         }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a0, a1, a2, a3;
-          codes_f16<I8>(kw[0][k], a0, a2);
-          codes_f16<I8>(kw[1][k], a1, a3);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) mma16816(s[i], a0, a1, a2, a3, qf[i][k][0], qf[i][k][1]);
+        __syncwarp();
+      }
+      --left, ++ahead;
+      if (lvalues) ++lat;
+      lvalues = !lvalues;
+      if (++lslot == kRing) lslot = 0, lphase ^= 1u;
+    }
+    ok = ok && warp_wait(&full[slot], phase, abort, A.err);
+    if (!ok) {
+      if (m == 0 && lane == 0) {
+        // Gave up: copies still in flight must land before the shared memory is given back (each
+        // slot's last phase; one that was never filled counts as complete).
+        const uint64_t t0 = globaltimer_ns();
+        for (int i = 0; i < kRing; ++i) {
+          const uint32_t par = i < lslot ? lphase ^ 1u : lphase;
+          while (!mbar_test_wait(smem_u32(&full[i]), par) && globaltimer_ns() - t0 < kWaitLimitNs) {
+          }
         }
       }
-      // ---- values (read early: their latency passes under the softmax). vw[k]: token
-      // 2q + (k & 1) + 8 * (k >> 1) of the slice, D/8 bytes from column (D/8) * lrow
-      uint32_t vw[4][kVw];
+      return;
+    }
+    if (!values) {
+      // ============================================================ keys
+      flags = __shfl_sync(0xffffffffu, x.flags, at), rel = __shfl_sync(0xffffffffu, x.rel, at);
+      const float kf = __shfl_sync(0xffffffffu, x.kf, at), lv = __shfl_sync(0xffffffffu, x.lv, at);
+      const float ivs = __shfl_sync(0xffffffffu, x.ivs, at);
+      if (flags & kFirst) {
+        const int q0 = __shfl_sync(0xffffffffu, x.q0, at), n = __shfl_sync(0xffffffffu, x.n, at);
+        const int h = __shfl_sync(0xffffffffu, x.h, at), r0 = __shfl_sync(0xffffffffu, x.row0, at) + m * 8 * NT;
+        const int rows = n * G;
+        tok_lo = r0 / G;
+        tok_hi = r0 < rows ? min(n - 1, (r0 + 8 * NT - 1) / G) : -1;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int tk = ts + 2 * q + (k & 1) + 8 * (k >> 1);
-        if constexpr (D == 128) {
-          const uint4 a = lds128(vt + tk * D + ((lrow ^ (tk & 7)) << 4));
-          vw[k][0] = a.x, vw[k][1] = a.y, vw[k][2] = a.z, vw[k][3] = a.w;
-        } else {
-          const uint2 a = lds64(vt + tk * D + (((lrow >> 1) ^ ((tk >> 1) & 3)) << 4) + (lrow & 1) * 8);
-          vw[k][0] = a.x, vw[k][1] = a.y;
+        for (int i = 0; i < NT; ++i) {
+          const int row = r0 + 8 * i + lrow;
+          const bool valid = row < rows;
+          const int t = valid ? row / G : 0;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              A.q + (int64_t)(q0 + t) * A.q_stride + (int64_t)(h * G + (valid ? row - t * G : 0)) * D + q * (D / 4));
+          uint32_t w[D / 8];
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const uint4 v = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+            w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+          }
+          float big = 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) big = max3(big, fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k])));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          // the row times 2^(14 - e), e the exponent of its largest value (none for infinities)
+          const int e = min(max((int)(__float_as_uint(big) >> 23), 15), 254);
+          const float up = __uint_as_float((uint32_t)(268 - e) << 23);
+          const float down = __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) qf[i][k >> 1][k & 1] = pack_f16(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int mine = r0 + 8 * i + 2 * q + hh;
+            rowf[i][hh] = __shfl_sync(0xffffffffu, down, 4 * (2 * q + hh));
+            tok[i][hh] = mine < rows ? mine / G : -(1 << 30);
+            M[i][hh] = kNone;
+            l[i][hh] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
         }
       }
-      // ---- softmax
-      bool grew = false;
-      float keep[NT][2];
-      uint32_t pb[NT][2];                         // weights, f16: rows by lane group, keys 2q, 2q+1 (0) and + 8 (1)
+      seen = (flags & kVoid) ? -1 : min(rel + tok_hi, kPage - 1);   // last key any row of the warp sees
+      some = tok_hi >= 0 && seen >= 0;
+      whole = rel + tok_lo >= kPage - 1;                            // every row sees every key
+      if (some) {
+        // ---- scores: s[sl][i][0..3] are keys lrow (0, 1) and lrow + 8 (2, 3) of slice sl with rows 2q,
+        // 2q+1 (the steps of kPair slices in turn: each waits for its own previous one only)
+        float s[kSlices][NT][4];
+        const uint32_t kt = smem_u32(ring + slot * S::kHalf);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+        for (int s0 = 0; s0 < kSlices; s0 += kPair) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f = x.kf * rowf[i][h];
-          float z0 = s[i][h] * f, z1 = s[i][2 + h] * f;
+          for (int sl = s0; sl < s0 + kPair; ++sl)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) s[sl][i][0] = s[sl][i][1] = s[sl][i][2] = s[sl][i][3] = 0.f;
+#pragma unroll
+          for (int part = 0; part < D / 64; ++part) {
+            uint4 kw[kPair][2];
+#pragma unroll
+            for (int sl = 0; sl < kPair; ++sl)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t row = kt + (16 * (s0 + sl) + 8 * j + lrow) * D;
+                kw[sl][j] = lds128(row + ((D == 128 ? (2 * q + part) ^ lrow : q ^ ((lrow >> 1) & 3)) << 4));
+              }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int sl = 0; sl < kPair; ++sl) {
+                uint32_t a0, a1, a2, a3;
+                codes_f16<I8>(k == 0 ? kw[sl][0].x : k == 1 ? kw[sl][0].y : k == 2 ? kw[sl][0].z : kw[sl][0].w, a0, a2);
+                codes_f16<I8>(k == 0 ? kw[sl][1].x : k == 1 ? kw[sl][1].y : k == 2 ? kw[sl][1].z : kw[sl][1].w, a1, a3);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                  mma16816(s[s0 + sl][i], a0, a1, a2, a3, qf[i][4 * part + k][0], qf[i][4 * part + k][1]);
+              }
+          }
+        }
+        // ---- softmax
+        bool grew = false;
+        float keep[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = kf * rowf[i][h];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int sl = 0; sl < kSlices; ++sl) {
+              s[sl][i][h] *= f, s[sl][i][2 + h] *= f;
+              if (!whole) {
+                const int lim = rel + tok[i][h] - 16 * sl;
+                if (lrow > lim) s[sl][i][h] = -INFINITY;
+                if (lrow + 8 > lim) s[sl][i][2 + h] = -INFINITY;
+              }
+              mx = max3(mx, s[sl][i][h], s[sl][i][2 + h]);
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float Mn = fmaxf(M[i][h], mx + lv);
+            grew |= Mn > M[i][h];
+            keep[i][h] = ex2(M[i][h] - Mn);
+            M[i][h] = Mn;
+            const float ref = Mn - lv;
+            float sum = 0.f;
+#pragma unroll
+            for (int sl = 0; sl < kSlices; ++sl) {
+              s[sl][i][h] = ex2(s[sl][i][h] - ref);
+              s[sl][i][2 + h] = ex2(s[sl][i][2 + h] - ref);
+              sum += s[sl][i][h] + s[sl][i][2 + h];
+            }
+            l[i][h] = l[i][h] * keep[i][h] + sum * ivs;
+          }
+#pragma unroll
+          for (int sl = 0; sl < kSlices; ++sl) {
+            pb[sl][i][0] = transpose8(pack_f16(s[sl][i][0], s[sl][i][1]));
+            pb[sl][i][1] = transpose8(pack_f16(s[sl][i][2], s[sl][i][3]));
+          }
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+              o[i][j][0] *= keep[i][0], o[i][j][1] *= keep[i][1], o[i][j][2] *= keep[i][0], o[i][j][3] *= keep[i][1];
+        }
+      }
+    } else {
+      // ============================================================ values times weights
+      if (some) {
+        const uint32_t vt = smem_u32(ring + slot * S::kHalf);
+#pragma unroll
+        for (int sl = 0; sl < kSlices; ++sl) {
+          // vw[k]: token 2q + (k & 1) + 8 * (k >> 1) of the slice, D/8 bytes from column (D/8) * lrow
+          uint32_t vw[4][kVw];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tk = 16 * sl + 2 * q + (k & 1) + 8 * (k >> 1);
+            if constexpr (D == 128) {
+              const uint4 a = lds128(vt + tk * D + ((lrow ^ (tk & 7)) << 4));
+              vw[k][0] = a.x, vw[k][1] = a.y, vw[k][2] = a.z, vw[k][3] = a.w;
+            } else {
+              const uint2 a = lds64(vt + tk * D + (((lrow >> 1) ^ ((tk >> 1) & 3)) << 4) + (lrow & 1) * 8);
+              vw[k][0] = a.x, vw[k][1] = a.y;
+            }
+          }
+          bool apart = false;                     // a NaN value that only some rows may meet
           if (!whole) {
-            const int lim = x.rel + tok[i][h] - ts;
-            if (lrow > lim) z0 = -INFINITY;
-            if (lrow + 8 > lim) z1 = -INFINITY;
+            bool nan = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool out = 16 * sl + 2 * q + (k & 1) + 8 * (k >> 1) > seen;
+#pragma unroll
+              for (int w = 0; w < kVw; ++w) {
+                if (out) vw[k][w] = 0u;
+                if (!I8) nan |= __vcmpeq4(vw[k][w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+              }
+            }
+            apart = !I8 && __any_sync(0xffffffffu, nan);
           }
-          float mx = fmaxf(z0, z1);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float Mn = fmaxf(M[i][h], mx + x.lv);
-          grew |= Mn > M[i][h];
-          keep[i][h] = ex2(M[i][h] - Mn);
-          M[i][h] = Mn;
-          const float ref = Mn - x.lv;
-          z0 = ex2(z0 - ref);
-          z1 = ex2(z1 - ref);
-          l[i][h] = l[i][h] * keep[i][h] + (z0 + z1) * x.ivs;
-          s[i][h] = z0, s[i][2 + h] = z1;
+          if (!apart) {
+            value_tiles<D, I8>(vw, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+              for (int i = 0; i < NT; ++i) mma16816(o[i][j], a0, a1, a2, a3, pb[sl][i][0], pb[sl][i][1]);
+            });
+          } else {
+#pragma unroll 1
+            for (int t = tok_lo; t <= tok_hi; ++t) {
+              uint32_t v[4][kVw];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int w = 0; w < kVw; ++w)
+                  v[k][w] = 16 * sl + 2 * q + (k & 1) + 8 * (k >> 1) > rel + t ? 0u : vw[k][w];
+              value_tiles<D, I8>(v, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                  float c[4] = {o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]};
+                  mma16816(c, a0, a1, a2, a3, pb[sl][i][0], pb[sl][i][1]);
+                  if (tok[i][0] == t) o[i][j][0] = c[0], o[i][j][2] = c[2];
+                  if (tok[i][1] == t) o[i][j][1] = c[1], o[i][j][3] = c[3];
+                }
+              });
+            }
+          }
         }
-        pb[i][0] = transpose8(pack_f16(s[i][0], s[i][1]));
-        pb[i][1] = transpose8(pack_f16(s[i][2], s[i][3]));
       }
-      if (__any_sync(0xffffffffu, grew)) {
+      if (flags & kLast) {
+        // ---- the item's outputs, or the run's part of it; a lane holds columns lrow*D/8 .. of its rows
+        const int q0 = __shfl_sync(0xffffffffu, x.q0, at), h0 = __shfl_sync(0xffffffffu, x.h, at);
+        const int row0 = __shfl_sync(0xffffffffu, x.row0, at), pslot = __shfl_sync(0xffffffffu, x.slot, at);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < kTiles; ++j)
-            o[i][j][0] *= keep[i][0], o[i][j][1] *= keep[i][1], o[i][j][2] *= keep[i][0], o[i][j][3] *= keep[i][1];
-      }
-      // ---- values times weights
-      bool apart = false;                         // a NaN value that only some rows may meet
-      if (!whole) {
-        bool nan = false;
+          for (int h = 0; h < 2; ++h) {
+            float sum = l[i][h];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            if (tok[i][h] >= 0) {
+              const int rr = m * 8 * NT + 8 * i + 2 * q + h;             // row of the item's tile
+              auto col = [&](int d) { return o[i][d >> 1][2 * (d & 1) + h]; };
+              if (pslot < 0) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int64_t to = (int64_t)(q0 + tok[i][h]) * H + h0 * G + (row0 + rr - tok[i][h] * G);
+                uint4* dst = reinterpret_cast<uint4*>(A.out + to * D + lrow * (D / 8));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool out = ts + 2 * q + (k & 1) + 8 * (k >> 1) > seen;
+                for (int d = 0; d < D / 8; d += 8) {
+                  uint32_t w[4];
 #pragma unroll
-          for (int w = 0; w < kVw; ++w) {
-            if (out) vw[k][w] = 0u;
-            if (!I8) nan |= __vcmpeq4(vw[k][w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
-          }
-        }
-        apart = !I8 && __any_sync(0xffffffffu, nan);
-      }
-      if (!apart) {
-        value_tiles<D, I8>(vw, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                  for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(col(d + 2 * k) * inv, col(d + 2 * k + 1) * inv);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&v);
+                  }
+                  dst[d / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (A.lse && lrow == 0) A.lse[to] = sum == 0.f ? -INFINITY : (M[i][h] + log2f(sum)) * 0.6931471805599453f;
+              } else {
+                const int64_t to = (int64_t)pslot * kRows + rr;
+                float4* dst = reinterpret_cast<float4*>(parts.o + to * D + lrow * (D / 8));
 #pragma unroll
-          for (int i = 0; i < NT; ++i) mma16816(o[i][j], a0, a1, a2, a3, pb[i][0], pb[i][1]);
-        });
-      } else {
-        for (int t = tok_lo; t <= tok_hi; ++t) {
-          uint32_t v[4][kVw];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int w = 0; w < kVw; ++w)
-              v[k][w] = ts + 2 * q + (k & 1) + 8 * (k >> 1) > x.rel + t ? 0u : vw[k][w];
-          value_tiles<D, I8>(v, [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              float c[4] = {o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]};
-              mma16816(c, a0, a1, a2, a3, pb[i][0], pb[i][1]);
-              if (tok[i][0] == t) o[i][j][0] = c[0], o[i][j][2] = c[2];
-              if (tok[i][1] == t) o[i][j][1] = c[1], o[i][j][3] = c[3];
+                for (int d = 0; d < D / 8; d += 4) dst[d / 4] = make_float4(col(d), col(d + 1), col(d + 2), col(d + 3));
+                if (lrow == 0) *reinterpret_cast<float2*>(parts.ml + to * 2) = make_float2(M[i][h], sum);
+              }
             }
-          });
-        }
+            __syncwarp();
+          }
+      }
+      if (++at == cnt) {                           // on to the next batch (which the loads have reached)
+        x = y;
+        cnt = ycnt, at = 0, ycnt = 0;
       }
     }
+    // the half has been read: by the whole warp, then by the team
+    values = !values;
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&s_empty[stage]));
-    if (++stage == kStages) stage = 0, phase ^= 1u;
-    if (!(x.flags & kLast)) continue;
-
-    // ---- end of the run's part of the item: the sums of the warps that shared its rows
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 4);
-        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 8);
-        l[i][h] += __shfl_xor_sync(0xffffffffu, l[i][h], 16);
-      }
-    if (S::kGroups > 1) {
-      if (!meet()) break;                         // the last merge has been read
-      if (group > 0) {
-        float* buf = merge + ((group - 1) * MT + m) * S::kMergeFloats + lane;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-#pragma unroll
-          for (int j = 0; j < 4 * kTiles; ++j) buf[(i * 4 * kTiles + j) * 32] = o[i][j >> 2][j & 3];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            buf[(S::kAcc + 4 * i + h) * 32] = M[i][h];
-            buf[(S::kAcc + 4 * i + 2 + h) * 32] = l[i][h];
-          }
-        }
-      }
-      if (!meet()) break;
-      if (group > 0) continue;
-#pragma unroll 1
-      for (int gr = 1; gr < S::kGroups; ++gr) {
-        const float* buf = merge + ((gr - 1) * MT + m) * S::kMergeFloats + lane;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          float mine[2], other[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float Mo = buf[(S::kAcc + 4 * i + h) * 32], Mn = fmaxf(M[i][h], Mo);
-            mine[h] = ex2(M[i][h] - Mn);
-            other[h] = ex2(Mo - Mn);
-            l[i][h] = l[i][h] * mine[h] + buf[(S::kAcc + 4 * i + 2 + h) * 32] * other[h];
-            M[i][h] = Mn;
-          }
-#pragma unroll
-          for (int j = 0; j < 4 * kTiles; ++j)
-            o[i][j >> 2][j & 3] = o[i][j >> 2][j & 3] * mine[j & 1] + buf[(i * 4 * kTiles + j) * 32] * other[j & 1];
-        }
-      }
-    }
-    // a lane holds columns lrow*D/8 .. of its rows
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (tok[i][h] < 0) continue;
-        const int r = m * 8 * NT + 8 * i + 2 * q + h;                 // row of the item's tile
-        auto col = [&](int d) { return o[i][d >> 1][2 * (d & 1) + h]; };
-        if (x.slot < 0) {
-          const float inv = l[i][h] == 0.f ? 0.f : 1.f / l[i][h];
-          const int64_t at = (int64_t)(x.q0 + tok[i][h]) * H + x.h * G + (x.row0 + r - tok[i][h] * G);
-          uint4* dst = reinterpret_cast<uint4*>(A.out + at * D + lrow * (D / 8));
-#pragma unroll
-          for (int d = 0; d < D / 8; d += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(col(d + 2 * k) * inv, col(d + 2 * k + 1) * inv);
-              w[k] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            dst[d / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          if (A.lse && lrow == 0) A.lse[at] = l[i][h] == 0.f ? -INFINITY : (M[i][h] + log2f(l[i][h])) * 0.6931471805599453f;
-        } else {
-          const int64_t at = (int64_t)x.slot * kRows + r;
-          float4* dst = reinterpret_cast<float4*>(parts.o + at * D + lrow * (D / 8));
-#pragma unroll
-          for (int d = 0; d < D / 8; d += 4) dst[d / 4] = make_float4(col(d), col(d + 1), col(d + 2), col(d + 3));
-          if (lrow == 0) *reinterpret_cast<float2*>(parts.ml + at * 2) = make_float2(M[i][h], l[i][h]);
-        }
-      }
+    if (MT > 1 && lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+    if (++slot == kRing) slot = 0, phase ^= 1u;
+    --ahead;
   }
 }
 
-// Merges the parts of items that were cut, in the order of the blocks of threads: block c
-// (x) looks whether it holds an item's first part; eight rows per block (y), a warp each,
-// or all warps on one row after another where an item has many parts.
+// Merges the parts of items that were cut, in the order of the runs: block c (x) looks whether
+// run c holds an item's first part, and if so merges eight of its rows (y). The warps share the
+// parts, each adding its own for all eight rows (so that eight rows' loads are in flight), then
+// each finishes one row.
 constexpr int kMergeWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps)
-    gqa_merge_kernel(const GqaAttendArgs A, const GqaParts s) {
-  constexpr int V = D / 32;
-  __shared__ float s_o[kMergeWarps][D];
-  __shared__ float s_ml[kMergeWarps][2];
+__global__ void __launch_bounds__(32 * kMergeWarps) gqa_merge_kernel(const GqaAttendArgs A, const GqaParts s) {
+  constexpr int V = D / 32, kRows = 8;
+  __shared__ float s_o[kMergeWarps][kRows][D];
+  __shared__ float2 s_ml[kMergeWarps][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
   const Cut k = s.cuts[blockIdx.x];
   if (k.follow <= 0) return;
-  const int rows = s.rows, parts = k.follow + 1, H = A.G * A.c.Hkv;
-  const bool many = parts > 2 * kMergeWarps;
-  const int first = many ? warp : 0, step = many ? kMergeWarps : 1;
-  for (int i = many ? 0 : warp; i < kMergeWarps; i += many ? 1 : kMergeWarps) {
-    const int r = blockIdx.y * kMergeWarps + i, row = k.row0 + r;
-    if (row >= k.n * A.G) break;
-    float M = kNone, l = 0.f, o[V] = {};
-    for (int p = first; p < parts; p += step) {
-      const int64_t slot = p == 0 ? k.slot : 2 * (int64_t)(blockIdx.x + p);
-      const int64_t at = slot * rows + r;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(s.ml + at * 2));
-      float v[V];
-      if constexpr (V == 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(s.o + at * D) + lane);
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-      } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(s.o + at * D) + lane);
-        v[0] = f.x, v[1] = f.y;
-      }
-      const float Mn = fmaxf(M, ml.x), a = ex2(M - Mn), b = ex2(ml.x - Mn);
-      M = Mn;
-      l = l * a + ml.y * b;
+  const int parts = k.follow + 1, r0 = blockIdx.y * kRows;
+  if (k.row0 + r0 >= k.n * A.G) return;
+  float M[kRows], l[kRows], o[kRows][V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = o[j] * a + v[j] * b;
-    }
-    if (many) {
+  for (int r = 0; r < kRows; ++r) {
+    M[r] = kNone, l[r] = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) s_o[warp][lane * V + j] = o[j];
-      if (lane == 0) s_ml[warp][0] = M, s_ml[warp][1] = l;
-      __syncthreads();
-      if (warp == 0) {
-        for (int w = 1; w < kMergeWarps; ++w) {
-          const float Mn = fmaxf(M, s_ml[w][0]), a = ex2(M - Mn), b = ex2(s_ml[w][0] - Mn);
-          M = Mn;
-          l = l * a + s_ml[w][1] * b;
-#pragma unroll
-          for (int j = 0; j < V; ++j) o[j] = o[j] * a + s_o[w][lane * V + j] * b;
-        }
-      }
-      __syncthreads();
-      if (warp != 0) continue;
-    }
-    const int t = row / A.G;
-    const int64_t at = (int64_t)(k.q0 + t) * H + k.h * A.G + (row - t * A.G);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat162 w[V / 2];
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) w[j] = __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
-    if constexpr (V == 4) *(reinterpret_cast<uint2*>(A.out + at * D) + lane) = *reinterpret_cast<uint2*>(w);
-    else *(reinterpret_cast<uint32_t*>(A.out + at * D) + lane) = *reinterpret_cast<uint32_t*>(w);
-    if (A.lse && lane == 0) A.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+    for (int j = 0; j < V; ++j) o[r][j] = 0.f;
   }
+  const unsigned rows = __ballot_sync(0xffffffffu, k.row0 + r0 + (lane & 7) < k.n * A.G) & 0xFFu;   // (others were not written)
+  for (int p = warp; p < parts; p += kMergeWarps) {
+    const int64_t slot = p == 0 ? k.slot : 2 * (int64_t)(blockIdx.x + p);
+    const int64_t at = slot * s.rows + r0;
+    float2 ml[kRows];
+    float v[kRows][V];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (!((rows >> r) & 1u)) continue;
+      ml[r] = __ldcg(reinterpret_cast<const float2*>(s.ml + (at + r) * 2));
+      if constexpr (V == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(s.o + (at + r) * D) + lane);
+        v[r][0] = f.x, v[r][1] = f.y, v[r][2] = f.z, v[r][3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(s.o + (at + r) * D) + lane);
+        v[r][0] = f.x, v[r][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (!((rows >> r) & 1u)) continue;
+      const float Mn = fmaxf(M[r], ml[r].x), a = ex2(M[r] - Mn), b = ex2(ml[r].x - Mn);
+      M[r] = Mn;
+      l[r] = l[r] * a + ml[r].y * b;
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[r][j] = o[r][j] * a + v[r][j] * b;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_o[warp][r][lane * V + j] = o[r][j];
+    if (lane == 0) s_ml[warp][r] = make_float2(M[r], l[r]);
+  }
+  __syncthreads();
+  const int row = k.row0 + r0 + warp;
+  if (row >= k.n * A.G) return;
+  float Mt = kNone, lt = 0.f, ot[V] = {};
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) Mt = fmaxf(Mt, s_ml[w][warp].x);
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float2 ml = s_ml[w][warp];
+    const float b = ex2(ml.x - Mt);
+    lt += ml.y * b;
+#pragma unroll
+    for (int j = 0; j < V; ++j) ot[j] += s_o[w][warp][lane * V + j] * b;
+  }
+  const int t = row / A.G;
+  const int64_t at = (int64_t)(k.q0 + t) * (A.G * A.c.Hkv) + k.h * A.G + (row - t * A.G);
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  __nv_bfloat162 w[V / 2];
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) w[j] = __floats2bfloat162_rn(ot[2 * j] * inv, ot[2 * j + 1] * inv);
+  if constexpr (V == 4) *(reinterpret_cast<uint2*>(A.out + at * D) + lane) = *reinterpret_cast<uint2*>(w);
+  else *(reinterpret_cast<uint32_t*>(A.out + at * D) + lane) = *reinterpret_cast<uint32_t*>(w);
+  if (A.lse && lane == 0) A.lse[at] = lt == 0.f ? -INFINITY : (Mt + log2f(lt)) * 0.6931471805599453f;
 }
 
-// Query rows (tokens x heads of a key head) that meet a unit together. Up to 16 rows: every
-// warp has them all and a quarter of the keys. More: a unit's codes are converted by two or
-// four warps, each for 16 of the rows. Above 64: gqa_tiles.cu.
+// Query rows (tokens x heads of a key head) that meet a unit together. Up to 16 rows: a warp
+// has them all. More: a unit's codes are converted by two or four warps, each for 16 of the
+// rows. Above 64: gqa_tiles.cu.
 int rows_per_item(int T, int B, int G, bool listed) {
   const int64_t rows = listed ? G : ((int64_t)T + B - 1) / B * G;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kGqaTileRows;
 }
 
-int rows_grid(int rows, int num_sms) { return (rows == 8 ? Shape<128, 1, 1>::kCtas : Shape<128, 2, 1>::kCtas) * num_sms; }
+int rows_runs(int rows, int num_sms) {
+  return (rows <= 16 ? Shape<128, 1, 1>::kTeams : rows == 32 ? Shape<128, 2, 2>::kTeams : Shape<128, 2, 4>::kTeams) * num_sms;
+}
 
 template <int D, bool I8, int NT, int MT>
-cudaError_t launch(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
+cudaError_t launch(GqaAttendArgs A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
   using S = Shape<D, NT, MT>;
   constexpr int rows = S::kRows;
-  const int grid = rows_grid(rows, num_sms);
-  const GqaParts s = gqa_parts(A.scratch, grid, rows);
+  const int runs = rows_runs(rows, num_sms);
+  const GqaParts s = gqa_parts(A.scratch, runs, rows);
+  // The shortest run: with few items of many units, shorter runs save a warp time that merging
+  // their parts costs again (a unit takes a lone warp about as long as the merge takes for 16 parts).
+  const int most = A.blocks ? A.n_sel : (A.g.max_seq_len + kPage - 1) / kPage;
+  A.min_run = 1;
+  while ((A.min_run + 1) * (A.min_run + 1) * 16 <= most) ++A.min_run;
   auto kern = gqa_rows_kernel<D, I8, NT, MT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, S::kSmem, st>>>(A, mk, mv, s);
+  kern<<<num_sms, 32 * S::kWarps, S::kSmem, st>>>(A, mk, mv, s);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return gqa_merge_launch(A, s, grid, st);
+  return e != cudaSuccess ? e : gqa_merge_launch(A, s, runs, st);
 }
 
 template <int D, bool I8>
@@ -729,7 +748,7 @@ cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int grid
 
 size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int, int D, int G, int n_sel, int num_sms) {
   const int rows = rows_per_item(g->T, g->B, G, n_sel > 0);
-  return rows > 64 ? gqa_parts_bytes(num_sms, kGqaTileRows, D) : gqa_parts_bytes(rows_grid(rows, num_sms), rows, D);
+  return rows > 64 ? gqa_parts_bytes(num_sms, kGqaTileRows, D) : gqa_parts_bytes(rows_runs(rows, num_sms), rows, D);
 }
 
 cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st) {
