@@ -332,43 +332,51 @@ class GqaCache:
                 raise TypeError(f"{name} is on {t.device}, k on {k.device}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.k_mean, self.k_mean_scale = k_mean, k_mean_scale
-        self.Hkv, self.D, self.num_pages, self.device = int(Hkv), int(D), int(P), k.device
+        self.Hkv, self.D, self.num_pages = int(Hkv), int(D), int(P)
+        self.device, self.index = k.device, k.get_device()
         self.c = dsa_gqa_cache_t(kinds[k.dtype], self.Hkv, self.D, _dptr(k), _dptr(v), _dptr(k_scale), _dptr(v_scale),
                                  _dptr(k_mean), _dptr(k_mean_scale))
+        self.ref = C.byref(self.c)
 
-    @property
-    def ref(self):
-        return C.byref(self.c)
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _gqa_call(geom: Geometry, cache: GqaCache, ws, stream):
-    """Checks common to the grouped-query calls; the stream to enqueue on."""
+    """Checks common to the grouped-query calls; the raw stream to enqueue on. (These calls
+    take microseconds: on the way of a call that fits, nothing is formatted or looked up twice.)"""
+    dev = cache.index
     if cache.num_pages < geom.num_pages:
         raise ValueError(f"the cache has {cache.num_pages} pages, the geometry {geom.num_pages}")
-    if cache.device.index != torch.cuda.current_device() or geom.seq_lens.device != cache.device or ws.device != cache.device:
+    if ws.get_device() != dev or geom.seq_lens.get_device() != dev or torch.cuda.current_device() != dev:
         raise ValueError(f"cache on {cache.device}, geometry on {geom.seq_lens.device}, workspace on {ws.device}: "
                          f"all must be on the current device, cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _heads(name, t, geom, cache, heads=None, dtype=torch.bfloat16, strided=True):
-    """Address and token stride of a [T, heads, D] tensor (heads of a token side by side)."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != geom.T or t.shape[2] != cache.D or (heads and t.shape[1] != heads):
-        raise TypeError(f"{name} must be a {dtype} tensor of shape [{geom.T}, {heads or 'H'}, {cache.D}]")
+def _heads(name, t, geom, cache, heads=None, strided=True):
+    """Address and token stride of a bf16 [T, heads, D] tensor (heads of a token side by side)."""
+    sh, st, D = t.shape, t.stride(), cache.D
+    if (t.dtype is _BF16 and len(sh) == 3 and sh[0] == geom.T and sh[2] == D and (heads is None or sh[1] == heads)
+            and t.get_device() == cache.index):
+        row = sh[1] * D
+        if st[2] == 1 and (st[1] == D or sh[1] == 1) and (st[0] == row or strided or sh[0] <= 1):
+            return t.data_ptr(), (st[0] if sh[0] > 1 else row)
+        raise TypeError(f"{name}: " + ("each token's heads must lie side by side" if strided else "must be contiguous"))
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != cache.D and t.shape[1] > 1) or (not strided and not t.is_contiguous()):
-        raise TypeError(f"{name}: " + ("each token's heads must lie side by side" if strided else "must be contiguous"))
-    return _dptr(t), (s0 if t.shape[0] > 1 else t.shape[1] * cache.D)
+    raise TypeError(f"{name} must be a {_BF16} tensor of shape [{geom.T}, {heads or 'H'}, {D}]")
 
 
 def _plain(name, t, dtype, shape, cache):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == cache.index:
+        return t.data_ptr()
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    return _dptr(t)
+    raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
 
 
 def dsa_gqa_append_workspace_size(geom: Geometry, cache: GqaCache) -> int:
@@ -384,15 +392,18 @@ def dsa_gqa_append(geom: Geometry, cache: GqaCache, k_new, v_new, q_in=None, q_o
     v, vs = _heads("v_new", v_new, geom, cache, cache.Hkv)
     H, q, qs, qo = 0, None, 0, None
     if q_in is not None:
-        H = int(q_in.shape[1])
+        H = q_in.shape[1]
         q, qs = _heads("q_in", q_in, geom, cache)
-        qo, _ = _heads("q_out", q_out, geom, cache, H, strided=False)
+        qo, _ = _heads("q_out", q_out, geom, cache, H, False)
     cos = sin = None
     if rope_dim:
         table = (geom.max_seq_len, rope_dim // 2)
-        cos, sin = (_plain(n, t, torch.float32, table, cache) for n, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)))
-    _check(load().dsa_gqa_append(geom.ref, cache.ref, k, ks, v, vs, H, q, qs, qo, int(rope_dim), cos, sin, _dptr(ws),
-                                 ws.numel(), st), "dsa_gqa_append")
+        cos = _plain("rope_cos", rope_cos, _F32, table, cache)
+        sin = _plain("rope_sin", rope_sin, _F32, table, cache)
+    s = load().dsa_gqa_append(geom.ref, cache.ref, k, ks, v, vs, H, q, qs, qo, rope_dim, cos, sin, ws.data_ptr(),
+                              ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_gqa_append")
 
 
 def dsa_gqa_attend_workspace_size(geom: Geometry, cache: GqaCache, H: int) -> int:
@@ -403,12 +414,13 @@ def dsa_gqa_attend(geom: Geometry, cache: GqaCache, q, sm_scale: float, out, lse
     """Causal grouped-query attention of q [T, H, D] over the whole context into out
     [T, H, D] bf16 and lse [T, H] fp32 (or None)."""
     st = _gqa_call(geom, cache, ws, stream)
-    H = int(q.shape[1])
+    H = q.shape[1]
     qp, qs = _heads("q", q, geom, cache)
-    o, _ = _heads("out", out, geom, cache, H, strided=False)
-    le = None if lse is None else _plain("lse", lse, torch.float32, (geom.T, H), cache)
-    _check(load().dsa_gqa_attend(geom.ref, cache.ref, H, qp, qs, float(sm_scale), o, le, _dptr(ws), ws.numel(), st),
-           "dsa_gqa_attend")
+    o, _ = _heads("out", out, geom, cache, H, False)
+    le = None if lse is None else _plain("lse", lse, _F32, (geom.T, H), cache)
+    s = load().dsa_gqa_attend(geom.ref, cache.ref, H, qp, qs, sm_scale, o, le, ws.data_ptr(), ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_gqa_attend")
 
 
 def dsa_block_select_workspace_size(geom: Geometry, cache: GqaCache, n_sel: int) -> int:
@@ -419,11 +431,12 @@ def dsa_block_select(geom: Geometry, cache: GqaCache, q, n_sel: int, n_first: in
     """The n_sel blocks of each (token, key head) that score best by their means, the first
     n_first and last n_last visible ones always among them, into blocks [T, Hkv, n_sel]."""
     st = _gqa_call(geom, cache, ws, stream)
-    H = int(q.shape[1])
     qp, qs = _heads("q", q, geom, cache)
-    bp = _plain("blocks", blocks, torch.int32, (geom.T, cache.Hkv, int(n_sel)), cache)
-    _check(load().dsa_block_select(geom.ref, cache.ref, H, qp, qs, int(n_sel), int(n_first), int(n_last), bp, _dptr(ws),
-                                   ws.numel(), st), "dsa_block_select")
+    bp = _plain("blocks", blocks, _I32, (geom.T, cache.Hkv, n_sel), cache)
+    s = load().dsa_block_select(geom.ref, cache.ref, q.shape[1], qp, qs, n_sel, n_first, n_last, bp, ws.data_ptr(),
+                                ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_block_select")
 
 
 def dsa_gqa_attend_blocks_workspace_size(geom: Geometry, cache: GqaCache, H: int, n_sel: int) -> int:
@@ -433,13 +446,14 @@ def dsa_gqa_attend_blocks_workspace_size(geom: Geometry, cache: GqaCache, H: int
 def dsa_gqa_attend_blocks(geom: Geometry, cache: GqaCache, q, blocks, sm_scale: float, out, lse, ws, stream=None):
     """dsa_gqa_attend over the listed blocks [T, Hkv, n_sel] of each (token, key head)."""
     st = _gqa_call(geom, cache, ws, stream)
-    H, n = int(q.shape[1]), int(blocks.shape[-1])
+    H, n = q.shape[1], blocks.shape[-1]
     qp, qs = _heads("q", q, geom, cache)
-    bp = _plain("blocks", blocks, torch.int32, (geom.T, cache.Hkv, n), cache)
-    o, _ = _heads("out", out, geom, cache, H, strided=False)
-    le = None if lse is None else _plain("lse", lse, torch.float32, (geom.T, H), cache)
-    _check(load().dsa_gqa_attend_blocks(geom.ref, cache.ref, H, qp, qs, bp, n, float(sm_scale), o, le, _dptr(ws),
-                                        ws.numel(), st), "dsa_gqa_attend_blocks")
+    bp = _plain("blocks", blocks, _I32, (geom.T, cache.Hkv, n), cache)
+    o, _ = _heads("out", out, geom, cache, H, False)
+    le = None if lse is None else _plain("lse", lse, _F32, (geom.T, H), cache)
+    s = load().dsa_gqa_attend_blocks(geom.ref, cache.ref, H, qp, qs, bp, n, sm_scale, o, le, ws.data_ptr(), ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_gqa_attend_blocks")
 
 
 def dsa_stage_copy(dst, src, nbytes: int, stream=None):

@@ -19,7 +19,9 @@
 //     order of the summation index is free, so a lane's fragments are D/4 consecutive bytes
 //     of a key, and a value pair's halves are put side by side by one byte permute.
 //   * both 8-bit types are exact in f16. Queries are scaled by a power of two per row (so
-//     that bf16's range fits f16) and are exact to 2^-38 of the row's largest value.
+//     that bf16's range fits f16) and are exact to 2^-38 of the row's largest value. (The e4m3
+//     form of mma.sync, with the query as two e4m3 parts and the keys' codes as they are, was
+//     slower: 1,184 us instead of 837 for the blocks of 2048 tokens.)
 //   * the block's key scale multiplies the scores. Its value scale enters the exponent: with
 //     M the running maximum of z + log2(v_scale), the weights p = 2^(z - M + log2(v_scale))
 //     are at most 1, multiply the codes directly, and the softmax's sum is of p / v_scale.
@@ -51,6 +53,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -60,16 +63,17 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // The A fragments of a slice's values, 16 columns at a time: take(tile, a0, a1, a2, a3).
 template <int D, bool I8, typename F>
 __device__ __forceinline__ void value_tiles(const uint32_t (&v)[4][D / 32], F take) {
+  uint32_t f[2][4];
+  auto convert = [&](int j, uint32_t (&to)[4]) {
+    const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+    codes_f16<I8>(__byte_perm(v[0][j >> 1], v[1][j >> 1], sel), to[0], to[1]);
+    codes_f16<I8>(__byte_perm(v[2][j >> 1], v[3][j >> 1], sel), to[2], to[3]);
+  };
+  convert(0, f[0]);
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t sel = e ? 0x7362u : 0x5140u;
-      uint32_t a0, a1, a2, a3;
-      codes_f16<I8>(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
-      codes_f16<I8>(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
-      take(2 * w + e, a0, a1, a2, a3);
-    }
+  for (int j = 0; j < D / 16; ++j) {               // (the next tile is converted while this one is multiplied)
+    if (j + 1 < D / 16) convert(j + 1, f[(j + 1) & 1]);
+    take(j, f[j & 1][0], f[j & 1][1], f[j & 1][2], f[j & 1][3]);
   }
 }
 
@@ -93,25 +97,25 @@ __device__ __forceinline__ Request request_of(const GqaAttendArgs& A, int b, int
 }
 
 // A warp has NT tiles of 8 query rows; a team of MT warps shares its units, each with rows of
-// its own. The team's ring holds halves (a unit's keys, or its values) in turn.
-template <int D, int NT, int MT>
+// its own. The team's ring holds halves (a unit's keys, or its values) in turn. kWarps: a block
+// of threads per SM.
+template <int D, int NT, int MT, int kWarps = 8>
 struct Shape {
-  static constexpr int kWarps = 8;                               // one block of threads per SM
   static constexpr int kRows = 8 * NT * MT;
   static constexpr int kTeams = kWarps / MT;
   static constexpr int kHalf = kPage * D;                        // bytes
-  static constexpr int kRing = 3 * MT * (128 / D);               // halves
+  static constexpr int kRing = (kWarps == 12 ? 2 : 3 * MT) * (128 / D);   // halves
   // Halves that a lead warp stays behind with new loads, so that it does not wait for the
   // others to have read the slot.
   static constexpr int kLag = MT == 1 ? 0 : 2;
   static constexpr size_t kSmem = (size_t)kTeams * kRing * kHalf + 1024;
 };
 
-template <int D, bool I8, int NT, int MT>
-__global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
+template <int D, bool I8, int NT, int MT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 1)
     gqa_rows_kernel(const GqaAttendArgs A, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const GqaParts parts) {
-  using S = Shape<D, NT, MT>;
+  using S = Shape<D, NT, MT, kWarps>;
   constexpr int kRows = S::kRows, kRing = S::kRing, kAhead = S::kRing - S::kLag;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[S::kTeams][kRing], s_empty[S::kTeams][kRing];
@@ -134,16 +138,17 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
   __syncthreads();
 
   // ---- the run [begin, end) of all units; whole contexts: the request it starts in and where
-  // that request's units begin
-  int64_t total = 0, begin = 0, end = 0, base = 0;
+  // that request's units begin. A.whole: runs are cut between items (few units each), and
+  // nothing has to be merged.
+  int64_t total = 0, begin, end, base = 0;
   int req = 0;
   if (listed) {
-    total = (int64_t)A.g.T * A.c.Hkv * A.n_sel;
+    total = (int64_t)A.g.T * A.c.Hkv * (A.whole ? 1 : A.n_sel);
   } else {
     for (int b0 = 0; b0 < A.g.B; b0 += 32) {
       if (b0 + lane < A.g.B) {
         const Request r = request_of(A, b0 + lane, kRows);
-        total += (int64_t)A.c.Hkv * r.tiles * r.units;
+        total += (int64_t)A.c.Hkv * r.tiles * (A.whole ? 1 : r.units);
         if (r.bad && run == 0 && m == 0) record_error(A.err, kDevBadIndex);
       }
     }
@@ -154,42 +159,61 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
   if (run >= used) return;
   begin = split_begin(run, total, used);
   end = split_begin(run + 1, total, used);
-  if (!listed) {
-    for (int b0 = 0; b0 < A.g.B; b0 += 32) {
-      int64_t w = 0;
-      if (b0 + lane < A.g.B) {
-        const Request r = request_of(A, b0 + lane, kRows);
-        w = (int64_t)A.c.Hkv * r.tiles * r.units;
-      }
-      int64_t upto = w;
+  if (listed) {
+    if (A.whole) begin *= A.n_sel, end *= A.n_sel;
+  } else {
+    // the request that item or unit `at` lies in, and the unit that it is or begins with
+    auto locate = [&](int64_t at, int& in, int64_t& in_base) {
+      int64_t before = 0, unit = 0;                // items or units, and units, of the requests before
+      for (int b0 = 0; b0 < A.g.B; b0 += 32) {
+        int64_t w = 0, u = 0;
+        int each = 1;
+        if (b0 + lane < A.g.B) {
+          const Request r = request_of(A, b0 + lane, kRows);
+          u = (int64_t)A.c.Hkv * r.tiles * r.units;
+          w = A.whole ? (int64_t)A.c.Hkv * r.tiles : u;
+          each = A.whole ? r.units : 1;
+        }
+        int64_t wsum = w, usum = u;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, wsum, o), z = __shfl_up_sync(0xffffffffu, usum, o);
+          if (lane >= o) wsum += v, usum += z;
+        }
+        const unsigned mask = __ballot_sync(0xffffffffu, before + wsum > at);
+        if (mask) {
+          const int l = __ffs(mask) - 1;
+          in = b0 + l;
+          in_base = unit + __shfl_sync(0xffffffffu, usum - u, l);
+          return in_base + (at - before - __shfl_sync(0xffffffffu, wsum - w, l)) * __shfl_sync(0xffffffffu, each, l);
+        }
+        before += __shfl_sync(0xffffffffu, wsum, 31);
+        unit += __shfl_sync(0xffffffffu, usum, 31);
       }
-      const unsigned mask = __ballot_sync(0xffffffffu, base + upto > begin);
-      if (mask) {
-        const int l = __ffs(mask) - 1;
-        req = b0 + l;
-        base += __shfl_sync(0xffffffffu, upto - w, l);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, upto, 31);
+      return unit;                                 // (at == total)
+    };
+    if (A.whole) {
+      int64_t b2 = 0;
+      int r2 = 0;
+      end = locate(end, r2, b2);
     }
+    begin = locate(begin, req, base);
   }
   volatile int* abort = &s_abort;
 
   // ---- units, up to 32 at a time, one per lane; a batch stays within a request
   struct Lane {
-    float kf, lv, ivs;          // k_scale * sm_scale * log2(e); log2(v_scale), 1 / v_scale
+    float ks, vs;               // the block's scales
     int flags, rel;             // position of token 0, less the block's first position
-    int q0, n, row0, h, slot, tile;
+    int q0, n, row0, h, slot;
+    int tile;                   // page * Hkv + h, or -1: nothing to see
   };
   int64_t bu = begin;           // the next batch's first unit
   Request r{};
   if (!listed) r = request_of(A, req, kRows);
   auto batch = [&](Lane& x) {
     x = Lane{};
+    x.tile = -1;
     int64_t item_begin = 0, item_end = 0;
     int c = 0, bb = req, cnt;
     bool sees = false;
@@ -255,10 +279,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
           sees = false;
         } else {
           x.tile = page * A.c.Hkv + x.h;
-          const float vs = __ldg(A.c.v_scale + x.tile);
-          x.kf = __ldg(A.c.k_scale + x.tile) * A.scale_log2;
-          x.lv = log2f(vs);
-          x.ivs = 1.f / vs;
+          x.vs = __ldg(A.c.v_scale + x.tile);
+          x.ks = __ldg(A.c.k_scale + x.tile);
         }
       }
       const int64_t at = bu + lane;
@@ -266,7 +288,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
       x.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (sees ? 0 : kVoid);
       const bool cut = item_begin < begin || item_end > end;
       x.slot = !cut ? -1 : 2 * run + (max(item_begin, begin) == begin ? 0 : 1);
-      if (m == 0 && last && cut && item_begin >= begin) {   // the item's merge goes by this run's index
+      if (!A.whole && m == 0 && last && cut && item_begin >= begin) {   // the item's merge goes by this run's index
         Cut k{};
         k.follow = (int)split_owner(item_end - 1, total, used) - run;
         k.slot = x.slot;
@@ -288,15 +310,18 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
   int ycnt = 0, lat = 0;                         // lane of the next load, in x, or in y if ycnt
   int lslot = 0;
   uint32_t lphase = 1;
-  int64_t left = 2 * (end - begin);              // halves to load
+  int left = 2 * (int)(end - begin);             // halves to load
   int ahead = 0;                                 // halves loaded and not yet read
+  const bool issuer = elect_one();
   bool lvalues = false;
+  int ltile = -1;
+  const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full);
 
   // ---- computing
   constexpr int kSteps = D / 16;                 // k16 steps of a score = words of a lane's D/4 key bytes
   constexpr int kTiles = D / 16;                 // 16-column tiles of the output
   constexpr int kVw = D / 32;                    // words of a lane's D/8 bytes of a value
-  constexpr int kSlices = kPage / 16, kPair = NT == 1 ? 4 : 2;
+  constexpr int kSlices = kPage / 16, kPair = 2;
   const int q = lane & 3, lrow = lane >> 2;
   const int G = A.G, H = A.G * A.c.Hkv;
   uint32_t qf[NT][kSteps][2];
@@ -312,7 +337,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
 
   // Each turn loads ahead, then works on one half.
 #pragma unroll 1
-  for (int64_t todo = 2 * (end - begin); todo > 0; --todo) {
+  for (int todo = left; todo > 0; --todo) {
     // up to kAhead halves ahead, but not past the batch after the one at work
     while (left > 0 && ahead < kAhead) {
       if (!lvalues && lat == (ycnt ? ycnt : cnt)) {
@@ -320,21 +345,20 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
         ycnt = batch(y);
         lat = 0;
       }
-      const int fl = ycnt ? y.flags : x.flags, ti = ycnt ? y.tile : x.tile;
-      const bool load = !(__shfl_sync(0xffffffffu, fl, lat) & kVoid);
-      const int tile = __shfl_sync(0xffffffffu, ti, lat);
+      if (!lvalues) ltile = __shfl_sync(0xffffffffu, ycnt ? y.tile : x.tile, lat);
       if (m == 0) {
         if (MT > 1) {
           ok = warp_wait(&empty[lslot], lphase, abort, A.err);
           if (!ok) break;
         }
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&full[lslot]);
-          if (load) {
-            mbar_arrive_expect_tx(bar, S::kHalf);
-            tma_load_3d(smem_u32(ring + lslot * S::kHalf), lvalues ? &map_v : &map_k, bar, 0, 0, tile);
-          } else {
+        if (issuer) {
+          const uint32_t bar = full0 + 8 * lslot, dst = ring0 + lslot * S::kHalf;
+          if (ltile < 0) {
             mbar_arrive(bar);
+          } else {
+            mbar_arrive_expect_tx(bar, S::kHalf);
+            if (lvalues) tma_load_3d(dst, &map_v, bar, 0, 0, ltile);
+            else tma_load_3d(dst, &map_k, bar, 0, 0, ltile);
           }
         }
         __syncwarp();
@@ -361,8 +385,8 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
     if (!values) {
       // ============================================================ keys
       flags = __shfl_sync(0xffffffffu, x.flags, at), rel = __shfl_sync(0xffffffffu, x.rel, at);
-      const float kf = __shfl_sync(0xffffffffu, x.kf, at), lv = __shfl_sync(0xffffffffu, x.lv, at);
-      const float ivs = __shfl_sync(0xffffffffu, x.ivs, at);
+      const float kf = __shfl_sync(0xffffffffu, x.ks, at) * A.scale_log2, vs = __shfl_sync(0xffffffffu, x.vs, at);
+      const float lv = __log2f(vs), ivs = __frcp_rn(vs);
       if (flags & kFirst) {
         const int q0 = __shfl_sync(0xffffffffu, x.q0, at), n = __shfl_sync(0xffffffffu, x.n, at);
         const int h = __shfl_sync(0xffffffffu, x.h, at), r0 = __shfl_sync(0xffffffffu, x.row0, at) + m * 8 * NT;
@@ -412,7 +436,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
         // ---- scores: s[sl][i][0..3] are keys lrow (0, 1) and lrow + 8 (2, 3) of slice sl with rows 2q,
         // 2q+1 (the steps of kPair slices in turn: each waits for its own previous one only)
         float s[kSlices][NT][4];
-        const uint32_t kt = smem_u32(ring + slot * S::kHalf);
+        const uint32_t kt = ring0 + slot * S::kHalf;
 #pragma unroll
         for (int s0 = 0; s0 < kSlices; s0 += kPair) {
 #pragma unroll
@@ -429,17 +453,26 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
                 const uint32_t row = kt + (16 * (s0 + sl) + 8 * j + lrow) * D;
                 kw[sl][j] = lds128(row + ((D == 128 ? (2 * q + part) ^ lrow : q ^ ((lrow >> 1) & 3)) << 4));
               }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
+            // (a step's fragments are converted while the step before is multiplied)
+            uint32_t f[2][kPair][4];
+            auto convert = [&](int k, uint32_t (&to)[kPair][4]) {
 #pragma unroll
               for (int sl = 0; sl < kPair; ++sl) {
-                uint32_t a0, a1, a2, a3;
-                codes_f16<I8>(k == 0 ? kw[sl][0].x : k == 1 ? kw[sl][0].y : k == 2 ? kw[sl][0].z : kw[sl][0].w, a0, a2);
-                codes_f16<I8>(k == 0 ? kw[sl][1].x : k == 1 ? kw[sl][1].y : k == 2 ? kw[sl][1].z : kw[sl][1].w, a1, a3);
+                codes_f16<I8>(word(kw[sl][0], k), to[sl][0], to[sl][2]);
+                codes_f16<I8>(word(kw[sl][1], k), to[sl][1], to[sl][3]);
+              }
+            };
+            convert(0, f[0]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k < 3) convert(k + 1, f[(k + 1) & 1]);
+#pragma unroll
+              for (int sl = 0; sl < kPair; ++sl)
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                  mma16816(s[s0 + sl][i], a0, a1, a2, a3, qf[i][4 * part + k][0], qf[i][4 * part + k][1]);
-              }
+                  mma16816(s[s0 + sl][i], f[k & 1][sl][0], f[k & 1][sl][1], f[k & 1][sl][2], f[k & 1][sl][3],
+                           qf[i][4 * part + k][0], qf[i][4 * part + k][1]);
+            }
           }
         }
         // ---- softmax
@@ -495,7 +528,7 @@ __global__ void __launch_bounds__(32 * Shape<D, NT, MT>::kWarps, 1)
     } else {
       // ============================================================ values times weights
       if (some) {
-        const uint32_t vt = smem_u32(ring + slot * S::kHalf);
+        const uint32_t vt = ring0 + slot * S::kHalf;
 #pragma unroll
         for (int sl = 0; sl < kSlices; ++sl) {
           // vw[k]: token 2q + (k & 1) + 8 * (k >> 1) of the slice, D/8 bytes from column (D/8) * lrow
@@ -690,6 +723,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) gqa_merge_kernel(const GqaAt
   if (A.lse && lane == 0) A.lse[at] = lt == 0.f ? -INFINITY : (Mt + log2f(lt)) * 0.6931471805599453f;
 }
 
+// Items of at most this many units are not cut: a warp takes them about as long as the launch
+// of the merge.
+constexpr int kWhole = 2;
+
 // Query rows (tokens x heads of a key head) that meet a unit together. Up to 16 rows: a warp
 // has them all. More: a unit's codes are converted by two or four warps, each for 16 of the
 // rows. Above 64: gqa_tiles.cu.
@@ -698,36 +735,48 @@ int rows_per_item(int T, int B, int G, bool listed) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kGqaTileRows;
 }
 
-int rows_runs(int rows, int num_sms) {
-  return (rows <= 16 ? Shape<128, 1, 1>::kTeams : rows == 32 ? Shape<128, 2, 2>::kTeams : Shape<128, 2, 4>::kTeams) * num_sms;
+// Warps per SM. Lists that give twelve warps 32 units each take twelve: the codes' conversion
+// bounds them (their blocks come from L2), and three warps a sub-partition hide more of its
+// latency than two (2048 tokens, 32 of 256 blocks each: 837 us instead of 954). Otherwise eight,
+// with deeper rings and fewer parts to merge (decode 121 instead of 124 us, 32 blocks of 131072
+// tokens for 8 requests 19 instead of 25).
+int rows_warps(int64_t T, int Hkv, int rows, int n_sel, int num_sms) {
+  return rows == 8 && T * Hkv * n_sel >= (int64_t)32 * 12 * num_sms ? 12 : 8;
 }
 
-template <int D, bool I8, int NT, int MT>
+int rows_runs(int rows, int warps, int num_sms) { return warps / (rows <= 16 ? 1 : rows / 16) * num_sms; }
+
+template <int D, bool I8, int NT, int MT, int kWarps>
 cudaError_t launch(GqaAttendArgs A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
-  using S = Shape<D, NT, MT>;
+  using S = Shape<D, NT, MT, kWarps>;
   constexpr int rows = S::kRows;
-  const int runs = rows_runs(rows, num_sms);
+  const int runs = rows_runs(rows, kWarps, num_sms);
   const GqaParts s = gqa_parts(A.scratch, runs, rows);
   // The shortest run: with few items of many units, shorter runs save a warp time that merging
   // their parts costs again (a unit takes a lone warp about as long as the merge takes for 16 parts).
   const int most = A.blocks ? A.n_sel : (A.g.max_seq_len + kPage - 1) / kPage;
   A.min_run = 1;
-  while ((A.min_run + 1) * (A.min_run + 1) * 16 <= most) ++A.min_run;
-  auto kern = gqa_rows_kernel<D, I8, NT, MT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+  A.whole = most <= kWhole;
+  while (!A.whole && (A.min_run + 1) * (A.min_run + 1) * 16 <= most) ++A.min_run;
+  auto kern = gqa_rows_kernel<D, I8, NT, MT, kWarps>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, S::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  kern<<<num_sms, 32 * S::kWarps, S::kSmem, st>>>(A, mk, mv, s);
+  kern<<<num_sms, 32 * kWarps, S::kSmem, st>>>(A, mk, mv, s);
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : gqa_merge_launch(A, s, runs, st);
+  return e != cudaSuccess || A.whole ? e : gqa_merge_launch(A, s, runs, st);
 }
 
 template <int D, bool I8>
 cudaError_t launch_rows(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
   switch (rows_per_item(A.g.T, A.g.B, A.G, A.blocks != nullptr)) {
-    case 8: return launch<D, I8, 1, 1>(A, mk, mv, num_sms, st);
-    case 16: return launch<D, I8, 2, 1>(A, mk, mv, num_sms, st);
-    case 32: return launch<D, I8, 2, 2>(A, mk, mv, num_sms, st);
-    default: return launch<D, I8, 2, 4>(A, mk, mv, num_sms, st);
+    case 8:
+      if (rows_warps(A.g.T, A.c.Hkv, 8, A.blocks ? A.n_sel : 0, num_sms) == 12)
+        return launch<D, I8, 1, 1, 12>(A, mk, mv, num_sms, st);
+      return launch<D, I8, 1, 1, 8>(A, mk, mv, num_sms, st);
+    case 16: return launch<D, I8, 2, 1, 8>(A, mk, mv, num_sms, st);
+    case 32: return launch<D, I8, 2, 2, 8>(A, mk, mv, num_sms, st);
+    default: return launch<D, I8, 2, 4, 8>(A, mk, mv, num_sms, st);
   }
 }
 
@@ -746,9 +795,10 @@ cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int grid
   return A.c.D == 128 ? cudaLaunchKernelEx(&cfg, gqa_merge_kernel<128>, A, s) : cudaLaunchKernelEx(&cfg, gqa_merge_kernel<64>, A, s);
 }
 
-size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int, int D, int G, int n_sel, int num_sms) {
+size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int Hkv, int D, int G, int n_sel, int num_sms) {
   const int rows = rows_per_item(g->T, g->B, G, n_sel > 0);
-  return rows > 64 ? gqa_parts_bytes(num_sms, kGqaTileRows, D) : gqa_parts_bytes(rows_runs(rows, num_sms), rows, D);
+  if (rows > 64) return gqa_parts_bytes(num_sms, kGqaTileRows, D);
+  return gqa_parts_bytes(rows_runs(rows, rows_warps(g->T, Hkv, rows, n_sel, num_sms), num_sms), rows, D);
 }
 
 cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st) {

@@ -1,5 +1,6 @@
 // What the grouped-query kernels share: tokens of a padded flattened batch, and codes.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -41,6 +42,19 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float2 e4m3x2_f32(uint32_t v) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory; the driver is asked once per device.
+template <typename K>
+inline cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& devices) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (devices.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // ---- attention: runs of units (gqa_attend.cu, gqa_tiles.cu)

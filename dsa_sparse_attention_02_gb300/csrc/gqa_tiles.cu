@@ -646,7 +646,8 @@ template <int D, bool I8>
 cudaError_t launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st) {
   const GqaParts s = gqa_parts(A.scratch, num_sms, kGqaTileRows);
   auto kern = gqa_tiles_kernel<D, I8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TileShape<D>::kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, TileShape<D>::kSmem, allowed);
   if (e != cudaSuccess) return e;
   kern<<<num_sms, kThreads, TileShape<D>::kSmem, st>>>(A, s);
   e = cudaGetLastError();

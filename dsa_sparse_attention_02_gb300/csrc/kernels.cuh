@@ -186,7 +186,8 @@ struct GqaAttendArgs {
   __nv_bfloat16* out;           // [T, G * Hkv, D]
   float* lse;                   // [T, G * Hkv] or null
   void* scratch;
-  int min_run;                  // shortest run of units (set by the launch)
+  int min_run;                  // shortest run of units, and whether runs keep items whole (set by the launch)
+  bool whole;
   int* err;
 };
 size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int Hkv, int D, int G, int n_sel, int num_sms);

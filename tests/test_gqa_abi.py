@@ -116,7 +116,7 @@ def test_binding_refuses_tensors_that_do_not_fit():
             _lib.GqaCache(*bad)
 
     class Handle:                                     # a cache and a geometry without a device
-        D, Hkv, T, num_pages, device = 64, 2, 5, 3, torch.device("cpu")
+        D, Hkv, T, num_pages, device, index = 64, 2, 5, 3, torch.device("cpu"), -1
 
     h = Handle()
     for bad in (torch.zeros(5, 4, 64), torch.zeros(4, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 4, 32, dtype=torch.bfloat16),
@@ -124,8 +124,11 @@ def test_binding_refuses_tensors_that_do_not_fit():
         with pytest.raises(TypeError):
             _lib._heads("q", bad, h, h)
     with pytest.raises(TypeError):
-        _lib._heads("out", torch.zeros(5, 8, 64, dtype=torch.bfloat16)[:, :4], h, h, 4, strided=False)
+        _lib._heads("out", torch.zeros(5, 8, 64, dtype=torch.bfloat16)[:, :4], h, h, 4, False)
     with pytest.raises(TypeError):
         _lib._plain("blocks", torch.zeros(5, 2, 3, dtype=torch.int64), torch.int32, (5, 2, 3), h)
+    h.device, h.index = torch.device("cuda", 0), 0    # now a cache on a GPU: host tensors do not fit
     with pytest.raises(ValueError):
-        _lib._plain("blocks", torch.zeros(5, 2, 3, dtype=torch.int32, device="meta"), torch.int32, (5, 2, 3), h)
+        _lib._plain("blocks", torch.zeros(5, 2, 3, dtype=torch.int32), torch.int32, (5, 2, 3), h)
+    with pytest.raises(ValueError):
+        _lib._heads("q", torch.zeros(5, 4, 64, dtype=torch.bfloat16), h, h)
