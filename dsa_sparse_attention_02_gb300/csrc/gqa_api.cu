@@ -131,9 +131,6 @@ dsa_status_t dsa_gqa_append(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache
   A.rope_cos = rope_cos;
   A.rope_sin = rope_sin;
   A.err = reinterpret_cast<int*>(ws);
-  // Blocks with few new tokens: one block of threads does a key head's keys, values and
-  // queries. Long runs of new tokens: each query head has its own, so that every SM has work.
-  A.parts = geom->T / geom->B >= 16 ? A.G + 1 : 1;
   return from_cuda(gqa_append_launch(A, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -2,6 +2,10 @@
 // quantisation of keys and values into their blocks, and the blocks' key means, in one
 // launch (the definition is at dsa_gqa_append in include/dsa.h).
 //
+// Two kinds of blocks of threads. Queries: a thread owns W rotated pairs of a token (W 8 where
+// the halves allow 16-byte accesses, else 4) and takes its head group's rows with the cosines
+// and sines in registers. Keys and values:
+//
 // A block's scale is a maximum over its tokens, so one block of threads owns the new
 // tokens of one (page, key head): it holds their values in registers, reduces the two
 // magnitudes, and only then encodes. A scale that grows moves the older codes of the
@@ -13,14 +17,14 @@
 // take slots cu_q[b]/64 + 2b onward (n new tokens touch at most n/64 + 2 pages), so the
 // host needs only T and B. Rotation, scale, quotient and code are single IEEE operations
 // in a fixed order: the stored state does not depend on the launch.
+#include <type_traits>
 #include "gqa_common.cuh"
 
 namespace dsa {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kTok = kPage / kWarps;          // new tokens of a block per warp
+constexpr int kQHeads = 4;                    // query heads per thread
 constexpr float kScaleFloor = 7.888609052210118e-31f;   // 2^-100
 constexpr float kFltMax = 3.4028234663852886e38f;
 
@@ -99,7 +103,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // Older codes of one tensor's block: rows [0, rows) of the block, multiplied by ratio if
 // grown; their sums per column into sum (shared) if kSum.
-template <int D, bool I8, bool kSum>
+template <int D, bool I8, bool kSum, int kWarps>
 __device__ __forceinline__ void older_codes(uint8_t* block, int rows, bool grown, float ratio, float* sum) {
   constexpr int kCh = D / 16;
   const int tid = threadIdx.x, ch = tid % kCh;
@@ -137,15 +141,85 @@ __device__ __forceinline__ void older_codes(uint8_t* block, int rows, bool grown
   }
 }
 
-template <int D, bool I8>
-__global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppendArgs A) {
-  constexpr int V = D / 32;
+// Query rows: blocks of threads cover 32 * kWarps / (D / 2W) tokens and kQHeads heads.
+template <int D, int W, int kWarps>
+__device__ __forceinline__ void rotate_queries(const GqaAppendArgs& A, int index) {
+  constexpr int kPer = D / (2 * W);              // threads per row
+  constexpr int kTokens = 32 * kWarps / kPer;
+  const int H = A.G * A.c.Hkv, groups = (H + kQHeads - 1) / kQHeads;
+  const int t = (index / groups) * kTokens + threadIdx.x / kPer, h0 = (index % groups) * kQHeads, ch = threadIdx.x % kPer;
+  const int r = A.rope_dim >> 1;
+  const bool turned = ch < r / W;
+  // the thread's values: W at first, W at second
+  const int first = turned ? ch * W : 2 * r + (ch - r / W) * 2 * W, second = turned ? first + r : first + W;
+  const __nv_bfloat16* src = A.q_in + (int64_t)t * A.q_stride + (int64_t)h0 * D;
+  __nv_bfloat16* dst = A.q_out + ((int64_t)t * H + h0) * D;
+  using Vec = typename std::conditional<W == 8, uint4, uint2>::type;
+  Vec lo[kQHeads], hi[kQHeads];
+#pragma unroll
+  for (int i = 0; i < kQHeads; ++i)
+    if (t < A.g.T && h0 + i < H) {
+      lo[i] = __ldg(reinterpret_cast<const Vec*>(src + i * D + first));
+      hi[i] = __ldg(reinterpret_cast<const Vec*>(src + i * D + second));
+    }
+  // position of each of the warp's tokens, or -1: left as it is
+  int pos = -1;
+#pragma unroll
+  for (int k = 0; k < 32 / kPer; ++k) {
+    const int tk = __shfl_sync(0xffffffffu, t, k * kPer);
+    if (tk >= A.g.T || tk >= __ldg(A.g.cu_q + A.g.B)) continue;
+    const QueryInfo qi = query_info_warp(A.g, tk);
+    const int q0 = __ldg(A.g.cu_q + qi.b), q1 = __ldg(A.g.cu_q + qi.b + 1);
+    const bool ok = tk >= q0 && tk < q1 && q0 >= 0 && q1 <= A.g.T && qi.len <= A.g.max_seq_len && qi.pos < qi.len;
+    if (ok && tk == t) pos = qi.pos;
+  }
+  if (pos < 0) return;
+  float c[W], s[W];
+  if (turned) {
+#pragma unroll
+    for (int j = 0; j < W; j += 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(A.rope_cos + (int64_t)pos * r + first + j));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(A.rope_sin + (int64_t)pos * r + first + j));
+      c[j] = a.x, c[j + 1] = a.y, c[j + 2] = a.z, c[j + 3] = a.w;
+      s[j] = b.x, s[j + 1] = b.y, s[j + 2] = b.z, s[j + 3] = b.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kQHeads; ++i) {
+    if (h0 + i >= H) break;
+    if (turned) {
+      uint32_t* a = reinterpret_cast<uint32_t*>(&lo[i]);
+      uint32_t* b = reinterpret_cast<uint32_t*>(&hi[i]);
+#pragma unroll
+      for (int j = 0; j < W; j += 2) {
+        const float x0 = bf16_lo(a[j / 2]), x1 = bf16_hi(a[j / 2]), y0 = bf16_lo(b[j / 2]), y1 = bf16_hi(b[j / 2]);
+        const __nv_bfloat162 u = __floats2bfloat162_rn(__fsub_rn(__fmul_rn(x0, c[j]), __fmul_rn(y0, s[j])),
+                                                       __fsub_rn(__fmul_rn(x1, c[j + 1]), __fmul_rn(y1, s[j + 1])));
+        const __nv_bfloat162 v = __floats2bfloat162_rn(__fadd_rn(__fmul_rn(y0, c[j]), __fmul_rn(x0, s[j])),
+                                                       __fadd_rn(__fmul_rn(y1, c[j + 1]), __fmul_rn(x1, s[j + 1])));
+        a[j / 2] = *reinterpret_cast<const uint32_t*>(&u);
+        b[j / 2] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    *reinterpret_cast<Vec*>(dst + i * D + first) = lo[i];
+    *reinterpret_cast<Vec*>(dst + i * D + second) = hi[i];
+  }
+}
+
+// Blocks of threads below kv_blocks own (slot, key head)s, the others query rows.
+template <int D, bool I8, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppendArgs A, int slots, int kv_blocks) {
+  constexpr int V = D / 32, kTok = kPage / kWarps;   // kTok: new tokens of a block per warp
   __shared__ float s_amax[2][kWarps];
   __shared__ float s_sum[D];
+  if ((int)blockIdx.x >= kv_blocks) {
+    if ((A.rope_dim & 15) == 0) rotate_queries<D, 8, kWarps>(A, blockIdx.x - kv_blocks);
+    else rotate_queries<D, 4, kWarps>(A, blockIdx.x - kv_blocks);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const GeomDev& g = A.g;
-  const int slot = blockIdx.x;
-  const int kvh = blockIdx.y / A.parts, part = blockIdx.y - kvh * A.parts;
+  const int slot = blockIdx.x % slots, kvh = blockIdx.x / slots;
 
   // request of this slot: the last b with cu_q[b]/64 + 2b <= slot (32 probes a round)
   int lo = 0, n = g.B;
@@ -173,48 +247,10 @@ __global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppend
   if (p0 >= p1) return;
   const int cnt = p1 - p0, t0 = q1 - len + p0;         // token of position p0
 
-  // ---- queries
-  {
-    const int h0 = A.parts == 1 ? 0 : part - 1, nh = A.parts == 1 ? A.G : (part ? 1 : 0);
-    const int H = A.G * A.c.Hkv;
-    constexpr int kU = 4;
-    for (int r0 = warp; r0 < cnt * nh; r0 += kWarps * kU) {
-      Raw<V> raw[kU];
-#pragma unroll
-      for (int i = 0; i < kU; ++i) {
-        const int r = r0 + i * kWarps;
-        if (r < cnt * nh)
-          raw[i] = load_row<V>(A.q_in + (int64_t)(t0 + r / nh) * A.q_stride + (kvh * A.G + h0 + r % nh) * D, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < kU; ++i) {
-        const int r = r0 + i * kWarps;
-        if (r >= cnt * nh) break;
-        float x[V], c[V], s[V];
-        unpack<V>(raw[i], x);
-        load_turn<V>(A, p0 + r / nh, lane, c, s);
-        turn<V>(A, lane, x, c, s);
-        __nv_bfloat162 o[V / 2];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) o[j] = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        __nv_bfloat16* dst = A.q_out + ((int64_t)(t0 + r / nh) * H + kvh * A.G + h0 + r % nh) * D + lane * V;
-        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(o);
-        else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<uint32_t*>(o);
-      }
-    }
-  }
-  if (part != 0) return;
-
   // ---- keys and values
   const int page = gqa_page(g, b, blk);
-  if (page < 0) {
-    if (tid == 0) record_error(A.err, kDevBadIndex);
-    return;
-  }
   const int off = p0 - (blk << 6);                     // older tokens of the block
-  const int64_t tile = (int64_t)page * A.c.Hkv + kvh;
-  const float ks_old = off > 0 ? A.c.k_scale[tile] : 0.f, vs_old = off > 0 ? A.c.v_scale[tile] : 0.f;
-  Raw<V> rk[kTok], rv[kTok];
+  Raw<V> rk[kTok], rv[kTok];                           // (before the page is known)
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
     const int tt = warp + i * kWarps;
@@ -223,6 +259,12 @@ __global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppend
       rv[i] = load_row<V>(A.v_new + (int64_t)(t0 + tt) * A.v_stride + kvh * D, lane);
     }
   }
+  if (page < 0) {
+    if (tid == 0) record_error(A.err, kDevBadIndex);
+    return;
+  }
+  const int64_t tile = (int64_t)page * A.c.Hkv + kvh;
+  const float ks_old = off > 0 ? A.c.k_scale[tile] : 0.f, vs_old = off > 0 ? A.c.v_scale[tile] : 0.f;
   for (int d = tid; d < D; d += 32 * kWarps) s_sum[d] = 0.f;
   float xk[kTok][V], mk = 0.f, mv = 0.f;
 #pragma unroll
@@ -254,9 +296,9 @@ __global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppend
   if (tid == 0) A.c.k_scale[tile] = ks, A.c.v_scale[tile] = vs;
   const bool mean = A.c.k_mean != nullptr;
   const bool kgrown = off > 0 && ks > ks_old, vgrown = off > 0 && vs > vs_old;
-  if (mean) older_codes<D, I8, true>(kb, off, kgrown, __fdiv_rn(ks_old, ks), s_sum);
-  else if (kgrown) older_codes<D, I8, false>(kb, off, true, __fdiv_rn(ks_old, ks), nullptr);
-  if (vgrown) older_codes<D, I8, false>(vb, off, true, __fdiv_rn(vs_old, vs), nullptr);
+  if (mean) older_codes<D, I8, true, kWarps>(kb, off, kgrown, __fdiv_rn(ks_old, ks), s_sum);
+  else if (kgrown) older_codes<D, I8, false, kWarps>(kb, off, true, __fdiv_rn(ks_old, ks), nullptr);
+  if (vgrown) older_codes<D, I8, false, kWarps>(vb, off, true, __fdiv_rn(vs_old, vs), nullptr);
 
   float sum[V] = {};
 #pragma unroll
@@ -308,18 +350,27 @@ __global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppend
   }
 }
 
+template <int D, bool I8, int kWarps>
+cudaError_t launch(const GqaAppendArgs& A, cudaStream_t st) {
+  const int slots = A.g.T / kPage + 2 * A.g.B, kv = slots * A.c.Hkv;
+  const int W = (A.rope_dim & 15) == 0 ? 8 : 4, tokens = 32 * kWarps * 2 * W / D, H = A.G * A.c.Hkv;
+  const int64_t blocks = kv + (A.q_in ? (int64_t)((A.g.T + tokens - 1) / tokens) * ((H + kQHeads - 1) / kQHeads) : 0);
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  gqa_append_kernel<D, I8, kWarps><<<(unsigned)blocks, 32 * kWarps, 0, st>>>(A, slots, kv);
+  return cudaGetLastError();
+}
+
+// Warps of a block: full blocks of new tokens keep sixteen busy, a few tokens not even four.
+template <int D>
+cudaError_t launch_warps(const GqaAppendArgs& A, cudaStream_t st) {
+  if (A.g.T / A.g.B >= 16) return A.c.i8 ? launch<D, true, 16>(A, st) : launch<D, false, 16>(A, st);
+  return A.c.i8 ? launch<D, true, 4>(A, st) : launch<D, false, 4>(A, st);
+}
+
 }  // namespace
 
 cudaError_t gqa_append_launch(const GqaAppendArgs& A, cudaStream_t st) {
-  const dim3 grid(A.g.T / kPage + 2 * A.g.B, A.c.Hkv * A.parts);
-  if (A.c.D == 128) {
-    if (A.c.i8) gqa_append_kernel<128, true><<<grid, 32 * kWarps, 0, st>>>(A);
-    else gqa_append_kernel<128, false><<<grid, 32 * kWarps, 0, st>>>(A);
-  } else {
-    if (A.c.i8) gqa_append_kernel<64, true><<<grid, 32 * kWarps, 0, st>>>(A);
-    else gqa_append_kernel<64, false><<<grid, 32 * kWarps, 0, st>>>(A);
-  }
-  return cudaGetLastError();
+  return A.c.D == 128 ? launch_warps<128>(A, st) : launch_warps<64>(A, st);
 }
 
 }  // namespace dsa

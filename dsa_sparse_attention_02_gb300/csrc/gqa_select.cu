@@ -8,17 +8,21 @@
 // selects there by radix (8 bits a pass), then lists the taken blocks in ascending order
 // with ballots; nothing but the lists goes back to memory.
 //
-// Two shapes: one token per block of threads (decode: every warp scores, all of them
-// select), or eight consecutive tokens (prompts: the mean of a block, read once, meets all
-// tokens of the same request, and each warp selects for one token).
+// Two shapes. One token per block of threads (decode): every warp scores on dp4a, all of them
+// select by radix. Tiles of 16 or 8 consecutive tokens (prompts): a block's mean, converted to
+// f16 once, meets the tile's tokens of the same request on the tensor cores (the codes' products
+// and sums are whole numbers that f16 operands and fp32 sums hold exactly), and each warp selects
+// for one or two tokens, by bisection between its largest and smallest score where a lane can
+// hold its share of the scores in registers.
 #include "gqa_common.cuh"
 
 namespace dsa {
 
 namespace {
 
-constexpr int kTokTile = 8;      // tokens per block of threads in the prompt shape
-constexpr int kOneWarps = 16;    // warps in the one-token shape
+constexpr int kTileWarps = 16;   // warps in the tile shape
+constexpr int kOneWarps = 32;    // warps in the one-token shape
+constexpr int kHeld = 16;        // scores that a lane can hold in registers: rows of up to 512 blocks
 
 // The n_sel largest of nv keys (n_sel < nv), ties to the lower index, ascending into out.
 // NW warps take part; scr: 256 + 2 * NW + 4 ints.
@@ -109,18 +113,26 @@ __device__ __forceinline__ void pool_query(const GqaSelectArgs& A, int t, int kv
   constexpr int V = D / 32;
   const __nv_bfloat16* row = A.q + (int64_t)t * A.q_stride + (int64_t)kvh * A.G * D + lane * V;
   float x[V] = {};
-  for (int h = 0; h < A.G; ++h) {
-    uint32_t w[V / 2];
-    if constexpr (V == 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + h * D));
-      w[0] = v.x, w[1] = v.y;
-    } else {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(row + h * D));
+  for (int h0 = 0; h0 < A.G; h0 += 8) {          // (eight heads' loads in flight)
+    uint32_t w[8][V / 2];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      if (h0 + h >= A.G) continue;
+      if constexpr (V == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + (h0 + h) * D));
+        w[h][0] = v.x, w[h][1] = v.y;
+      } else {
+        w[h][0] = __ldg(reinterpret_cast<const uint32_t*>(row + (h0 + h) * D));
+      }
     }
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      x[2 * j] = h ? __fadd_rn(x[2 * j], bf16_lo(w[j])) : bf16_lo(w[j]);
-      x[2 * j + 1] = h ? __fadd_rn(x[2 * j + 1], bf16_hi(w[j])) : bf16_hi(w[j]);
+    for (int h = 0; h < 8; ++h) {
+      if (h0 + h >= A.G) continue;
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        x[2 * j] = h0 + h ? __fadd_rn(x[2 * j], bf16_lo(w[h][j])) : bf16_lo(w[h][j]);
+        x[2 * j + 1] = h0 + h ? __fadd_rn(x[2 * j + 1], bf16_hi(w[h][j])) : bf16_hi(w[h][j]);
+      }
     }
   }
   float u = 0.f;
@@ -134,17 +146,23 @@ __device__ __forceinline__ void pool_query(const GqaSelectArgs& A, int t, int kv
   }
 }
 
-// Keys of 32 blocks c0..c0+31 of request b for the tokens [w0, w1) of the tile; the whole
-// warp. keys + w * stride receives token w's.
+// The key that block c of nv is ranked by.
+__device__ __forceinline__ uint32_t score_key(const GqaSelectArgs& A, float s, int c, int nv, int page) {
+  if (c < A.n_first || c >= nv - A.n_last) return 0xFFFFFFFFu;
+  return page < 0 ? 0u : s == s ? max(orderable_key(s), 2u) : 1u;
+}
+
+// Keys of 32 blocks c0..c0+31, by the whole warp; page: the lane's block's, or -1.
 template <int D>
-__device__ __forceinline__ void score_blocks(const GqaSelectArgs& A, int b, int kvh, int c0, int nv_max, int w0, int w1,
-                                             const uint8_t* codes, const int* nv, uint32_t* keys, int stride, int lane) {
+__device__ __forceinline__ void score_blocks(const GqaSelectArgs& A, int kvh, int c0, int nv, int page,
+                                             const uint8_t* codes, uint32_t* keys, int lane) {
   constexpr int kLpb = D / 16;                   // lanes to a block's mean, 16 bytes each
   const int sub = lane % kLpb, grp = lane / kLpb;
   const int c = c0 + lane;
-  const int page = c < nv_max ? gqa_page(A.g, b, c) : -1;
-  if (c < nv_max && page < 0) record_error(A.err, kDevBadIndex);
+  if (c < nv && page < 0) record_error(A.err, kDevBadIndex);
   const float scale = page >= 0 ? __ldg(A.c.k_mean_scale + (int64_t)page * A.c.Hkv + kvh) : 0.f;
+  int v[kLpb];
+  const uint4 q = *reinterpret_cast<const uint4*>(codes + sub * 16);
   uint4 mean[kLpb];
 #pragma unroll
   for (int j = 0; j < kLpb; ++j) {
@@ -152,37 +170,98 @@ __device__ __forceinline__ void score_blocks(const GqaSelectArgs& A, int b, int 
     mean[j] = p >= 0 ? __ldg(reinterpret_cast<const uint4*>(A.c.k_mean + ((int64_t)p * A.c.Hkv + kvh) * D) + sub)
                      : make_uint4(0, 0, 0, 0);
   }
-  for (int w = w0; w < w1; ++w) {
-    if (c0 >= nv[w]) continue;                   // (uniform)
-    const uint4 q = *reinterpret_cast<const uint4*>(codes + w * D + sub * 16);
-    int v[kLpb];
 #pragma unroll
-    for (int j = 0; j < kLpb; ++j) {
-      v[j] = __dp4a((int)mean[j].x, (int)q.x, 0);
-      v[j] = __dp4a((int)mean[j].y, (int)q.y, v[j]);
-      v[j] = __dp4a((int)mean[j].z, (int)q.z, v[j]);
-      v[j] = __dp4a((int)mean[j].w, (int)q.w, v[j]);
-    }
-    // sums over the lanes of a block, lane `sub` keeping the group's block `sub`
+  for (int j = 0; j < kLpb; ++j) {
+    v[j] = __dp4a((int)mean[j].x, (int)q.x, 0);
+    v[j] = __dp4a((int)mean[j].y, (int)q.y, v[j]);
+    v[j] = __dp4a((int)mean[j].z, (int)q.z, v[j]);
+    v[j] = __dp4a((int)mean[j].w, (int)q.w, v[j]);
+  }
+  // sums over the lanes of a block, lane `sub` keeping the group's block `sub`
 #pragma unroll
-    for (int o = kLpb / 2; o > 0; o >>= 1) {
-      const bool up = (sub & o) != 0;
+  for (int o = kLpb / 2; o > 0; o >>= 1) {
+    const bool up = (sub & o) != 0;
 #pragma unroll
-      for (int j = 0; j < kLpb / 2; ++j) {
-        if (j < o) {
-          const int keep = up ? v[j + o] : v[j], send = up ? v[j] : v[j + o];
-          v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
+    for (int j = 0; j < kLpb / 2; ++j) {
+      if (j < o) {
+        const int keep = up ? v[j + o] : v[j], send = up ? v[j] : v[j + o];
+        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
       }
     }
-    if (c < nv[w]) {
-      const float s = __fmul_rn((float)v[0], scale);
-      uint32_t key = s == s ? max(orderable_key(s), 2u) : 1u;
-      if (page < 0) key = 0u;
-      if (c < A.n_first || c >= nv[w] - A.n_last) key = 0xFFFFFFFFu;
-      keys[w * stride + c] = key;
+  }
+  if (c < nv) keys[c] = score_key(A, __fmul_rn((float)v[0], scale), c, nv, page);
+}
+
+// The same choice by one warp, for nv <= 32 * kHeld: the keys of the lane's blocks lane, lane +
+// 32, ... in registers, the smallest key taken found by bisection. kForced keys are all taken.
+constexpr uint32_t kForced = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float key_value(uint32_t k) {   // inverse of orderable_key
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+template <int kHeld>
+__device__ __forceinline__ void choose_held(const uint32_t* keys, int nv, int n_sel, int* out, int lane) {
+  uint32_t k[kHeld];
+  uint32_t top = 0, low = kForced;
+  int forced = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = lane + 32 * i;
+    k[i] = c < nv ? keys[c] : 0u;                 // (a key of 0, a bad page's, ranks with what is not there: see below)
+    if (k[i] == kForced) ++forced;
+    else if (c < nv) top = max(top, k[i]), low = min(low, k[i]);
+  }
+  forced = __reduce_add_sync(0xffffffffu, forced);
+  top = __reduce_max_sync(0xffffffffu, top);
+  low = __reduce_min_sync(0xffffffffu, low);
+  // at least n_sel keys are >= lo, fewer than n_sel are >= hi; more: those >= hi
+  uint32_t lo = low, hi = top + 1u;
+  int more = forced;
+  bool exact = more == n_sel;
+  if (exact) lo = hi;
+  float flo = key_value(lo), fhi = key_value(top);
+  bool by_value = true;                           // halve the scores' range, later the keys'
+  while (!exact && hi - lo > 1u) {
+    uint32_t mid = lo + (hi - lo) / 2u;
+    if (by_value) {
+      const float fm = 0.5f * flo + 0.5f * fhi;
+      const uint32_t m = orderable_key(fm);
+      by_value = m > lo && m < hi;                // (also false for what is no number)
+      if (by_value) mid = m;
+    }
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) n += k[i] >= mid;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n >= n_sel) {
+      lo = mid, flo = key_value(mid);
+      exact = n == n_sel;
+    } else {
+      hi = mid, fhi = key_value(mid);
+      more = n;
     }
   }
+  // keys above lo, and the first of those equal to it
+  int need = exact ? INT32_MAX : n_sel - more, above = 0, equal = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    if (32 * i >= nv) break;
+    const bool there = lane + 32 * i < nv;
+    const bool a = there && k[i] > lo, e = there && k[i] == lo;
+    const unsigned ma = __ballot_sync(0xffffffffu, a), me = __ballot_sync(0xffffffffu, e);
+    const unsigned below = (1u << lane) - 1u;
+    const int eq = equal + __popc(me & below);
+    if (a || (e && eq < need)) out[above + __popc(ma & below) + min(eq, need)] = lane + 32 * i;
+    above += __popc(ma);
+    equal += __popc(me);
+  }
+}
+
+// Four int8 codes as f16 pairs: (byte 0, byte 1) and (byte 2, byte 3).
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // A token's list where nothing has to be chosen: all of its nv <= n_sel blocks.
@@ -190,74 +269,169 @@ __device__ __forceinline__ void list_all(int* out, int nv, int n_sel, int at, in
   for (int i = at; i < n_sel; i += step) out[i] = i < nv ? i : -1;
 }
 
-template <int D, int TQ, int NW>
-__global__ void __launch_bounds__(32 * NW) gqa_select_kernel(const GqaSelectArgs A, int stride) {
+// One token.
+template <int D>
+__global__ void __launch_bounds__(32 * kOneWarps) gqa_select_one_kernel(const GqaSelectArgs A) {
   extern __shared__ __align__(16) uint8_t select_smem[];
-  __shared__ __align__(16) uint8_t s_codes[TQ][D];
-  __shared__ int s_nv[TQ], s_b[TQ], s_row[TQ];
-  constexpr int kSelWarps = TQ == 1 ? NW : 1;               // warps that select for one token
-  __shared__ int s_scr[TQ][256 + 4 + 2 * kSelWarps];
+  __shared__ __align__(16) uint8_t s_codes[D];
+  __shared__ int s_scr[256 + 4 + 2 * kOneWarps];
   uint32_t* keys = reinterpret_cast<uint32_t*>(select_smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = blockIdx.x * TQ, kvh = blockIdx.y;
+  const int t = blockIdx.x, kvh = blockIdx.y;
+  bool bad;
+  const GqaToken k = gqa_token_warp(A.g, t, &bad);
+  if (bad && threadIdx.x == 0) record_error(A.err, kDevBadIndex);
+  if (k.row == kRowPadding) return;
+  int* out = A.blocks + ((int64_t)t * A.c.Hkv + kvh) * A.n_sel;
+  const int nv = k.row == kRowSees ? (k.pos >> 6) + 1 : 0;
+  if (nv <= A.n_sel) {
+    list_all(out, nv, A.n_sel, threadIdx.x, 32 * kOneWarps);
+    return;
+  }
+  if (warp == 0) pool_query<D>(A, t, kvh, s_codes, lane);
+  // (the pages are looked up meanwhile)
+  int c0 = warp * 32, page = c0 + lane < nv ? gqa_page(A.g, k.b, c0 + lane) : -1;
+  __syncthreads();
+  for (; c0 < nv; c0 += kOneWarps * 32) {
+    const int next = c0 + kOneWarps * 32 + lane;
+    const int after = next < nv ? gqa_page(A.g, k.b, next) : -1;
+    score_blocks<D>(A, kvh, c0, nv, page, s_codes, keys, lane);
+    page = after;
+  }
+  __syncthreads();
+  choose<kOneWarps>(keys, nv, A.n_sel, out, s_scr, warp, lane);
+}
 
-  if (warp < TQ) {
-    const int t = t0 + warp;
+// TQ consecutive tokens (a multiple of 8); stride: words between tokens' keys.
+template <int D, int TQ>
+__global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(const GqaSelectArgs A, int stride) {
+  constexpr int kSteps = D / 16, kNT = TQ / 8;
+  extern __shared__ __align__(16) uint8_t select_smem[];
+  __shared__ __align__(16) uint8_t s_codes[TQ][D];
+  __shared__ uint2 s_qf[kNT][kSteps][32];
+  __shared__ int s_nv[TQ], s_b[TQ], s_row[TQ];
+  __shared__ int s_scr[TQ][256 + 4 + 2];
+  uint32_t* keys = reinterpret_cast<uint32_t*>(select_smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = lane & 3, lrow = lane >> 2;
+  const int t0 = blockIdx.x * TQ, kvh = blockIdx.y;
+  for (int w = warp; w < TQ; w += kTileWarps) {
+    const int t = t0 + w;
     GqaToken k{0, -1, kRowPadding};
     bool bad = false;
     if (t < A.g.T) k = gqa_token_warp(A.g, t, &bad);
+    const int nv = k.row == kRowSees ? (k.pos >> 6) + 1 : 0;
     if (lane == 0) {
       if (bad) record_error(A.err, kDevBadIndex);
-      s_row[warp] = k.row;
-      s_b[warp] = k.b;
-      s_nv[warp] = k.row == kRowSees ? (k.pos >> 6) + 1 : 0;
+      s_row[w] = k.row;
+      s_b[w] = k.b;
+      s_nv[w] = nv;
     }
-    if (k.row == kRowSees && (k.pos >> 6) + 1 > A.n_sel) pool_query<D>(A, t, kvh, s_codes[warp], lane);
+    if (nv > A.n_sel) {
+      pool_query<D>(A, t, kvh, s_codes[w], lane);
+    } else {
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) s_codes[w][lane * (D / 32) + j] = 0;
+    }
   }
   __syncthreads();
-  // scores: runs of tokens of one request
+  // the tokens' codes as B fragments: token lrow of each eight, columns q*D/4 ..
+  for (int i = warp; i < kNT * kSteps; i += kTileWarps) {
+    const int n = i / kSteps, k = i % kSteps;
+    uint2 f;
+    codes_f16<true>(*reinterpret_cast<const uint32_t*>(&s_codes[8 * n + lrow][q * (D / 4) + 4 * k]), f.x, f.y);
+    s_qf[n][k][lane] = f;
+  }
+  __syncthreads();
+  // scores: runs of tokens of one request, 16 blocks a warp and step
   for (int w0 = 0; w0 < TQ;) {
     int w1 = w0 + 1, most = s_nv[w0];
     while (w1 < TQ && s_b[w1] == s_b[w0]) {
       most = max(most, s_nv[w1]);
       ++w1;
     }
-    if (most > A.n_sel)
-      for (int c0 = warp * 32; c0 < most; c0 += NW * 32)
-        score_blocks<D>(A, s_b[w0], kvh, c0, most, w0, w1, &s_codes[0][0], s_nv, keys, stride, lane);
+    if (most > A.n_sel) {
+      const int b = s_b[w0];
+      for (int c0 = 16 * warp; c0 < most; c0 += 16 * kTileWarps) {
+        uint32_t a[kSteps][4];
+        float scale[2];
+        int page[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = c0 + lrow + 8 * h;
+          page[h] = c < most ? gqa_page(A.g, b, c) : -1;
+          if (c < most && page[h] < 0) record_error(A.err, kDevBadIndex);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t tile = (int64_t)max(page[h], 0) * A.c.Hkv + kvh;
+          scale[h] = __ldg(A.c.k_mean_scale + tile);
+          const uint4* src = reinterpret_cast<const uint4*>(A.c.k_mean + tile * D + q * (D / 4));
+#pragma unroll
+          for (int k = 0; k < kSteps; k += 4) {
+            const uint4 v = __ldg(src + k / 4);
+            codes_f16<true>(v.x, a[k][h], a[k][2 + h]);
+            codes_f16<true>(v.y, a[k + 1][h], a[k + 1][2 + h]);
+            codes_f16<true>(v.z, a[k + 2][h], a[k + 2][2 + h]);
+            codes_f16<true>(v.w, a[k + 3][h], a[k + 3][2 + h]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kNT; ++i) {
+          float s[4] = {};
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const uint2 f = s_qf[i][k][lane];
+            mma_f16(s, a[k], f.x, f.y);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int w = 8 * i + 2 * q + (j & 1), c = c0 + lrow + 8 * (j >> 1);
+            if (w < w0 || w >= w1 || c >= s_nv[w]) continue;
+            keys[w * stride + c] = score_key(A, __fmul_rn(s[j], scale[j >> 1]), c, s_nv[w], page[j >> 1]);
+          }
+        }
+      }
+    }
     w0 = w1;
   }
   __syncthreads();
-  if (TQ == 1) {
-    if (s_row[0] == kRowPadding) return;
-    int* out = A.blocks + ((int64_t)t0 * A.c.Hkv + kvh) * A.n_sel;
-    if (s_nv[0] <= A.n_sel) list_all(out, s_nv[0], A.n_sel, threadIdx.x, 32 * NW);
-    else choose<kSelWarps>(keys, s_nv[0], A.n_sel, out, s_scr[0], warp, lane);
-  } else if (warp < TQ && s_row[warp] != kRowPadding) {
-    int* out = A.blocks + ((int64_t)(t0 + warp) * A.c.Hkv + kvh) * A.n_sel;
-    if (s_nv[warp] <= A.n_sel) list_all(out, s_nv[warp], A.n_sel, lane, 32);
-    else choose<kSelWarps>(keys + warp * stride, s_nv[warp], A.n_sel, out, s_scr[warp], warp % kSelWarps, lane);
+  for (int w = warp; w < TQ; w += kTileWarps) {
+    if (s_row[w] == kRowPadding) continue;
+    int* out = A.blocks + ((int64_t)(t0 + w) * A.c.Hkv + kvh) * A.n_sel;
+    if (s_nv[w] <= A.n_sel) list_all(out, s_nv[w], A.n_sel, lane, 32);
+    else if (s_nv[w] <= 32 * kHeld / 2) choose_held<kHeld / 2>(keys + w * stride, s_nv[w], A.n_sel, out, lane);
+    else if (s_nv[w] <= 32 * kHeld) choose_held<kHeld>(keys + w * stride, s_nv[w], A.n_sel, out, lane);
+    else choose<1>(keys + w * stride, s_nv[w], A.n_sel, out, s_scr[w], 0, lane);
+    __syncwarp();
   }
+}
+
+template <int D, int TQ>
+cudaError_t launch_tile(const GqaSelectArgs& A, int stride, cudaStream_t st) {
+  const size_t bytes = (size_t)stride * 4 * TQ;
+  auto kern = gqa_select_tile_kernel<D, TQ>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, 98304, allowed);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((A.g.T + TQ - 1) / TQ, A.c.Hkv), 32 * kTileWarps, bytes, st>>>(A, stride);
+  return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch(const GqaSelectArgs& A, int num_sms, cudaStream_t st) {
-  const int nb = (A.g.max_seq_len + kPage - 1) / kPage, stride = (nb + 3) / 4 * 4;
-  const size_t tile = (size_t)stride * 4 * kTokTile;
+  const int nb = (A.g.max_seq_len + kPage - 1) / kPage;
+  const int stride = (nb + 15) / 16 * 16 + 4;     // (a warp's 8 x 8 keys then fall into 32 banks)
   // Tiles of tokens pay once they alone fill the SMs and their scores fit beside others'.
-  const bool tiles = (int64_t)A.g.T * A.c.Hkv >= (int64_t)2 * kTokTile * num_sms && A.g.T / A.g.B >= kTokTile && tile <= 98304;
-  if (tiles) {
-    auto kern = gqa_select_kernel<D, kTokTile, kTokTile>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile);
-    if (e != cudaSuccess) return e;
-    kern<<<dim3((A.g.T + kTokTile - 1) / kTokTile, A.c.Hkv), 32 * kTokTile, tile, st>>>(A, stride);
-  } else {
-    auto kern = gqa_select_kernel<D, 1, kOneWarps>;
-    const size_t bytes = (size_t)stride * 4;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-    kern<<<dim3(A.g.T, A.c.Hkv), 32 * kOneWarps, bytes, st>>>(A, stride);
-  }
+  const int64_t rows = (int64_t)A.g.T * A.c.Hkv;
+  const bool runs = A.g.T / A.g.B >= 8;
+  if (runs && rows >= (int64_t)16 * num_sms && (size_t)stride * 4 * 16 <= 98304) return launch_tile<D, 16>(A, stride, st);
+  if (runs && rows >= (int64_t)16 * num_sms && (size_t)stride * 4 * 8 <= 98304) return launch_tile<D, 8>(A, stride, st);
+  auto kern = gqa_select_one_kernel<D>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, 131072, allowed);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(A.g.T, A.c.Hkv), 32 * kOneWarps, (size_t)nb * 4, st>>>(A);
   return cudaGetLastError();
 }
 

@@ -156,7 +156,6 @@ struct GqaAppendArgs {
   __nv_bfloat16* q_out;         // [T, G * Hkv, D]
   int64_t k_stride, v_stride, q_stride;
   int G;                        // query heads per key head
-  int parts;                    // blocks of threads per (block, key head): the query heads are spread over them
   int rope_dim;
   const float* rope_cos;
   const float* rope_sin;
