@@ -208,7 +208,7 @@ __device__ __forceinline__ void rotate_queries(const GqaAppendArgs& A, int index
 
 // Blocks of threads below kv_blocks own (slot, key head)s, the others query rows.
 template <int D, bool I8, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) gqa_append_kernel(const GqaAppendArgs A, int slots, int kv_blocks) {
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 16 ? 2 : 4) gqa_append_kernel(const GqaAppendArgs A, int slots, int kv_blocks) {
   constexpr int V = D / 32, kTok = kPage / kWarps;   // kTok: new tokens of a block per warp
   __shared__ float s_amax[2][kWarps];
   __shared__ float s_sum[D];

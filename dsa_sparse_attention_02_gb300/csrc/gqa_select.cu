@@ -107,17 +107,17 @@ __device__ __forceinline__ void choose(const uint32_t* keys, int nv, int n_sel, 
   }
 }
 
-// The query token's pooled int8 code of key head kvh (D bytes at dst), by one warp.
+// The query token's pooled int8 code of key head kvh (D bytes at dst), by one warp; the first
+// eight heads' loads are issued at construction, to pass under other lookups.
 template <int D>
-__device__ __forceinline__ void pool_query(const GqaSelectArgs& A, int t, int kvh, uint8_t* dst, int lane) {
-  constexpr int V = D / 32;
-  const __nv_bfloat16* row = A.q + (int64_t)t * A.q_stride + (int64_t)kvh * A.G * D + lane * V;
-  float x[V] = {};
-  for (int h0 = 0; h0 < A.G; h0 += 8) {          // (eight heads' loads in flight)
-    uint32_t w[8][V / 2];
+struct PooledQuery {
+  static constexpr int V = D / 32;
+  const __nv_bfloat16* row;
+  uint32_t w[8][V / 2];
+  __device__ __forceinline__ void load(int G, int h0) {
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
-      if (h0 + h >= A.G) continue;
+      if (h0 + h >= G) continue;
       if constexpr (V == 4) {
         const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + (h0 + h) * D));
         w[h][0] = v.x, w[h][1] = v.y;
@@ -125,26 +125,36 @@ __device__ __forceinline__ void pool_query(const GqaSelectArgs& A, int t, int kv
         w[h][0] = __ldg(reinterpret_cast<const uint32_t*>(row + (h0 + h) * D));
       }
     }
+  }
+  __device__ __forceinline__ PooledQuery(const GqaSelectArgs& A, int t, int kvh, int lane)
+      : row(A.q + (int64_t)t * A.q_stride + (int64_t)kvh * A.G * D + lane * V) {
+    load(A.G, 0);
+  }
+  __device__ __forceinline__ void finish(int G, uint8_t* dst, int lane) {
+    float x[V] = {};
+    for (int h0 = 0; h0 < G; h0 += 8) {
+      if (h0) load(G, h0);
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      if (h0 + h >= A.G) continue;
+      for (int h = 0; h < 8; ++h) {
+        if (h0 + h >= G) continue;
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        x[2 * j] = h0 + h ? __fadd_rn(x[2 * j], bf16_lo(w[h][j])) : bf16_lo(w[h][j]);
-        x[2 * j + 1] = h0 + h ? __fadd_rn(x[2 * j + 1], bf16_hi(w[h][j])) : bf16_hi(w[h][j]);
+        for (int j = 0; j < V / 2; ++j) {
+          x[2 * j] = h0 + h ? __fadd_rn(x[2 * j], bf16_lo(w[h][j])) : bf16_lo(w[h][j]);
+          x[2 * j + 1] = h0 + h ? __fadd_rn(x[2 * j + 1], bf16_hi(w[h][j])) : bf16_hi(w[h][j]);
+        }
       }
     }
-  }
-  float u = 0.f;
+    float u = 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) u = fmaxf(u, fabsf(x[j]));
-  u = __fdiv_rn(warp_max(u), 127.f);
+    for (int j = 0; j < V; ++j) u = fmaxf(u, fabsf(x[j]));
+    u = __fdiv_rn(warp_max(u), 127.f);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = u > 0.f ? max(-127, min(127, __float2int_rn(__fdiv_rn(x[j], u)))) : 0;
-    dst[lane * V + j] = (uint8_t)(c & 0xFF);
+    for (int j = 0; j < V; ++j) {
+      const int c = u > 0.f ? max(-127, min(127, __float2int_rn(__fdiv_rn(x[j], u)))) : 0;
+      dst[lane * V + j] = (uint8_t)(c & 0xFF);
+    }
   }
-}
+};
 
 // The key that block c of nv is ranked by.
 __device__ __forceinline__ uint32_t score_key(const GqaSelectArgs& A, float s, int c, int nv, int page) {
@@ -278,6 +288,10 @@ __global__ void __launch_bounds__(32 * kOneWarps) gqa_select_one_kernel(const Gq
   uint32_t* keys = reinterpret_cast<uint32_t*>(select_smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x, kvh = blockIdx.y;
+  if (warp == kOneWarps - 1) {                    // (meanwhile the others look the token up)
+    PooledQuery<D> pooled(A, t, kvh, lane);
+    pooled.finish(A.G, s_codes, lane);
+  }
   bool bad;
   const GqaToken k = gqa_token_warp(A.g, t, &bad);
   if (bad && threadIdx.x == 0) record_error(A.err, kDevBadIndex);
@@ -288,8 +302,6 @@ __global__ void __launch_bounds__(32 * kOneWarps) gqa_select_one_kernel(const Gq
     list_all(out, nv, A.n_sel, threadIdx.x, 32 * kOneWarps);
     return;
   }
-  if (warp == 0) pool_query<D>(A, t, kvh, s_codes, lane);
-  // (the pages are looked up meanwhile)
   int c0 = warp * 32, page = c0 + lane < nv ? gqa_page(A.g, k.b, c0 + lane) : -1;
   __syncthreads();
   for (; c0 < nv; c0 += kOneWarps * 32) {
@@ -315,26 +327,56 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(con
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int q = lane & 3, lrow = lane >> 2;
   const int t0 = blockIdx.x * TQ, kvh = blockIdx.y;
-  for (int w = warp; w < TQ; w += kTileWarps) {
-    const int t = t0 + w;
+  static_assert(TQ <= kTileWarps, "a warp per token");
+  if (warp < TQ) {
+    const int t = t0 + warp;
+    PooledQuery<D> pooled(A, min(t, A.g.T - 1), kvh, lane);
     GqaToken k{0, -1, kRowPadding};
     bool bad = false;
     if (t < A.g.T) k = gqa_token_warp(A.g, t, &bad);
-    const int nv = k.row == kRowSees ? (k.pos >> 6) + 1 : 0;
     if (lane == 0) {
       if (bad) record_error(A.err, kDevBadIndex);
-      s_row[w] = k.row;
-      s_b[w] = k.b;
-      s_nv[w] = nv;
+      s_row[warp] = k.row;
+      s_b[warp] = k.b;
+      s_nv[warp] = k.row == kRowSees ? (k.pos >> 6) + 1 : 0;
     }
-    if (nv > A.n_sel) {
-      pool_query<D>(A, t, kvh, s_codes[w], lane);
-    } else {
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) s_codes[w][lane * (D / 32) + j] = 0;
-    }
+    pooled.finish(A.G, s_codes[warp], lane);
   }
   __syncthreads();
+  // 16 blocks' means and scales of a request, as they are
+  struct Means {
+    uint4 v[2][D / 64];
+    float scale[2];
+    int page[2];
+  };
+  auto means = [&](Means& m, int b, int c0, int most) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + lrow + 8 * h;
+      m.page[h] = c < most ? gqa_page(A.g, b, c) : -1;
+      if (c < most && m.page[h] < 0) record_error(A.err, kDevBadIndex);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t tile = (int64_t)max(m.page[h], 0) * A.c.Hkv + kvh;
+      m.scale[h] = __ldg(A.c.k_mean_scale + tile);
+      const uint4* src = reinterpret_cast<const uint4*>(A.c.k_mean + tile * D + q * (D / 4));
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k) m.v[h][k] = __ldg(src + k);
+    }
+  };
+  // the first run of tokens of one request: its first slice is loaded under what follows
+  int w0 = 0, w1, most;
+  auto run = [&]() {
+    w1 = w0 + 1, most = s_nv[w0];
+    while (w1 < TQ && s_b[w1] == s_b[w0]) {
+      most = max(most, s_nv[w1]);
+      ++w1;
+    }
+  };
+  run();
+  Means m;
+  if (most > A.n_sel && 16 * warp < most) means(m, s_b[0], 16 * warp, most);
   // the tokens' codes as B fragments: token lrow of each eight, columns q*D/4 ..
   for (int i = warp; i < kNT * kSteps; i += kTileWarps) {
     const int n = i / kSteps, k = i % kSteps;
@@ -343,39 +385,22 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(con
     s_qf[n][k][lane] = f;
   }
   __syncthreads();
-  // scores: runs of tokens of one request, 16 blocks a warp and step
-  for (int w0 = 0; w0 < TQ;) {
-    int w1 = w0 + 1, most = s_nv[w0];
-    while (w1 < TQ && s_b[w1] == s_b[w0]) {
-      most = max(most, s_nv[w1]);
-      ++w1;
-    }
+  // scores, 16 blocks a warp and step
+  for (;;) {
     if (most > A.n_sel) {
-      const int b = s_b[w0];
       for (int c0 = 16 * warp; c0 < most; c0 += 16 * kTileWarps) {
+        if (w0 > 0 || c0 > 16 * warp) means(m, s_b[w0], c0, most);
         uint32_t a[kSteps][4];
-        float scale[2];
-        int page[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = c0 + lrow + 8 * h;
-          page[h] = c < most ? gqa_page(A.g, b, c) : -1;
-          if (c < most && page[h] < 0) record_error(A.err, kDevBadIndex);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t tile = (int64_t)max(page[h], 0) * A.c.Hkv + kvh;
-          scale[h] = __ldg(A.c.k_mean_scale + tile);
-          const uint4* src = reinterpret_cast<const uint4*>(A.c.k_mean + tile * D + q * (D / 4));
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int k = 0; k < kSteps; k += 4) {
-            const uint4 v = __ldg(src + k / 4);
+            const uint4 v = m.v[h][k / 4];
             codes_f16<true>(v.x, a[k][h], a[k][2 + h]);
             codes_f16<true>(v.y, a[k + 1][h], a[k + 1][2 + h]);
             codes_f16<true>(v.z, a[k + 2][h], a[k + 2][2 + h]);
             codes_f16<true>(v.w, a[k + 3][h], a[k + 3][2 + h]);
           }
-        }
 #pragma unroll
         for (int i = 0; i < kNT; ++i) {
           float s[4] = {};
@@ -388,12 +413,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(con
           for (int j = 0; j < 4; ++j) {
             const int w = 8 * i + 2 * q + (j & 1), c = c0 + lrow + 8 * (j >> 1);
             if (w < w0 || w >= w1 || c >= s_nv[w]) continue;
-            keys[w * stride + c] = score_key(A, __fmul_rn(s[j], scale[j >> 1]), c, s_nv[w], page[j >> 1]);
+            keys[w * stride + c] = score_key(A, __fmul_rn(s[j], m.scale[j >> 1]), c, s_nv[w], m.page[j >> 1]);
           }
         }
       }
     }
     w0 = w1;
+    if (w0 >= TQ) break;
+    run();
   }
   __syncthreads();
   for (int w = warp; w < TQ; w += kTileWarps) {
