@@ -251,15 +251,28 @@ __device__ __forceinline__ void choose_held(const uint32_t* keys, int nv, int n_
       more = n;
     }
   }
+  const unsigned below = (1u << lane) - 1u;
+  if (exact) {                                    // the keys from lo on (the usual end)
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (32 * i >= nv) break;
+      const bool in = lane + 32 * i < nv && k[i] >= lo;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (in) out[n + __popc(m & below)] = lane + 32 * i;
+      n += __popc(m);
+    }
+    return;
+  }
   // keys above lo, and the first of those equal to it
-  int need = exact ? INT32_MAX : n_sel - more, above = 0, equal = 0;
+  const int need = n_sel - more;
+  int above = 0, equal = 0;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     if (32 * i >= nv) break;
     const bool there = lane + 32 * i < nv;
     const bool a = there && k[i] > lo, e = there && k[i] == lo;
     const unsigned ma = __ballot_sync(0xffffffffu, a), me = __ballot_sync(0xffffffffu, e);
-    const unsigned below = (1u << lane) - 1u;
     const int eq = equal + __popc(me & below);
     if (a || (e && eq < need)) out[above + __popc(ma & below) + min(eq, need)] = lane + 32 * i;
     above += __popc(ma);
