@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
   using S = TileShape<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kStages], s_empty[kStages];
-  __shared__ uint64_t s_sfull[2][2], s_pfull[2][2],   // [tile][S buffer]
-       s_odone[2], s_qfull[2], s_drain[2];
+  __shared__ uint64_t s_sfull[2][2], s_pfull[2][2], s_odone[2][2],   // [tile][unit % 2]
+       s_qfull[2], s_drain[2];
   __shared__ Unit s_unit[kStages];
   __shared__ int s_nan[I8 ? 1 : kNanSlots][D];
   __shared__ int64_t s_begin, s_end, s_base, s_total;
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       for (int k = 0; k < 2; ++k) {
         mbar_init(smem_u32(&s_sfull[i][k]), 1);
         mbar_init(smem_u32(&s_pfull[i][k]), 4);
+        mbar_init(smem_u32(&s_odone[i][k]), 1);
       }
-      mbar_init(smem_u32(&s_odone[i]), 1);
       mbar_init(smem_u32(&s_qfull[i]), 4);
       mbar_init(smem_u32(&s_drain[i]), 1);
     }
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
 #pragma unroll
           for (int k = 0; k < kPage / 16; ++k)
             mma_f16_ts(tcol + kOCol, p + 8 * k, desc_add(vd, k * 2048), idesc_o, k != 0 ? 1u : fresh ^ 1u);
-          mma_commit(smem_u32(&s_odone[i]));
+          mma_commit(smem_u32(&s_odone[i][n & 1]));
           mma_commit(smem_u32(&s_empty[before]));
         }
       }
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
         M = Mn;
         l *= keep;
         if (!(x.flags & kFirst)) {                 // O so far, once its last product is done
-          if (!warp_wait(&s_odone[i], (n - 1) & 1, abort, A.err)) break;
+          if (!warp_wait(&s_odone[i][(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err)) break;
           tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < D; k += 16) {
@@ -582,7 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       if (!(x.flags & kLast)) continue;
 
       // ---- the segment's outputs, or its part
-      if (!warp_wait(&s_odone[i], n & 1, abort, A.err)) break;
+      // (one barrier for every second unit: the warps of a tile run up to a unit apart, so the
+      // products of unit n - 1 may still be to come, and a single barrier's parity would let n pass)
+      if (!warp_wait(&s_odone[i][n & 1], (n >> 1) & 1, abort, A.err)) break;
       tc_fence_after();
       const int pos = x.rel + tok + end.c * kPage;
       const bool none = l == 0.f;

@@ -547,3 +547,163 @@ def test_no_work():
     _lib.dsa_block_select(geom, d.cache, none, 2, 0, 1, torch.zeros(0, 2, 2, dtype=torch.int32, device=DEV), ws)
     _lib.dsa_gqa_attend_blocks(geom, d.cache, none, torch.zeros(0, 2, 2, dtype=torch.int32, device=DEV), 0.1, none, None, ws)
     assert _lib.dsa_get_error(ws) == 0
+
+
+# ---------------------------------------------------------------- batches and sizes at the edges
+
+def test_attend_rows_between_warps_and_tiles():
+    """33 to 64 query rows per request and key head under long tables (the declared lengths
+    choose the kernel), with short contexts in them."""
+    for dtype in (E4, I8):
+        c = ref.Case([700, 90, 6], [6, 4, 5], 16, 2, 128, dtype, seed=17, pad=2, max_len=64 * 2600)
+        check_attend(Dev(c), 0.09)
+
+
+@pytest.mark.parametrize("dtype", [E4, I8], ids=["e4m3", "i8"])
+@pytest.mark.parametrize("lens,new,H,Hkv,D", [
+    ([1558, 143], [75, 3], 40, 8, 128), ([700, 249, 60], [40, 90, 8], 14, 2, 64),
+    ([90 + 7 * i % 170 for i in range(70)], [1 + 3 * i % 10 for i in range(70)], 21, 3, 128)])
+def test_attend_sharp_softmax(lens, new, H, Hkv, D, dtype):
+    """Weights on few keys: the running maximum moves often and at different units for the
+    rows of one tile, so that its warps drift apart. The same bits every time."""
+    c = ref.Case(lens, new, H, Hkv, D, dtype, seed=71, pad=1, max_len=max(lens) if len(lens) < 9 else 64 * 300)
+    d = Dev(c)
+    a, la = check_attend(d, 0.5)
+    for _ in range(5):
+        b, lb = d.attend(0.5)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("lens,new,H,Hkv,D", [
+    ([900] + [70 + 5 * i for i in range(40)], [500] + [1] * 40, 16, 2, 128),     # a prompt among decoding requests
+    ([150] + [40 + i for i in range(120)], [100] + [1] * 120, 8, 1, 64),
+    ([33] * 700 + [200, 9], [0] * 700 + [3, 1], 4, 2, 64),                       # slots without tokens
+    ([0, 65, 0] * 200 + [130], [1, 0, 1] * 200 + [2], 2, 1, 128), ([65] * 2, [2] * 2, 128, 128, 64), ([70], [2], 2048, 128, 64)])
+def test_uneven_batches(lens, new, H, Hkv, D):
+    c = ref.Case(lens, new, H, Hkv, D, E4, seed=len(lens), pad=3)
+    d = Dev(c)
+    check_attend(d, D ** -0.5)
+    got = d.select(3, 1, 1)
+    assert _lib.dsa_get_error(d.ws) == 0
+    n = sum(new)
+    assert np.array_equal(got[:n].cpu().numpy(), ref.select(c, 3, 1, 1)[:n])
+    check_attend(d, D ** -0.5, blocks=got.cpu())
+
+
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_far_pages(new):
+    """Codes beyond 2^32 bytes: the same answers, bit for bit, as from a small cache."""
+    c = ref.Case([400, 130], [new, new], 16, 1, 64, E4, seed=14)
+    near, far = Dev(c), Dev(c)
+    P = 2 ** 20 + 4096
+    at = [(i + 1) * (P // c.P) - 1 for i in range(c.P)]
+    assert at[-1] * 64 * 64 > 2 ** 32
+    for name in ("k", "v", "k_scale", "v_scale", "k_mean", "k_mean_scale"):
+        x = getattr(near, name)
+        big = torch.empty((P,) + tuple(x.shape[1:]), dtype=x.dtype, device=DEV)
+        for i, p in enumerate(at):
+            big[p].view(torch.uint8).copy_(x[i].view(torch.uint8))
+        setattr(far, name, big)
+    bt = c.block_table.clone()
+    for i, p in enumerate(at):
+        bt[c.block_table == i] = p
+    far.block_table = bt.to(DEV)
+    far.geom = _lib.Geometry(far.seq_lens, far.cu_q, far.block_table, P, c.max_len, c.T)
+    far.cache = _lib.GqaCache(far.k, far.v, far.k_scale, far.v_scale, far.k_mean, far.k_mean_scale)
+    x = torch.randn(c.T, 18, 64, generator=c.gen).bfloat16().to(DEV)
+    got = []
+    for d in (near, far):
+        q = torch.zeros(c.T, 16, 64, dtype=torch.bfloat16, device=DEV)
+        ws = _lib.workspace(256, DEV)
+        _lib.dsa_gqa_append(d.geom, d.cache, x[:, 16:17], x[:, 17:], x[:, :16], q, 0, ws=ws)
+        sel = d.select(4, 1, 1)
+        a, la = d.attend(0.125)
+        b, lb = d.attend(0.125, sel)
+        assert _lib.dsa_get_error(ws) == 0 and _lib.dsa_get_error(d.ws) == 0
+        pages = list(range(c.P)) if d is near else at
+        held = [torch.stack([getattr(d, n)[p].view(torch.uint8) for p in pages]) for n in ("k", "v", "k_scale", "v_scale", "k_mean", "k_mean_scale")]
+        got.append([q, sel, a, la, b, lb] + held)
+    for u, w in zip(*got):
+        assert torch.equal(u, w)
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_many_rows(new):
+    """Queries and outputs of more than 2^32 elements: the first and the last request."""
+    H, Hkv, D, n = 64, 4, 128, 1
+    B = 2 ** 32 // (H * D * new) + 3
+    c = ref.Case([64], [new], H, Hkv, D, I8, seed=15)
+    d = Dev(c)
+    T = B * new
+    seq = torch.full((B,), 64, dtype=torch.int32, device=DEV)
+    cu = torch.arange(B + 1, dtype=torch.int32, device=DEV) * new
+    bt = d.block_table.expand(B, 1).contiguous()
+    geom = _lib.Geometry(seq, cu, bt, c.P, 64, T)
+    q = torch.zeros(T, H, D, dtype=torch.bfloat16, device=DEV)
+    q[:new], q[-new:] = d.q, d.q
+    out, lse = torch.full_like(q, 7.0), torch.full((T, H), 7.0, device=DEV)
+    r = ref.attend(c, 0.09)
+    bo, bl = ref.attend_bounds(r)
+    blocks = torch.full((T, Hkv, n), -9, dtype=torch.int32, device=DEV)
+    for listed in (False, True):
+        if listed:
+            ws = _lib.workspace(max(_lib.dsa_block_select_workspace_size(geom, d.cache, n),
+                                    _lib.dsa_gqa_attend_blocks_workspace_size(geom, d.cache, H, n)), DEV)
+            _lib.dsa_block_select(geom, d.cache, q, n, 0, 1, blocks, ws)
+            assert (blocks == 0).all()
+            _lib.dsa_gqa_attend_blocks(geom, d.cache, q, blocks, 0.09, out, lse, ws)
+        else:
+            ws = _lib.workspace(_lib.dsa_gqa_attend_workspace_size(geom, d.cache, H), DEV)
+            _lib.dsa_gqa_attend(geom, d.cache, q, 0.09, out, lse, ws)
+        assert _lib.dsa_get_error(ws) == 0
+        for part in (slice(0, new), slice(T - new, T)):
+            assert (np.abs(out[part].double().cpu().numpy() - r["out"]) <= bo).all()
+            assert (np.abs(lse[part].double().cpu().numpy() - r["lse"]) <= bl).all()
+        assert torch.isfinite(lse).all()
+        out.fill_(7.0), lse.fill_(7.0)
+
+
+def test_two_graphs_share_a_workspace():
+    """A decode step and a prompt's step, captured with one workspace and replayed in turn."""
+    a = Dev(ref.Case([700, 3000], [1, 1], 16, 2, 128, E4, seed=18))
+    b = Dev(ref.Case([300, 250], [200, 90], 16, 2, 128, I8, seed=19))
+    want = [x.attend(0.09) for x in (a, b)]
+    ws = _lib.workspace(max(_lib.dsa_gqa_attend_workspace_size(x.geom, x.cache, 16) for x in (a, b)), DEV)
+    graphs, got = [], []
+    for x in (a, b):
+        out, lse = torch.zeros_like(want[len(got)][0]), torch.zeros_like(want[len(got)][1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _lib.dsa_gqa_attend(x.geom, x.cache, x.q, 0.09, out, lse, ws)
+        graphs.append(g), got.append((out, lse))
+    for i in (0, 1, 1, 0, 1):
+        got[i][0].fill_(7.0), got[i][1].fill_(7.0)
+        graphs[i].replay()
+        assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
+    assert _lib.dsa_get_error(ws) == 0
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace of its own, over one cache."""
+    c = ref.Case([5000, 3000, 900], [1, 2, 1], 16, 2, 128, E4, seed=20)
+    d = Dev(c)
+    li = d.select(6, 1, 2)
+    want, listed = d.attend(0.09), d.attend(0.09, li)
+    size = max(_lib.dsa_gqa_attend_workspace_size(d.geom, d.cache, 16), _lib.dsa_gqa_attend_blocks_workspace_size(d.geom, d.cache, 16, 6))
+    wss = [_lib.workspace(size, DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (s, ws) in enumerate(zip(streams, wss)):
+            with torch.cuda.stream(s):
+                out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+                if i:
+                    _lib.dsa_gqa_attend_blocks(d.geom, d.cache, d.q, li, 0.09, out, lse, ws)
+                else:
+                    _lib.dsa_gqa_attend(d.geom, d.cache, d.q, 0.09, out, lse, ws)
+                got[i].append((out, lse))
+    torch.cuda.synchronize()
+    for i, right in enumerate((want, listed)):
+        assert all(torch.equal(o, right[0]) and torch.equal(l, right[1]) for o, l in got[i])
+        assert _lib.dsa_get_error(wss[i]) == 0
