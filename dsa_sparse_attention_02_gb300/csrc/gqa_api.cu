@@ -67,7 +67,8 @@ dsa_status_t attend(const dsa_geom_t* g, const dsa_gqa_cache_t* c, int H, const 
   dsa_status_t s = check_geom(g);
   if (s == DSA_OK) s = check_cache(c);
   if (s != DSA_OK) return s;
-  if (!heads_ok(c, H) || !std::isfinite(sm_scale) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
+  const float scale_log2 = sm_scale * 1.4426950408889634f;   // scores in powers of two
+  if (!heads_ok(c, H) || !std::isfinite(scale_log2) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
   if ((int64_t)g->num_pages * c->Hkv > INT32_MAX) {
     set_last_error("grouped-query attention", "num_pages * Hkv above 2^31 - 1");
     return DSA_ERR_UNSUPPORTED;
@@ -82,7 +83,7 @@ dsa_status_t attend(const dsa_geom_t* g, const dsa_gqa_cache_t* c, int H, const 
   A.q = reinterpret_cast<const __nv_bfloat16*>(q);
   A.q_stride = q_stride;
   A.G = H / c->Hkv;
-  A.scale_log2 = sm_scale * 1.4426950408889634f;
+  A.scale_log2 = scale_log2;
   A.blocks = blocks;
   A.n_sel = n_sel;
   A.out = reinterpret_cast<__nv_bfloat16*>(out);

@@ -729,10 +729,14 @@ constexpr int kWhole = 2;
 
 // Query rows (tokens x heads of a key head) that meet a unit together. Up to 16 rows: a warp
 // has them all. More: a unit's codes are converted by two or four warps, each for 16 of the
-// rows. Above 64: gqa_tiles.cu.
-int rows_per_item(int T, int B, int G, bool listed) {
-  const int64_t rows = listed ? G : ((int64_t)T + B - 1) / B * G;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kGqaTileRows;
+// rows. Above 64: gqa_tiles.cu; above 32 as well if the contexts may have 64 units an SM and
+// more, for it is quicker by unit but slower to start (48 rows, 32 requests of 4096 to 16384
+// tokens: 321 instead of 412 us, one request of 100000: 103 instead of 137; 96 requests of 100
+// to 400 tokens, 35 units an SM: 85 instead of 73, one request of 2000: 20 instead of 17).
+int rows_per_item(const GeomDev& g, int Hkv, int G, bool listed, int num_sms) {
+  const int64_t rows = listed ? G : ((int64_t)g.T + g.B - 1) / g.B * G;
+  const int64_t units = (int64_t)g.B * Hkv * ((g.max_seq_len + kPage - 1) / kPage);
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 && units < (int64_t)64 * num_sms ? 64 : kGqaTileRows;
 }
 
 // Warps per SM. Lists that give twelve warps 32 units each take twelve: the codes' conversion
@@ -769,7 +773,7 @@ cudaError_t launch(GqaAttendArgs A, const CUtensorMap& mk, const CUtensorMap& mv
 
 template <int D, bool I8>
 cudaError_t launch_rows(const GqaAttendArgs& A, const CUtensorMap& mk, const CUtensorMap& mv, int num_sms, cudaStream_t st) {
-  switch (rows_per_item(A.g.T, A.g.B, A.G, A.blocks != nullptr)) {
+  switch (rows_per_item(A.g, A.c.Hkv, A.G, A.blocks != nullptr, num_sms)) {
     case 8:
       if (rows_warps(A.g.T, A.c.Hkv, 8, A.blocks ? A.n_sel : 0, num_sms) == 12)
         return launch<D, I8, 1, 1, 12>(A, mk, mv, num_sms, st);
@@ -796,13 +800,15 @@ cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int grid
 }
 
 size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int Hkv, int D, int G, int n_sel, int num_sms) {
-  const int rows = rows_per_item(g->T, g->B, G, n_sel > 0);
+  GeomDev gd{};
+  gd.B = g->B, gd.T = g->T, gd.max_seq_len = g->max_seq_len;
+  const int rows = rows_per_item(gd, Hkv, G, n_sel > 0, num_sms);
   if (rows > 64) return gqa_parts_bytes(num_sms, kGqaTileRows, D);
   return gqa_parts_bytes(rows_runs(rows, rows_warps(g->T, Hkv, rows, n_sel, num_sms), num_sms), rows, D);
 }
 
 cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st) {
-  if (rows_per_item(A.g.T, A.g.B, A.G, A.blocks != nullptr) > 64) return gqa_tiles_launch(A, num_sms, st);
+  if (rows_per_item(A.g, A.c.Hkv, A.G, A.blocks != nullptr, num_sms) > 64) return gqa_tiles_launch(A, num_sms, st);
   CUtensorMap mk, mv;
   const uint64_t tiles = (uint64_t)A.g.num_pages * A.c.Hkv;
   if (!encode_code_tiles(&mk, A.c.k, A.c.D, tiles) || !encode_code_tiles(&mv, A.c.v, A.c.D, tiles))

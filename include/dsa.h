@@ -436,7 +436,7 @@ size_t dsa_gqa_append_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache
  *     ln(sum_s exp(z_s)). A row that sees no key gives out = 0 and lse = -inf. What lies
  *     in a key or value that a row does not see (NaN codes, pages of other requests) does
  *     not reach it. out overlaps no input; out 16-byte aligned.
- *   sm_scale finite and >= 0. num_pages * Hkv < 2^31.
+ *   sm_scale >= 0, and sm_scale * log2(e) finite in fp32. num_pages * Hkv < 2^31.
  */
 dsa_status_t dsa_gqa_attend(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H, const void* q,
                             int64_t q_stride, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,

@@ -72,7 +72,7 @@ def test_attend_refusals(lib):
     def call(g=geom(), c=cache(k_mean=None, k_mean_scale=None), H=8, q=16, qs=1024, sm=0.1, out=16, lse=16, ws=256, wb=BIG):
         return lib.dsa_gqa_attend(ref(g), ref(c), H, q, qs, sm, out, lse, ws, wb, None)
     sweep(call)
-    for kw in (dict(H=0), dict(H=3), dict(H=34), dict(q=None), dict(q=8), dict(qs=1000), dict(qs=1025), dict(sm=float("nan")),
+    for kw in (dict(H=0), dict(H=3), dict(H=34), dict(q=None), dict(q=8), dict(qs=1000), dict(qs=1025), dict(sm=float("nan")), dict(sm=3e38),
                dict(sm=float("inf")), dict(sm=-0.5), dict(out=None), dict(out=8), dict(lse=18)):
         assert call(**kw) == INV, kw
     assert call(wb=lib.dsa_gqa_attend_workspace_size(ref(geom()), ref(cache()), 8) - 1) == WSP
