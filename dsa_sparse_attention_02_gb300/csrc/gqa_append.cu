@@ -17,6 +17,10 @@
 // take slots cu_q[b]/64 + 2b onward (n new tokens touch at most n/64 + 2 pages), so the
 // host needs only T and B. Rotation, scale, quotient and code are single IEEE operations
 // in a fixed order: the stored state does not depend on the launch.
+//
+// A chunk of 2048 tokens with 64 + 8 + 8 heads of 128 (81 MB) takes 19.8 us in a graph, 4.1 TB/s:
+// every block of threads loads, waits for its maximum and encodes, and two of them an SM
+// overlap (one: 27). One or two tokens take 6 to 7.8: a chain of loads behind the launch.
 #include <type_traits>
 #include "gqa_common.cuh"
 

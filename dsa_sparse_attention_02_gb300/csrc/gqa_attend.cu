@@ -27,6 +27,10 @@
 //     are at most 1, multiply the codes directly, and the softmax's sum is of p / v_scale.
 //     p is rounded to f16 for the product (2^-11 of it), the sum and all else is fp32.
 //
+// 64 requests of 2048 to 8192 tokens with 64 query heads over 8 of 128 (671 MB) take 120 us in a
+// graph, 8 of 131072 (2.15 GB) 331, 6.5 TB/s: HBM. 32 requests of 4096 to 16384 with 20 rows
+// (685 MB) take 150: a unit takes a warp some 4,100 clocks, and rows 17 to 20 read the keys again.
+//
 // A lane whose row does not see a key sets p = 0; values that no row of the tile sees are
 // zeroed, and where some rows see an e4m3 NaN value that others do not, the product is made
 // token by token (0 * NaN would reach the others).
