@@ -735,7 +735,7 @@ constexpr int kWhole = 2;
 // has them all. More: a unit's codes are converted by two or four warps, each for 16 of the
 // rows. Above 64: gqa_tiles.cu; above 32 as well if the contexts may have 64 units an SM and
 // more, for it is quicker by unit but slower to start (48 rows, 32 requests of 4096 to 16384
-// tokens: 321 instead of 412 us, one request of 100000: 103 instead of 137; 96 requests of 100
+// tokens: 300 instead of 412 us, one request of 100000: 97 instead of 137; 96 requests of 100
 // to 400 tokens, 35 units an SM: 85 instead of 73, one request of 2000: 20 instead of 17).
 int rows_per_item(const GeomDev& g, int Hkv, int G, bool listed, int num_sms) {
   const int64_t rows = listed ? G : ((int64_t)g.T + g.B - 1) / g.B * G;

@@ -561,7 +561,8 @@ def test_attend_rows_between_warps_and_tiles():
 
 @pytest.mark.parametrize("dtype", [E4, I8], ids=["e4m3", "i8"])
 @pytest.mark.parametrize("lens,new,H,Hkv,D", [
-    ([1558, 143], [75, 3], 40, 8, 128), ([700, 249, 60], [40, 90, 8], 14, 2, 64),
+    ([1558, 143], [75, 3], 40, 8, 128), ([700, 249, 60], [40, 90, 8], 14, 2, 64), ([64], [16], 8, 1, 128),
+    ([1500, 700, 64, 900], [9, 14, 1, 40], 24, 4, 128), ([3000, 5, 2000], [12, 5, 8], 16, 2, 64),
     ([90 + 7 * i % 170 for i in range(70)], [1 + 3 * i % 10 for i in range(70)], 21, 3, 128)])
 def test_attend_sharp_softmax(lens, new, H, Hkv, D, dtype):
     """Weights on few keys: the running maximum moves often and at different units for the
