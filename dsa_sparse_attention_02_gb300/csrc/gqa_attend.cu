@@ -34,6 +34,7 @@
 // A lane whose row does not see a key sets p = 0; values that no row of the tile sees are
 // zeroed, and where some rows see an e4m3 NaN value that others do not, the product is made
 // token by token (0 * NaN would reach the others).
+#include <algorithm>
 #include "gqa_common.cuh"
 
 namespace dsa {
@@ -803,12 +804,18 @@ cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int grid
   return A.c.D == 128 ? cudaLaunchKernelEx(&cfg, gqa_merge_kernel<128>, A, s) : cudaLaunchKernelEx(&cfg, gqa_merge_kernel<64>, A, s);
 }
 
+// Enough for any smaller T as well: a buffer sized for a batch's largest step serves its others.
 size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int Hkv, int D, int G, int n_sel, int num_sms) {
   GeomDev gd{};
   gd.B = g->B, gd.T = g->T, gd.max_seq_len = g->max_seq_len;
-  const int rows = rows_per_item(gd, Hkv, G, n_sel > 0, num_sms);
-  if (rows > 64) return gqa_parts_bytes(num_sms, kGqaTileRows, D);
-  return gqa_parts_bytes(rows_runs(rows, rows_warps(g->T, Hkv, rows, n_sel, num_sms), num_sms), rows, D);
+  const int most = rows_per_item(gd, Hkv, G, n_sel > 0, num_sms);
+  size_t need = 0;
+  for (int rows : {8, 16, 32, 64, kGqaTileRows}) {
+    if (rows > most) break;
+    const int runs = rows > 64 ? num_sms : rows_runs(rows, rows_warps(g->T, Hkv, rows, n_sel, num_sms), num_sms);
+    need = std::max(need, gqa_parts_bytes(runs, rows, D));
+  }
+  return need;
 }
 
 cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st) {

@@ -441,6 +441,7 @@ size_t dsa_gqa_append_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache
 dsa_status_t dsa_gqa_attend(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H, const void* q,
                             int64_t q_stride, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
                             void* stream);
+/* Never less for a larger T with the other sizes as they are (also of dsa_gqa_attend_blocks). */
 size_t dsa_gqa_attend_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H);
 
 /*

@@ -105,6 +105,15 @@ def test_workspace_sizes_of_refused_arguments(lib):
         assert fn(ref(geom(T=0)), ref(cache()), *more) == 256
 
 
+@pytest.mark.parametrize("B,H,Hkv,D,max_len", [(1, 8, 8, 128, 4096), (32, 40, 8, 128, 16384), (7, 16, 1, 64, 300), (64, 128, 8, 64, 131072)])
+def test_workspace_sizes_grow_with_the_tokens(lib, B, H, Hkv, D, max_len):
+    c = cache(Hkv=Hkv, D=D)
+    for size in (lambda g: lib.dsa_gqa_attend_workspace_size(ref(g), ref(c), H),
+                 lambda g: lib.dsa_gqa_attend_blocks_workspace_size(ref(g), ref(c), H, 16)):
+        got = [size(geom(B=B, T=T, max_seq_len=max_len, bt_stride=max_len // 64 + 1)) for T in list(range(1, 40 * B)) + [10 ** 4, 10 ** 6]]
+        assert got == sorted(got) and got[0] > 256
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     k = torch.zeros(3, 2, 64, 64, dtype=torch.int8)
     sc = torch.zeros(3, 2)
