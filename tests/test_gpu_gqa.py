@@ -708,3 +708,29 @@ def test_two_streams_at_once():
     for i, right in enumerate((want, listed)):
         assert all(torch.equal(o, right[0]) and torch.equal(l, right[1]) for o, l in got[i])
         assert _lib.dsa_get_error(wss[i]) == 0
+
+
+@pytest.mark.parametrize("lens,new,H,Hkv,D", [
+    ([130, 64, 5, 300, 1], [1, 1, 2, 3, 1], 8, 1, 64), ([200, 90, 700], [20, 33, 64], 16, 2, 128), ([75] * 30, [70] * 30, 12, 3, 64)])
+def test_attend_nan_reaches_those_who_see_it(lens, new, H, Hkv, D):
+    """NaN codes at random visible places: a value's reaches its column of the rows that see
+    it, a key's the whole row, and nothing else changes."""
+    c = ref.Case(lens, new, H, Hkv, D, E4, seed=23, pad=1)
+    kb, vb = c.k.view(torch.uint8), c.v.view(torch.uint8)
+    for b, m in enumerate(lens):
+        for i in range(3):
+            pos = m - 1 - int(torch.randint(0, min(m, 100), (1,), generator=c.gen))
+            (kb if b % 3 == 2 and i == 0 else vb)[int(c.block_table[b, pos // 64]), (b + i) % Hkv, pos % 64, (37 * b + i) % D] = 0x7F if i else 0xFF
+    d = Dev(c)
+    li = lists(c, 3, "random")
+    n = sum(new)
+    for blocks in (None, li):
+        out, lse = d.attend(0.2, None if blocks is None else blocks.to(DEV))
+        with np.errstate(invalid="ignore"):
+            r = ref.attend(c, 0.2, blocks)
+            bo, bl = ref.attend_bounds(r)
+        got, want = out.double().cpu().numpy()[:n], r["out"][:n]
+        assert np.isnan(want).any() and np.array_equal(np.isnan(got), np.isnan(want))
+        assert np.array_equal(np.isnan(lse[:n].cpu().numpy()), np.isnan(r["lse"][:n]))
+        ok = np.isfinite(want) & np.isfinite(bo[:n])       # (a NaN value has no bound for its key head's rows: `top`)
+        assert (np.abs(got - want)[ok] <= bo[:n][ok]).all()
