@@ -23,13 +23,17 @@
 //     form of mma.sync, with the query as two e4m3 parts and the keys' codes as they are, was
 //     slower: 1,184 us instead of 837 for the blocks of 2048 tokens.)
 //   * the block's key scale multiplies the scores. Its value scale enters the exponent: with
-//     M the running maximum of z + log2(v_scale), the weights p = 2^(z - M + log2(v_scale))
-//     are at most 1, multiply the codes directly, and the softmax's sum is of p / v_scale.
-//     p is rounded to f16 for the product (2^-11 of it), the sum and all else is fp32.
+//     M the running maximum of z + log2(v_scale), the weights p = 2^(z - M + log2(v_scale) + 15)
+//     multiply the codes directly, and the softmax's sum is of p / v_scale / 2^15. p is rounded
+//     to f16 for the product, the sum and all else is fp32. The largest p of a run's part is
+//     2^15, so that all of f16's range lies below it: a p is off by 2^-11 of itself down to
+//     2^-29 of the largest one, and by 2^-40 of the largest below that. (Behind a sink key
+//     whose value is 0, or a block whose value scale dwarfs the others', the small weights are
+//     what the output is made of; with p up to 1 they were lost from 2^-25 on.)
 //
-// 64 requests of 2048 to 8192 tokens with 64 query heads over 8 of 128 (671 MB) take 120 us in a
-// graph, 8 of 131072 (2.15 GB) 331, 6.5 TB/s: HBM. 32 requests of 4096 to 16384 with 20 rows
-// (685 MB) take 150: a unit takes a warp some 4,100 clocks, and rows 17 to 20 read the keys again.
+// 64 requests of 2048 to 8192 tokens with 64 query heads over 8 of 128 (671 MB) take 122 us in a
+// graph, 8 of 131072 (2.15 GB) 341, 6.3 TB/s: HBM. 32 requests of 4096 to 16384 with 20 rows
+// (685 MB) take 149: a unit takes a warp some 4,100 clocks, and rows 17 to 20 read the keys again.
 //
 // A lane whose row does not see a key sets p = 0; values that no row of the tile sees are
 // zeroed, and where some rows see an e4m3 NaN value that others do not, the product is made
@@ -40,6 +44,8 @@
 namespace dsa {
 
 namespace {
+
+constexpr float kLift = 15.f, kDown = 1.f / 32768.f;   // log2 of the largest weight, and what takes it back
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -502,11 +508,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float Mn = fmaxf(M[i][h], mx + lv);
-            grew |= Mn > M[i][h];
-            keep[i][h] = ex2(M[i][h] - Mn);
+            const float Mo = M[i][h], Mn = fmaxf(Mo, mx + lv);
+            grew |= Mn > Mo;
+            keep[i][h] = ex2(Mo - Mn);
             M[i][h] = Mn;
-            const float ref = Mn - lv;
+            // (where scores are so large that M and lv do not add exactly, this block's largest
+            // weight is still 2^15 if M is its own, and not above it if not)
+            const float ref = (mx + lv >= Mo ? mx : fmaxf(Mn - lv, mx)) - kLift;
             float sum = 0.f;
 #pragma unroll
             for (int sl = 0; sl < kSlices; ++sl) {
@@ -514,12 +522,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
               s[sl][i][2 + h] = ex2(s[sl][i][2 + h] - ref);
               sum += s[sl][i][h] + s[sl][i][2 + h];
             }
-            l[i][h] = l[i][h] * keep[i][h] + sum * ivs;
+            l[i][h] = l[i][h] * keep[i][h] + sum * kDown * ivs;
           }
 #pragma unroll
           for (int sl = 0; sl < kSlices; ++sl) {
-            pb[sl][i][0] = transpose8(pack_f16(s[sl][i][0], s[sl][i][1]));
-            pb[sl][i][1] = transpose8(pack_f16(s[sl][i][2], s[sl][i][3]));
+            pb[sl][i][0] = transpose8(pack_weights(s[sl][i][0], s[sl][i][1]));
+            pb[sl][i][1] = transpose8(pack_weights(s[sl][i][2], s[sl][i][3]));
           }
         }
         if (__any_sync(0xffffffffu, grew)) {
@@ -604,7 +612,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             if (tok[i][h] >= 0) {
               const int rr = m * 8 * NT + 8 * i + 2 * q + h;             // row of the item's tile
-              auto col = [&](int d) { return o[i][d >> 1][2 * (d & 1) + h]; };
+              auto col = [&](int d) { return o[i][d >> 1][2 * (d & 1) + h] * kDown; };
               if (pslot < 0) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 const int64_t to = (int64_t)(q0 + tok[i][h]) * H + h0 * G + (row0 + rr - tok[i][h] * G);

@@ -131,6 +131,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// The same of weights (cut at f16's largest value; a NaN stays one).
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
 // f16 pairs of a word's four codes: (byte 0, byte 1) and (byte 2, byte 3).
 template <bool I8>
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
