@@ -22,17 +22,20 @@
 //   * eight warps do the softmax, one thread per row: while tile 0's four work, the tensor
 //     cores do tile 1's products, and the other way round. The block's value scale is part
 //     of the exponent, as in gqa_attend.cu; the reference maximum M moves only when a score
-//     passes it by more than 2^8 (P stays below 256), and only then O is rescaled.
+//     passes it by more than 2^4, and only then O is rescaled. P at M is 2^11, so that f16 holds
+//     it up to 2^4 above, and keeps 2^-11 of every weight down to 2^-25 of the largest one, 2^-36 of
+//     the largest below that.
 //   * one thread per tile issues its MMAs (each costs the issuer some 40 clocks: with one thread
 //     for both tiles the tensor cores waited for it).
 // Items (request, key head, 256 rows) have as many units as blocks their last token sees;
 // all units are laid end to end and cut into equal runs, one per SM, so that the causal
 // triangle and ragged requests leave no SM idle; cut items are merged afterwards.
 //
-// 2048 tokens over 16384, 64 query heads over 8 of 128 (1.03 TFLOP): 760 to 776 us, 1.33 to 1.36
-// PFLOP/s, the tensor pipe 72% busy. A block takes some 1,770 clocks, where products and
-// shared-memory reads alone would take 1,280: the rest is the softmax between a tile's scores
-// and its products.
+// 2048 tokens over 16384, 64 query heads over 8 of 128 (1.03 TFLOP): 804 us, 1.28 PFLOP/s. A
+// block takes some 1,800 clocks, where products and shared-memory reads alone would take 1,280:
+// the rest is the softmax between a tile's scores and its products. (A reference that moves at
+// 2^8 would take 788 us and keep 4 bits less of the range, one that moves at 2^2 826 and 2 more;
+// weights of at most 2^8 as they were took 782.)
 //
 // A block that some rows see only in part has the keys past each row's position at weight
 // 0, and values that no row sees zeroed. An e4m3 NaN value in such a block is taken out and
@@ -51,7 +54,8 @@ constexpr int kDeep = 3;                    // units between a prefetch and the 
 constexpr int kNanSlots = 16;               // segments whose NaN notes are alive: converters run at most kStages units ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTileCols = 256, kSCols = 64, kOCol = 128;   // of a tile: S / P at 0 and 64
-constexpr float kRescale = 8.f;
+constexpr float kRescale = 4.f;             // log2 of what a weight may pass the reference by,
+constexpr float kLift = 11.f, kDown = 1.f / 2048.f;   // of the weight at the reference, and what takes that back
 
 template <int D>
 struct TileShape {
@@ -551,9 +555,12 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
       for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], s[60 + j]);
       // (a scale of 0 would make masked scores NaN)
       const float f = fmaxf(x.kf * rowf, 1.17549435e-38f);
-      const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f + x.lv;
+      const float mf = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
+      const float top = mf + x.lv;
+      bool rose = false;
       if (__any_sync(0xffffffffu, top > M + kRescale)) {
         const float Mn = fmaxf(M, top), keep = ex2(M - Mn);
+        rose = top >= M;
         M = Mn;
         l *= keep;
         if (!(x.flags & kFirst)) {                 // O so far, once its last product is done
@@ -571,7 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
           tmem_st_wait();
         }
       }
-      const float ref = x.lv - M;
+      // (where scores are so large that M and lv do not add exactly, this block's largest weight is
+      // still 2^11 if M is its own, and not above 2^15 if not)
+      const float ref = rose ? kLift - mf : fminf(x.lv - M + kLift, kLift + kRescale - mf);
       struct { int q0, row0, h, slot, c; } end{};   // (read before the stage may be given back)
       if (x.flags & kLast) end = {unit.q0, unit.row0, unit.h, unit.slot, unit.c};
       if (n + 1 < count) {
@@ -589,11 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
         for (int j = 0; j < 4; ++j) s[k + j] = ex2(s[k + j]);
         add2(a[0], a[1], s[k], s[k + 1]);
         add2(a[2], a[3], s[k + 2], s[k + 3]);
-        p[k / 2] = pack_f16(s[k], s[k + 1]);
-        p[k / 2 + 1] = pack_f16(s[k + 2], s[k + 3]);
+        p[k / 2] = pack_weights(s[k], s[k + 1]);
+        p[k / 2 + 1] = pack_weights(s[k + 2], s[k + 3]);
       }
       tmem_st32(sp, p);
-      l += ((a[0] + a[1]) + (a[2] + a[3])) * x.ivs;
+      l += ((a[0] + a[1]) + (a[2] + a[3])) * kDown * x.ivs;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -620,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            v[j] = D == 128 ? ((j >> 3) & 1 ? b[(j & 7) + 8 * (j >> 4)] : a[(j & 7) + 8 * (j >> 4)]) : (j < 16 ? a[j] : b[j - 16]);
+            v[j] = kDown * (D == 128 ? ((j >> 3) & 1 ? b[(j & 7) + 8 * (j >> 4)] : a[(j & 7) + 8 * (j >> 4)]) : (j < 16 ? a[j] : b[j - 16]));
         }
         if (!I8) {
 #pragma unroll

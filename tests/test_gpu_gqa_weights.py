@@ -59,8 +59,9 @@ def check(c, sm, rows=None):
     return out, lse
 
 
-# lens, new, H, Hkv, D: few rows (a warp's or a team's); the last with several units a run
+# lens, new, H, Hkv, D: few rows (a warp's or a team's), and tiles of many rows; the last of each with several units a run
 FEW = [([64], [1], 1, 1, 128), ([100, 128], [1, 2], 8, 2, 64), ([64, 40], [3, 4], 16, 1, 128), ([900] * 160, [1] * 160, 16, 8, 64)]
+MANY = [([64, 60], [64, 60], 16, 1, 128), ([64], [64], 5, 1, 64), ([300] * 40, [40] * 40, 32, 8, 64)]
 
 
 def sample(c, n=24):
@@ -69,7 +70,7 @@ def sample(c, n=24):
 
 @pytest.mark.parametrize("dtype", [E4, I8], ids=["e4m3", "i8"])
 @pytest.mark.parametrize("gap", [10.0, 17.0, 20.0])
-@pytest.mark.parametrize("lens,new,H,Hkv,D", FEW)
+@pytest.mark.parametrize("lens,new,H,Hkv,D", FEW + MANY)
 def test_sink_with_a_zero_value(lens, new, H, Hkv, D, gap, dtype):
     """The first key outscores all others by `gap` nats and its value is 0: what a row gives
     are the others' weights, e^-10 to e^-20 of the sink's."""
@@ -89,7 +90,7 @@ def test_sink_with_a_zero_value(lens, new, H, Hkv, D, gap, dtype):
 @pytest.mark.parametrize("dtype", [E4, I8], ids=["e4m3", "i8"])
 @pytest.mark.parametrize("up", [10, 20])
 @pytest.mark.parametrize("lens,new,H,Hkv,D", [
-    ([128], [1], 2, 2, 64), ([128, 110], [2, 1], 8, 1, 128)])
+    ([128], [1], 2, 2, 64), ([128, 110], [2, 1], 8, 1, 128), ([128] * 40, [20] * 40, 32, 8, 64)])
 def test_value_scale_above_the_others(lens, new, H, Hkv, D, up, dtype):
     """One outlier value raises its block's scale by 2^up, so that the block's other values
     are coded as 0: the other blocks' values still reach the output in every other column."""
@@ -105,7 +106,7 @@ def test_value_scale_above_the_others(lens, new, H, Hkv, D, up, dtype):
 
 @pytest.mark.parametrize("dtype", [E4, I8], ids=["e4m3", "i8"])
 @pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 20, 2.0 ** 24])
-@pytest.mark.parametrize("lens,new,H,Hkv,D", [([200], [1], 8, 2, 64), ([200], [9], 8, 2, 128)])
+@pytest.mark.parametrize("lens,new,H,Hkv,D", [([200], [1], 8, 2, 64), ([200], [9], 8, 2, 128), ([200], [70], 8, 2, 128)])
 def test_scores_without_fractions(lens, new, H, Hkv, D, size, dtype):
     """Two equal keys of one block far above all others (scores of `size` and twice that, sums
     of whole numbers): a row gives the mean of their values. Each weight is rounded to f16 and may
