@@ -29,6 +29,25 @@ __device__ __forceinline__ GqaToken gqa_token_warp(const GeomDev& g, int t, bool
   return k;
 }
 
+// Reports inconsistent requests: thread `at` of `step` looks at every step-th one. (A search by
+// token or slot can pass such a request over: none of its tokens has to exist.) The first one's
+// loads are issued at construction, to pass under other lookups.
+struct RequestCheck {
+  int c0 = 0, c1 = 0, len = 0;
+  __device__ __forceinline__ void load(const GeomDev& g, int64_t b) {
+    c0 = __ldg(g.cu_q + b), c1 = __ldg(g.cu_q + b + 1), len = __ldg(g.seq_lens + b);
+  }
+  __device__ __forceinline__ RequestCheck(const GeomDev& g, int64_t at) {
+    if (at < g.B) load(g, at);
+  }
+  __device__ __forceinline__ void report(const GeomDev& g, int64_t at, int64_t step, int* err) {
+    for (int64_t b = at; b < g.B; b += step) {
+      if (b != at) load(g, b);
+      if (c0 < 0 || c1 < c0 || c1 > g.T || len > g.max_seq_len) record_error(err, kDevBadIndex);
+    }
+  }
+};
+
 // Page of request b's block c, or -1.
 __device__ __forceinline__ int gqa_page(const GeomDev& g, int b, int c) {
   const int page = __ldg(g.block_table + (int64_t)b * g.bt_stride + c);

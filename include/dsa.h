@@ -419,6 +419,8 @@ typedef struct {
  *     (0 if u is 0), k_mean_scale = u * s / n.
  *   No other token's codes and no other block's scale or mean change. Two requests of a
  *   call must not append to the same page.
+ *   Where cu_q decreases or passes T (DSA_ERR_BAD_INDEX), tokens of the call's other requests
+ *   may go unstored as well.
  *   ws: 256 bytes (the header).
  */
 dsa_status_t dsa_gqa_append(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, const void* k_new,
