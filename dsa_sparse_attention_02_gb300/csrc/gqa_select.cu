@@ -305,6 +305,8 @@ __global__ void __launch_bounds__(32 * kOneWarps) gqa_select_one_kernel(const Gq
   uint32_t* keys = reinterpret_cast<uint32_t*>(select_smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x, kvh = blockIdx.y;
+  const int64_t at = ((int64_t)kvh * gridDim.x + t) * (32 * kOneWarps) + threadIdx.x;
+  RequestCheck check(A.g, at);
   if (warp == kOneWarps - 1) {                    // (meanwhile the others look the token up)
     PooledQuery<D> pooled(A, t, kvh, lane);
     pooled.finish(A.G, s_codes, lane);
@@ -312,6 +314,7 @@ __global__ void __launch_bounds__(32 * kOneWarps) gqa_select_one_kernel(const Gq
   bool bad;
   const GqaToken k = gqa_token_warp(A.g, t, &bad);
   if (bad && threadIdx.x == 0) record_error(A.err, kDevBadIndex);
+  check.report(A.g, at, (int64_t)gridDim.x * gridDim.y * (32 * kOneWarps), A.err);
   if (k.row == kRowPadding) return;
   int* out = A.blocks + ((int64_t)t * A.c.Hkv + kvh) * A.n_sel;
   const int nv = k.row == kRowSees ? (k.pos >> 6) + 1 : 0;
@@ -345,6 +348,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(con
   const int q = lane & 3, lrow = lane >> 2;
   const int t0 = blockIdx.x * TQ, kvh = blockIdx.y;
   static_assert(TQ <= kTileWarps, "a warp per token");
+  const int64_t at = ((int64_t)kvh * gridDim.x + blockIdx.x) * (32 * kTileWarps) + threadIdx.x;
+  RequestCheck check(A.g, at);
   if (warp < TQ) {
     const int t = t0 + warp;
     PooledQuery<D> pooled(A, min(t, A.g.T - 1), kvh, lane);
@@ -359,6 +364,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(con
     }
     pooled.finish(A.G, s_codes[warp], lane);
   }
+  check.report(A.g, at, (int64_t)gridDim.x * gridDim.y * (32 * kTileWarps), A.err);
   __syncthreads();
   // 16 blocks' means and scales of a request, as they are
   struct Means {
