@@ -155,6 +155,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   int req = 0;
   if (listed) {
     total = (int64_t)A.g.T * A.c.Hkv * (A.whole ? 1 : A.n_sel);
+    // (the last runs first: they have no work in small batches)
+    const int64_t at = ((int64_t)(kWarps - 1 - warp) * gridDim.x + (gridDim.x - 1 - blockIdx.x)) * 32 + lane;
+    RequestCheck(A.g, at).report(A.g, at, (int64_t)gridDim.x * (32 * kWarps), A.err);
   } else {
     for (int b0 = 0; b0 < A.g.B; b0 += 32) {
       if (b0 + lane < A.g.B) {

@@ -34,7 +34,7 @@ def call_all(d, T):
     return got
 
 
-@pytest.mark.parametrize("op", ["append", "append without queries", "attend", "select"])
+@pytest.mark.parametrize("op", ["append", "append without queries", "attend", "select", "attend_blocks"])
 @pytest.mark.parametrize("cu", [
     [0, 5, 3, 8], [0, 3, 2, 2, 8], [0, 8, 1, 8, 8], [0, 1, 0, 1, 2, 3, 4, 5, 6, 7, 8], [0, 2, 7, 6], [0, -1, 4, 8],
     list(range(0, 8)) + [6] + [8] * 70, [0] * 2000 + [8, 2] + [8] * 300, [0, 1000, 10, 40], [0, 64, 700, 20, 30, 800, 1000]])
