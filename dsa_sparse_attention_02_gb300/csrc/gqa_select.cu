@@ -291,9 +291,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A token's list where nothing has to be chosen: all of its nv <= n_sel blocks.
-__device__ __forceinline__ void list_all(int* out, int nv, int n_sel, int at, int step) {
-  for (int i = at; i < n_sel; i += step) out[i] = i < nv ? i : -1;
+// A token's list where nothing has to be chosen: all of its nv <= n_sel blocks. (Their pages are
+// looked up only to report bad ones, as where blocks are scored.)
+__device__ __forceinline__ void list_all(const GqaSelectArgs& A, int* out, int b, int nv, int at, int step) {
+  for (int i = at; i < A.n_sel; i += step) out[i] = i < nv ? i : -1;
+  for (int i = at; i < nv; i += step)
+    if (gqa_page(A.g, b, i) < 0) record_error(A.err, kDevBadIndex);
 }
 
 // One token.
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(32 * kOneWarps) gqa_select_one_kernel(const Gq
   int* out = A.blocks + ((int64_t)t * A.c.Hkv + kvh) * A.n_sel;
   const int nv = k.row == kRowSees ? (k.pos >> 6) + 1 : 0;
   if (nv <= A.n_sel) {
-    list_all(out, nv, A.n_sel, threadIdx.x, 32 * kOneWarps);
+    list_all(A, out, k.b, nv, threadIdx.x, 32 * kOneWarps);
     return;
   }
   int c0 = warp * 32, page = c0 + lane < nv ? gqa_page(A.g, k.b, c0 + lane) : -1;
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(con
   for (int w = warp; w < TQ; w += kTileWarps) {
     if (s_row[w] == kRowPadding) continue;
     int* out = A.blocks + ((int64_t)(t0 + w) * A.c.Hkv + kvh) * A.n_sel;
-    if (s_nv[w] <= A.n_sel) list_all(out, s_nv[w], A.n_sel, lane, 32);
+    if (s_nv[w] <= A.n_sel) list_all(A, out, s_b[w], s_nv[w], lane, 32);
     else if (s_nv[w] <= 32 * kHeld / 2) choose_held<kHeld / 2>(keys + w * stride, s_nv[w], A.n_sel, out, lane);
     else if (s_nv[w] <= 32 * kHeld) choose_held<kHeld>(keys + w * stride, s_nv[w], A.n_sel, out, lane);
     else choose<1>(keys + w * stride, s_nv[w], A.n_sel, out, s_scr[w], 0, lane);

@@ -1,5 +1,6 @@
-"""Inconsistent requests among good ones are reported by the grouped-query operators, wherever
-they stand in the batch."""
+"""Inconsistent requests among good ones, and bad pages, are reported by every grouped-query
+operator, wherever they stand in the batch."""
+import numpy as np
 import pytest
 import torch
 
@@ -45,3 +46,23 @@ def test_decreasing_offsets_are_reported(cu, op):
     assert set(call_all(d, T).values()) == {0}           # (no request has tokens)
     d.cu_q.copy_(torch.tensor(cu))
     assert call_all(d, T)[op] == BAD
+
+
+@pytest.mark.parametrize("new", [1, 700])
+@pytest.mark.parametrize("n_sel", [3, 40])
+def test_selection_reports_bad_pages_it_lists(n_sel, new):
+    """Also where every visible block is taken and nothing has to be scored."""
+    c = ref.Case([new + 63, 1100], [new, new], 8, 4, 64, E4, seed=2)
+    for block in (0, (new + 62) // 64):
+        bt = c.block_table.clone()
+        c.block_table[0, block] = c.P
+        d = Dev(c)
+        got = d.select(n_sel, 1, 2)
+        assert _lib.dsa_get_error(d.ws) == BAD
+        c.tokens = lambda: [x for x in ref.Case.tokens(c) if x[0] % 97 == 0]
+        ts = [t for t, _, _ in c.tokens()]
+        assert np.array_equal(got[ts].cpu().numpy(), ref.select(c, n_sel, 1, 2)[ts])
+        c.block_table = bt
+    d = Dev(c)
+    d.select(n_sel, 1, 2)
+    assert _lib.dsa_get_error(d.ws) == 0                             # entries behind the last block are no pages: not read
