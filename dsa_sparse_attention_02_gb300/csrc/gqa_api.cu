@@ -110,6 +110,11 @@ dsa_status_t dsa_gqa_append(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache
   if ((q_in == nullptr) != (q_out == nullptr)) return DSA_ERR_INVALID_ARG;
   if ((cache->k_mean == nullptr) != (cache->k_mean_scale == nullptr)) return DSA_ERR_INVALID_ARG;
   if (q_in && !heads_ok(cache, H)) return DSA_ERR_INVALID_ARG;
+  // (blocks of threads of the launch: one for each page that may receive tokens and key head)
+  if (((int64_t)geom->T / 64 + 2 * (int64_t)geom->B) * cache->Hkv > INT32_MAX) {
+    set_last_error("dsa_gqa_append", "(T / 64 + 2 * B) * Hkv above 2^31 - 1");
+    return DSA_ERR_UNSUPPORTED;
+  }
   if (!ws_ok(ws, ws_bytes, kHeaderBytes)) return DSA_ERR_WORKSPACE;
   if (geom->T == 0) return DSA_OK;
   const int64_t width = (int64_t)cache->Hkv * cache->D;

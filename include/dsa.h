@@ -421,7 +421,7 @@ typedef struct {
  *   call must not append to the same page.
  *   Where cu_q decreases or passes T (DSA_ERR_BAD_INDEX), tokens of the call's other requests
  *   may go unstored as well.
- *   ws: 256 bytes (the header).
+ *   (T/64 + 2*B) * Hkv < 2^31. ws: 256 bytes (the header).
  */
 dsa_status_t dsa_gqa_append(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, const void* k_new,
                             int64_t k_stride, const void* v_new, int64_t v_stride, int32_t H, const void* q_in,
