@@ -347,6 +347,8 @@ def _gqa_call(geom: Geometry, cache: GqaCache, ws, stream):
     """Checks common to the grouped-query calls; the raw stream to enqueue on. (These calls
     take microseconds: on the way of a call that fits, nothing is formatted or looked up twice.)"""
     dev = cache.index
+    if ws is None or not ws.is_contiguous():      # (its size goes by its elements)
+        raise TypeError("ws must be a contiguous tensor, as workspace() makes it")
     if cache.num_pages < geom.num_pages:
         raise ValueError(f"the cache has {cache.num_pages} pages, the geometry {geom.num_pages}")
     if ws.get_device() != dev or geom.seq_lens.get_device() != dev or torch.cuda.current_device() != dev:
@@ -359,6 +361,8 @@ def _gqa_call(geom: Geometry, cache: GqaCache, ws, stream):
 
 def _heads(name, t, geom, cache, heads=None, strided=True):
     """Address and token stride of a bf16 [T, heads, D] tensor (heads of a token side by side)."""
+    if t is None:
+        raise TypeError(f"{name} is missing")
     sh, st, D = t.shape, t.stride(), cache.D
     if (t.dtype is _BF16 and len(sh) == 3 and sh[0] == geom.T and sh[2] == D and (heads is None or sh[1] == heads)
             and t.get_device() == cache.index):
@@ -372,6 +376,8 @@ def _heads(name, t, geom, cache, heads=None, strided=True):
 
 
 def _plain(name, t, dtype, shape, cache):
+    if t is None:
+        raise TypeError(f"{name} is missing")
     if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == cache.index:
         return t.data_ptr()
     if t.device != cache.device:
@@ -387,6 +393,8 @@ def dsa_gqa_append(geom: Geometry, cache: GqaCache, k_new, v_new, q_in=None, q_o
                    rope_cos=None, rope_sin=None, ws=None, stream=None):
     """Rotates the new tokens' keys (and queries into q_out), quantises keys and values
     into the cache's blocks and refreshes the blocks' means."""
+    if (q_in is None) != (q_out is None):
+        raise TypeError("q_in and q_out go together")
     st = _gqa_call(geom, cache, ws, stream)
     k, ks = _heads("k_new", k_new, geom, cache, cache.Hkv)
     v, vs = _heads("v_new", v_new, geom, cache, cache.Hkv)
