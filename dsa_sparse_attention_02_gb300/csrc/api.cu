@@ -110,6 +110,7 @@ dsa_status_t check_geom(const dsa_geom_t* g) {
   if (!g) return DSA_ERR_INVALID_ARG;
   if (g->B < 0 || g->T < 0 || g->max_seq_len < 1 || g->num_pages < 1) return DSA_ERR_INVALID_ARG;
   if (g->page_size != 64) return DSA_ERR_UNSUPPORTED;
+  if (g->max_seq_len > INT32_MAX - 65536) return DSA_ERR_UNSUPPORTED;   // (rounded up to pages and chunks in 32 bits)
   if (g->T > 0 && g->B < 1) return DSA_ERR_INVALID_ARG;
   if (g->bt_stride < (g->max_seq_len + 63) / 64) return DSA_ERR_INVALID_ARG;
   if ((int64_t)g->num_pages * 64 > INT32_MAX) return DSA_ERR_UNSUPPORTED;

@@ -77,8 +77,8 @@ typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1, DSA_I8 = 2 } dsa_dtype_t;
 typedef struct {
   int32_t B;                  /* requests, >= 0 (no upper bound)                     */
   int32_t T;                  /* flattened query tokens = cu_q[B], >= 0              */
-  int32_t max_seq_len;        /* host upper bound on every seq_lens[b], >= 1; sizes the
-                                 grids and the top-k levels                          */
+  int32_t max_seq_len;        /* host upper bound on every seq_lens[b], 1 .. 2^31 - 65537;
+                                 sizes the grids and the top-k levels                */
   int32_t num_pages;          /* physical pages in each paged cache, 1 .. 2^31/64    */
   int32_t page_size;          /* must be 64                                          */
   int32_t bt_stride;          /* int32 elements between block-table rows,

@@ -36,3 +36,14 @@ def test_binding_refuses_what_is_missing_or_does_not_fit():
         _lib._heads("q", None, h, h)
     with pytest.raises(TypeError, match="rope_cos is missing"):
         _lib._plain("rope_cos", None, torch.float32, (8, 4), h)
+
+
+@pytest.mark.parametrize("n", [(1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 65536])
+def test_lengths_that_do_not_round_up_in_32_bits_are_refused(lib, n):  # noqa: F811
+    """(2^31 - 64 tokens and more came out as a negative number of pages, which any table holds.)"""
+    g, c = geom(max_seq_len=n, T=0), cache()
+    assert lib.dsa_gqa_attend(ref(g), ref(c), 8, None, 0, 0.1, None, None, 256, 1 << 20, None) == UNS
+    assert lib.dsa_gqa_append(ref(g), ref(c), None, 0, None, 0, 0, None, 0, None, 0, None, None, 256, 1 << 20, None) == UNS
+    assert lib.dsa_topk_workspace_size(ref(g), 2048) == 256
+    g = geom(max_seq_len=(1 << 31) - 65537, T=0, bt_stride=1 << 25)
+    assert lib.dsa_gqa_attend(ref(g), ref(c), 8, None, 0, 0.1, None, None, 256, 1 << 20, None) == OK
