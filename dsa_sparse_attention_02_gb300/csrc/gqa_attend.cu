@@ -47,12 +47,6 @@ namespace {
 
 constexpr float kLift = 15.f, kDown = 1.f / 32768.f;   // log2 of the largest weight, and what takes it back
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // An 8x8 matrix of 16-bit values, a row per four lanes and two values per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;

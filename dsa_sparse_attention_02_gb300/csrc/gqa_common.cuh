@@ -94,8 +94,9 @@ struct __align__(16) Unit {
 };
 enum : int { kFirst = 1, kLast = 2, kVoid = 4 };   // first / last unit of the run's part of an item; nothing to see
 
-// Merge order of an item that was cut: block of threads c holds its first part in `slot`,
-// the next `follow` ones each a part in their slot 0.
+// Merge order of an item that was cut: run c holds its first part in `slot`, the next `follow`
+// runs each a part in their slot 0. (A run belongs to a warp or a team of warps in gqa_attend.cu,
+// to a block of threads in gqa_tiles.cu.)
 struct __align__(16) Cut { int follow, slot, q0, n, row0, h, pad[2]; };
 
 // A bounded wait by a whole warp: all lanes go on, or all give up. The waiting loop stays
@@ -109,28 +110,28 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_try_wait(a, parity)) || warp_wait_loop(a, parity, abort, err);
 }
 
-// Partial results of cut items, in the workspace: two slots a block of threads, `rows` rows each.
+// Partial results of cut items, in the workspace: two slots a run, `rows` rows each.
 struct GqaParts {
   int rows;
-  Cut* cuts;      // one per block of threads
-  float* ml;      // [2 * grid, rows, 2] running maximum (log2 units) and sum
-  float* o;       // [2 * grid, rows, D]
+  Cut* cuts;      // one per run
+  float* ml;      // [2 * runs, rows, 2] running maximum (log2 units) and sum
+  float* o;       // [2 * runs, rows, D]
 };
-inline size_t gqa_parts_bytes(int grid, int rows, int D) {
-  return align_up(sizeof(Cut) * grid, 256) + align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256) +
-         (size_t)2 * grid * rows * D * sizeof(float);
+inline size_t gqa_parts_bytes(int runs, int rows, int D) {
+  return align_up(sizeof(Cut) * runs, 256) + align_up((size_t)2 * runs * rows * 2 * sizeof(float), 256) +
+         (size_t)2 * runs * rows * D * sizeof(float);
 }
-inline GqaParts gqa_parts(void* scratch, int grid, int rows) {
+inline GqaParts gqa_parts(void* scratch, int runs, int rows) {
   uint8_t* p = reinterpret_cast<uint8_t*>(scratch);
   GqaParts s;
   s.rows = rows;
   s.cuts = reinterpret_cast<Cut*>(p);
-  p += align_up(sizeof(Cut) * grid, 256);
+  p += align_up(sizeof(Cut) * runs, 256);
   s.ml = reinterpret_cast<float*>(p);
-  s.o = reinterpret_cast<float*>(p + align_up((size_t)2 * grid * rows * 2 * sizeof(float), 256));
+  s.o = reinterpret_cast<float*>(p + align_up((size_t)2 * runs * rows * 2 * sizeof(float), 256));
   return s;
 }
-cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int grid, cudaStream_t st);
+cudaError_t gqa_merge_launch(const GqaAttendArgs& A, const GqaParts& s, int runs, cudaStream_t st);
 
 // Rows of an item in the kernel for many query rows (gqa_tiles.cu).
 constexpr int kGqaTileRows = 256;
@@ -155,6 +156,13 @@ __device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
   uint32_t w;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
+}
+// c += A B, m16n8k16, f16 with fp32 sums, in fragments.
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // f16 pairs of a word's four codes: (byte 0, byte 1) and (byte 2, byte 3).
 template <bool I8>

@@ -285,12 +285,6 @@ __device__ __forceinline__ void choose_held(const uint32_t* keys, int nv, int n_
   }
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // A token's list where nothing has to be chosen: all of its nv <= n_sel blocks. (Their pages are
 // looked up only to report bad ones, as where blocks are scored.)
 __device__ __forceinline__ void list_all(const GqaSelectArgs& A, int* out, int b, int nv, int at, int step) {
@@ -433,7 +427,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) gqa_select_tile_kernel(con
 #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
             const uint2 f = s_qf[i][k][lane];
-            mma_f16(s, a[k], f.x, f.y);
+            mma16816(s, a[k][0], a[k][1], a[k][2], a[k][3], f.x, f.y);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {

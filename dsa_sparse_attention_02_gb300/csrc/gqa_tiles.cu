@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_tiles_kernel(const GqaAttendA
           x.kf = __ldg(A.c.k_scale + page_tile) * A.scale_log2;
           x.lv = log2f(vs);
           x.ivs = 1.f / vs;
-        } else {
         }
         seen = page >= 0 ? min(x.rel + hi, kPage - 1) : -1;
         whole_all = page >= 0 && x.rel + lo >= kPage - 1;
