@@ -21,7 +21,7 @@
 //
 // A chunk of 2048 tokens with 64 + 8 + 8 heads of 128 (81 MB) takes 19.8 us in a graph, 4.1 TB/s:
 // every block of threads loads, waits for its maximum and encodes, and two of them an SM
-// overlap (one: 27). One or two tokens take 6 to 7.8: a chain of loads behind the launch.
+// overlap (one: 27). One to four tokens take 6.9 to 7.9: a chain of loads behind the launch.
 #include <type_traits>
 #include "gqa_common.cuh"
 

@@ -32,7 +32,7 @@
 //     what the output is made of; with p up to 1 they were lost from 2^-25 on.)
 //
 // 64 requests of 2048 to 8192 tokens with 64 query heads over 8 of 128 (671 MB) take 122 us in a
-// graph, 8 of 131072 (2.15 GB) 341, 6.3 TB/s: HBM. 32 requests of 4096 to 16384 with 20 rows
+// graph, 8 of 131072 (2.15 GB) 340, 6.3 TB/s: HBM. 32 requests of 4096 to 16384 with 20 rows
 // (685 MB) take 149: a unit takes a warp some 4,100 clocks, and rows 17 to 20 read the keys again.
 //
 // A lane whose row does not see a key sets p = 0; values that no row of the tile sees are
@@ -741,7 +741,7 @@ constexpr int kWhole = 2;
 // has them all. More: a unit's codes are converted by two or four warps, each for 16 of the
 // rows. Above 64: gqa_tiles.cu; above 32 as well if the contexts may have 64 units an SM and
 // more, for it is quicker by unit but slower to start (48 rows, 32 requests of 4096 to 16384
-// tokens: 300 instead of 412 us, one request of 100000: 97 instead of 137; 96 requests of 100
+// tokens: 302 instead of 412 us, one request of 100000: 97 instead of 137; 96 requests of 100
 // to 400 tokens, 35 units an SM: 85 instead of 73, one request of 2000: 20 instead of 17).
 int rows_per_item(const GeomDev& g, int Hkv, int G, bool listed, int num_sms) {
   const int64_t rows = listed ? G : ((int64_t)g.T + g.B - 1) / g.B * G;

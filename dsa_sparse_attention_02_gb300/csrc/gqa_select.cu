@@ -15,9 +15,9 @@
 // for one or two tokens, by bisection between its largest and smallest score where a lane can
 // hold its share of the scores in registers.
 //
-// 8 tokens over 131072 each (17 MB of means) take 9.8 us in a graph: a chain of lookups, four
+// 8 tokens over 131072 each (17 MB of means) take 10.2 us in a graph: a chain of lookups, four
 // radix passes and their barriers. 2048 tokens over 16384 (36 MB, nearly all of it the queries)
-// take 38: issue, 17 for lookups and pooled queries, 4 for scores, 4 for keys, 13 for choosing.
+// take 39: issue, 17 for lookups and pooled queries, 4 for scores, 4 for keys, 13 for choosing.
 // One token per block of threads took 55 there. (32 tokens a tile spill registers: 42.)
 #include "gqa_common.cuh"
 

@@ -31,11 +31,11 @@
 // all units are laid end to end and cut into equal runs, one per SM, so that the causal
 // triangle and ragged requests leave no SM idle; cut items are merged afterwards.
 //
-// 2048 tokens over 16384, 64 query heads over 8 of 128 (1.03 TFLOP): 804 us, 1.28 PFLOP/s. A
-// block takes some 1,800 clocks, where products and shared-memory reads alone would take 1,280:
-// the rest is the softmax between a tile's scores and its products. (A reference that moves at
-// 2^8 would take 788 us and keep 4 bits less of the range, one that moves at 2^2 826 and 2 more;
-// weights of at most 2^8 as they were took 782.)
+// 2048 tokens over 16384, 64 query heads over 8 of 128 (1.03 TFLOP): 804 us, 1.28 PFLOP/s, the
+// tensor pipe 70% busy. A block takes some 1,800 clocks, where products and shared-memory reads
+// alone would take 1,280: the rest is the softmax between a tile's scores and its products. (A
+// reference that moves at 2^8 would take 788 us and keep 4 bits less of the range, one that moves
+// at 2^2 826 and 2 more; weights of at most 2^8 as they were took 782.)
 //
 // A block that some rows see only in part has the keys past each row's position at weight
 // 0, and values that no row sees zeroed. An e4m3 NaN value in such a block is taken out and
