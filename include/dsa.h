@@ -389,7 +389,8 @@ typedef struct {
   void* k;              /* device [num_pages, Hkv, 64, D] codes, 16-byte aligned              */
   void* v;              /* the same of the values                                             */
   float* k_scale;       /* device [num_pages, Hkv], finite, > 0 for blocks that hold tokens   */
-  float* v_scale;
+  float* v_scale;       /* the same, from 2^-100 (the append's least) up, and those of a
+                           request within 2^110 of each other                               */
   int8_t* k_mean;       /* device [num_pages, Hkv, D] or NULL, 16-byte aligned                */
   float* k_mean_scale;  /* device [num_pages, Hkv], NULL exactly if k_mean is                 */
 } dsa_gqa_cache_t;

@@ -126,3 +126,26 @@ def test_scores_without_fractions(lens, new, H, Hkv, D, size, dtype):
     off = (out.double().cpu() - want[None]).abs()
     assert (off <= 2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * 2.0 ** -10 * mag).all()
     assert (lse.double().cpu() - (2 * size + math.log(2))).abs().max() <= 2 * size * 2.0 ** -21 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", [E4, I8], ids=["e4m3", "i8"])
+@pytest.mark.parametrize("other", [2.0 ** -100, 2.0 ** -60, 2.0 ** 8])
+@pytest.mark.parametrize("lens,new,H,Hkv,D", [([128], [1], 2, 2, 64), ([700, 333], [2, 1], 8, 1, 128), ([600, 130], [300, 64], 8, 2, 128)])
+def test_blocks_of_zeros(lens, new, H, Hkv, D, other, dtype):
+    """Every second block holds zeros, at the least scale that the append writes, and the others'
+    scales are up to 2^108 above it: the zeros' weights count in the denominator all the same. (The
+    sum of a score in powers of two and a scale's logarithm is rounded to 2^-18 up to 128: 2^-15 for
+    a weight's relative error of several such.)"""
+    c = ref.Case(lens, new, H, Hkv, D, dtype, seed=8)
+    c.v_scale[:] = other * (1 + torch.rand(c.v_scale.shape, generator=c.gen)) / 2
+    for b, n in enumerate(lens):
+        zeros = c.block_table[b, :-(-n // 64):2].long()
+        c.v_scale[zeros] = 2.0 ** -100
+        c.v.view(torch.uint8)[zeros] = 0
+    out, lse = Dev(c).attend(D ** -0.5)
+    r = ref.attend(c, D ** -0.5)
+    rel = 2 * D * 2.0 ** -24 * r["dots"] + 2.0 ** -11 + 2.0 ** -15
+    got, le = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    bound = np.abs(r["out"]) * 2.0 ** -8 + (1 + 2.0 ** -8) * r["mag"] * 2 * rel[..., None]
+    assert (np.abs(got - r["out"]) <= bound).all()
+    assert (np.abs(le - r["lse"]) <= rel - 2.0 ** -11 + 2.0 ** -20 + np.abs(r["lse"]) * 2.0 ** -22).all()
