@@ -30,6 +30,8 @@ EXPORTED = (
     "dsa_gqa_append", "dsa_gqa_append_workspace_size", "dsa_gqa_attend", "dsa_gqa_attend_workspace_size",
     "dsa_block_select", "dsa_block_select_workspace_size",
     "dsa_gqa_attend_blocks", "dsa_gqa_attend_blocks_workspace_size",
+    "dsa_rope_init", "dsa_latent_append", "dsa_latent_append_workspace_size",
+    "dsa_latent_attend", "dsa_latent_attend_workspace_size", "dsa_latent_gather", "dsa_latent_gather_workspace_size",
     "dsa_get_error", "dsa_clear_error", "dsa_wait_probe", "dsa_status_string", "dsa_last_error", "dsa_abi_version",
 )
 
@@ -69,6 +71,11 @@ class dsa_gqa_cache_t(C.Structure):
                 ("k_mean", C.c_void_p), ("k_mean_scale", C.c_void_p)]
 
 
+class dsa_rope_t(C.Structure):
+    _fields_ = [("dim", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32),
+                ("turns", C.c_uint64 * 32)]
+
+
 _lib = None
 
 
@@ -84,6 +91,7 @@ def load(path: str = LIB_PATH):
     G = C.POINTER(dsa_geom_t)
     S = C.POINTER(dsa_step_args_t)
     K = C.POINTER(dsa_gqa_cache_t)
+    R = C.POINTER(dsa_rope_t)
     sig = {
         "dsa_indexer_scores": (C.c_int, [G, C.c_int, I32, P, P, P, P, P, P, I64, P, SZ, P]),
         "dsa_indexer_scores_workspace_size": (SZ, [G]),
@@ -112,6 +120,13 @@ def load(path: str = LIB_PATH):
         "dsa_block_select_workspace_size": (SZ, [G, K, I32]),
         "dsa_gqa_attend_blocks": (C.c_int, [G, K, I32, P, I64, P, I32, F, P, P, P, SZ, P]),
         "dsa_gqa_attend_blocks_workspace_size": (SZ, [G, K, I32, I32]),
+        "dsa_rope_init": (C.c_int, [R, I32, I32, F, F, I64, F, F, F]),
+        "dsa_latent_append": (C.c_int, [G, C.c_int, P, I64, P, F, R, P, P, I32, P, I64, I64, P, I64, I64, P, SZ, P]),
+        "dsa_latent_append_workspace_size": (SZ, [G]),
+        "dsa_latent_attend": (C.c_int, [G, C.c_int, I32, P, P, F, P, P, P, SZ, P]),
+        "dsa_latent_attend_workspace_size": (SZ, [G, I32]),
+        "dsa_latent_gather": (C.c_int, [G, C.c_int, P, P, P, I32, P, I64, P, SZ, P]),
+        "dsa_latent_gather_workspace_size": (SZ, [G]),
         "dsa_get_error": (C.c_int, [P, P]),
         "dsa_clear_error": (C.c_int, [P, P]),
         "dsa_wait_probe": (C.c_int, [P, SZ, C.c_uint32, P]),
@@ -462,6 +477,141 @@ def dsa_gqa_attend_blocks(geom: Geometry, cache: GqaCache, q, blocks, sm_scale: 
     s = load().dsa_gqa_attend_blocks(geom.ref, cache.ref, H, qp, qs, bp, n, sm_scale, o, le, ws.data_ptr(), ws.numel(), st)
     if s:
         raise DsaError(s, "dsa_gqa_attend_blocks")
+
+
+class Rope:
+    """Rotary frequencies of dsa_latent_append: the first dim (16, 32, 48 or 64) of the 64 rotary
+    values, interleaved or half layout, base^(-2i/dim), divided by factor, or where original_len
+    is given only as far as the ramp between beta_fast and beta_slow rotations over that length
+    says; attn_factor scales every sine and cosine. Host memory, kept by the caller."""
+
+    def __init__(self, dim: int = 64, base: float = 10000.0, *, interleaved: bool = True, factor: float = 1.0,
+                 original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, attn_factor: float = 1.0):
+        self.c = dsa_rope_t()
+        self.ref = C.byref(self.c)
+        _check(load().dsa_rope_init(self.ref, int(dim), int(bool(interleaved)), base, factor, int(original_len), beta_fast,
+                                    beta_slow, attn_factor), "dsa_rope_init")
+
+
+_LATENT_ROW = {DSA_BF16: ((64, 576), _BF16), DSA_E4M3: ((41984,), torch.uint8), DSA_I8: ((41984,), torch.uint8)}
+
+
+def _latent_call(ws, stream, index):
+    """Checks common to the latent calls; the raw stream to enqueue on."""
+    if ws is None or not ws.is_contiguous():      # (its size goes by its elements)
+        raise TypeError("ws must be a contiguous tensor, as workspace() makes it")
+    if ws.get_device() != index or index < 0 or torch.cuda.current_device() != index:
+        raise ValueError("tensors, geometry and workspace must be on the current device, "
+                         f"cuda:{torch.cuda.current_device()}" if torch.cuda.is_available() else "tensors must be CUDA tensors")
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _latent_cache(kv_dtype, kv_cache, geom, index):
+    """Address of a paged latent cache: [pages, 64, 576] bf16, or [pages, 41984] bytes of records."""
+    if kv_dtype not in _LATENT_ROW:
+        raise ValueError(f"kv_dtype {kv_dtype}")
+    shape, dtype = _LATENT_ROW[kv_dtype]
+    if (isinstance(kv_cache, torch.Tensor) and kv_cache.dtype is dtype and kv_cache.is_contiguous()
+            and kv_cache.shape[1:] == shape and kv_cache.get_device() == index):
+        if kv_cache.shape[0] < geom.num_pages:
+            raise ValueError(f"the cache has {kv_cache.shape[0]} pages, the geometry {geom.num_pages}")
+        return kv_cache.data_ptr()
+    raise TypeError(f"kv_cache must be a contiguous {dtype} tensor of shape [pages, {', '.join(map(str, shape))}] on the "
+                    "geometry's device")
+
+
+def _tensor(name, t, dtype, shape, index, inner=1):
+    """Address of a tensor of this type and shape whose innermost `inner` dimensions lie side by
+    side, and its other strides."""
+    if t is None:
+        raise TypeError(f"{name} is missing")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        raise TypeError(f"{name} must be a {dtype} tensor of shape {list(shape)} on cuda:{index}")
+    st, width = t.stride(), 1
+    for i in range(len(shape) - 1, len(shape) - 1 - inner, -1):
+        if shape[i] != 1 and st[i] != width:
+            raise TypeError(f"{name}: its innermost values must lie side by side")
+        width *= shape[i]
+    # (a stride over a single element says nothing: the least that fits)
+    outer, least = [], width
+    for i in range(len(shape) - inner - 1, -1, -1):
+        outer.append(st[i] if shape[i] > 1 else max(least, st[i]))
+        least = outer[-1] * shape[i] if shape[i] > 1 else outer[-1]
+    return (t.data_ptr(), *reversed(outer))
+
+
+def dsa_latent_append_workspace_size(geom: Geometry) -> int:
+    return int(load().dsa_latent_append_workspace_size(geom.ref))
+
+
+def dsa_latent_append(geom: Geometry, kv_dtype: int, kv_in, kv_cache, rope: Rope, gamma=None, eps: float = 1e-6,
+                      q_in=None, q_out=None, kv_out=None, ws=None, stream=None):
+    """Norms the new rows kv_in [T, 576], rotates their last 64 values, writes them into the
+    paged cache (and kv_out [T, 576] bf16), and rotates the queries' parts q_in [T, H, 64] into
+    q_out (which may be q_in). kv_in None: queries alone; q_in None: rows alone."""
+    if (q_in is None) != (q_out is None):
+        raise TypeError("q_in and q_out go together")
+    if kv_in is None and (kv_cache is not None or kv_out is not None):
+        raise TypeError("kv_cache and kv_out go with kv_in")
+    index = geom.seq_lens.get_device()
+    st = _latent_call(ws, stream, index)
+    T = geom.T
+    kv = cache = gm = ko = qi = qo = None
+    ks = H = qit = qih = qot = qoh = 0
+    if kv_in is not None:
+        cache = _latent_cache(kv_dtype, kv_cache, geom, index)
+        kv, ks = _tensor("kv_in", kv_in, _BF16, (T, 576), index)
+        if gamma is not None:
+            gm, = _tensor("gamma", gamma, _F32, (512,), index)
+        if kv_out is not None:
+            ko, = _tensor("kv_out", kv_out, _BF16, (T, 576), index, 2)
+    if q_in is not None:
+        H = q_in.shape[1]
+        qi, qit, qih = _tensor("q_in", q_in, _BF16, (T, H, 64), index)
+        qo, qot, qoh = _tensor("q_out", q_out, _BF16, (T, H, 64), index)
+    s = load().dsa_latent_append(geom.ref, kv_dtype, kv, ks, gm, eps, rope.ref, cache, ko, H, qi, qit, qih, qo, qot, qoh,
+                                 ws.data_ptr(), ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_latent_append")
+
+
+def dsa_latent_attend_workspace_size(geom: Geometry, H: int) -> int:
+    return int(load().dsa_latent_attend_workspace_size(geom.ref, int(H)))
+
+
+def dsa_latent_attend(geom: Geometry, kv_dtype: int, q, kv_cache, sm_scale: float, out, lse, ws, stream=None):
+    """Causal absorbed attention of q [T, H, 576] over the whole paged context into out
+    [T, H, 512] bf16 and lse [T, H] fp32 (or None)."""
+    index = geom.seq_lens.get_device()
+    st = _latent_call(ws, stream, index)
+    T, H = geom.T, q.shape[1]
+    qp, = _tensor("q", q, _BF16, (T, H, 576), index, 3)
+    cache = _latent_cache(kv_dtype, kv_cache, geom, index)
+    op, = _tensor("out", out, _BF16, (T, H, 512), index, 3)
+    lp = None if lse is None else _tensor("lse", lse, _F32, (T, H), index, 2)[0]
+    s = load().dsa_latent_attend(geom.ref, kv_dtype, H, qp, cache, sm_scale, op, lp, ws.data_ptr(), ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_latent_attend")
+
+
+def dsa_latent_gather_workspace_size(geom: Geometry) -> int:
+    return int(load().dsa_latent_gather_workspace_size(geom.ref))
+
+
+def dsa_latent_gather(geom: Geometry, kv_dtype: int, kv_cache, first, cu_k, out, ws, stream=None):
+    """Rows cu_k[b] .. cu_k[b+1]-1 of out [S, 576] bf16 = request b's cached rows from position
+    first[b] (None: 0) on, records dequantised."""
+    index = geom.seq_lens.get_device()
+    st = _latent_call(ws, stream, index)
+    cache = _latent_cache(kv_dtype, kv_cache, geom, index)
+    fp = None if first is None else _tensor("first", first, _I32, (geom.B,), index)[0]
+    cp, = _tensor("cu_k", cu_k, _I32, (geom.B + 1,), index)
+    op, os_ = _tensor("out", out, _BF16, (out.shape[0], 576), index)
+    s = load().dsa_latent_gather(geom.ref, kv_dtype, cache, fp, cp, out.shape[0], op, os_, ws.data_ptr(), ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_latent_gather")
 
 
 def dsa_stage_copy(dst, src, nbytes: int, stream=None):

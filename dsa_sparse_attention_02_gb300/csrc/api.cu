@@ -78,6 +78,25 @@ bool encode_code_tiles(CUtensorMap* m, const void* base, int D, uint64_t tiles) 
   return true;
 }
 
+bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
+                          const uint64_t (&strides)[2], const uint32_t (&box)[3], bool swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) { set_last_error("cudaGetDriverEntryPointByVersion", "cuTensorMapEncodeTiled unavailable"); return false; }
+  const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
+  const cuuint32_t b[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
+  const CUresult r = fn(m, dt, 3, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[128];
+    snprintf(buf, sizeof(buf), "CUresult %d (%llu x %llu x %llu, box %u x %u x %u)", (int)r, (unsigned long long)dims[0],
+             (unsigned long long)dims[1], (unsigned long long)dims[2], box[0], box[1], box[2]);
+    set_last_error("cuTensorMapEncodeTiled", buf);
+    return false;
+  }
+  return true;
+}
+
 bool encode_mla_q_map(CUtensorMap* map_q, const void* q, int T, int H) {
   const uint32_t box_rows = H < 16 ? (uint32_t)H : 16u;
   return encode_tensor_map_2d(map_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, 576, (uint64_t)T * H, 1152, 64, box_rows);

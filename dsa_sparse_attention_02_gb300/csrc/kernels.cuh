@@ -192,6 +192,54 @@ struct GqaAttendArgs {
 size_t gqa_attend_scratch_bytes(const dsa_geom_t* g, int Hkv, int D, int G, int n_sel, int num_sms);
 cudaError_t gqa_attend_launch(const GqaAttendArgs& A, int num_sms, cudaStream_t st);
 
+// ---- dense latent attention (latent_*.cu; entry points in latent_api.cu)
+struct LatentAppendArgs {
+  GeomDev g;
+  int kv_format;                // KvFormat
+  const __nv_bfloat16* kv_in;   // token t at t * kv_stride, or null
+  int64_t kv_stride;
+  const float* gamma;           // [512] or null (1)
+  float eps;
+  dsa_rope_t rope;
+  uint8_t* kv_cache;
+  __nv_bfloat16* kv_out;        // [T, 576] or null
+  int H;
+  const __nv_bfloat16* q_in;    // or null: token t's head h at t * qi_token + h * qi_head
+  __nv_bfloat16* q_out;
+  int64_t qi_token, qi_head, qo_token, qo_head;
+  int* err;
+};
+int64_t latent_append_blocks(int T, int H, bool rows, bool queries);   // of the launch
+cudaError_t latent_append_launch(const LatentAppendArgs& A, cudaStream_t st);
+struct LatentGatherArgs {
+  GeomDev g;
+  int kv_format;
+  const uint8_t* kv;
+  const int* first;             // [B] or null (0)
+  const int* cu_k;              // [B + 1]
+  int S;
+  __nv_bfloat16* out;           // row s at s * out_stride
+  int64_t out_stride;
+  int* err;
+};
+cudaError_t latent_gather_launch(const LatentGatherArgs& A, cudaStream_t st);
+struct LatentMaps { CUtensorMap q, pair, rope; };
+struct LatentAttendArgs {
+  GeomDev g;
+  int kv_format;
+  int H;
+  const uint8_t* kv;
+  float scale_log2;             // sm_scale * log2(e)
+  __nv_bfloat16* out;           // [T, H, 512]
+  float* lse;                   // [T, H] or null
+  void* scratch;
+  int min_run;                  // shortest run of units
+  int* err;
+};
+int latent_attend_rows(const GeomDev& g, int H);   // query rows of an item: the box of the queries' map
+size_t latent_attend_scratch_bytes(const dsa_geom_t* g, int H, int num_sms);
+cudaError_t latent_attend_launch(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st);
+
 // ---- host helpers defined in api.cu
 constexpr size_t kHeaderBytes = 256;   // workspace header: the error word comes first
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -209,6 +257,9 @@ dsa_status_t check_attend(const dsa_geom_t* g, dsa_dtype_t dt, int H, const void
 dsa_status_t resolve_outputs(const dsa_geom_t* g, int H, void* out, float* lse, void** dout, float** dlse);
 bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t cols,
                           uint64_t rows, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows);
+// 3-D tensor (innermost first; strides in bytes of the outer two) in boxes, 128-byte-swizzled or not.
+bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
+                          const uint64_t (&strides)[2], const uint32_t (&box)[3], bool swizzle);
 // Codes [tiles, 64, D] bytes in boxes of one tile, with the swizzle of D-byte rows (64 or
 // 128): 16-byte chunk i of row r lies at chunk i ^ (r & 7) (128), i ^ ((r >> 1) & 3) (64).
 bool encode_code_tiles(CUtensorMap* m, const void* base, int D, uint64_t tiles);

@@ -1,0 +1,799 @@
+// Dense causal attention in the absorbed form over the paged latent cache (the definition is
+// at dsa_latent_attend in include/dsa.h).
+//
+// All heads of a token share one row per key, so a request's tokens x heads are query rows
+// against the same pages. An item is (request, N of those rows); a unit is a page of 64 keys of
+// an item. For each unit, on tcgen05 with bf16 operands and fp32 sums:
+//   S = Q K^T      64 x 64 x 576 (Q rows past N are whatever lies behind: their lanes are not read)
+//   O^T += C^T P^T 4 x (128 x N x 64), C the page's 512 latent columns, read MN-major from the
+//                  same shared memory that S reads K-major
+// so that O takes 4 N columns of tensor memory (with O by rows, its 512 columns would fill it),
+// a page is read once for both products, and one 64-key page is what has to be whole: the rows
+// of N = 64 queries alone take 74 KB, and 128 keys would leave no room for the next ones.
+//
+//   warps 0-3  softmax: S has 16 rows in each lane quarter; a 16 x 256-bit load spreads them
+//              over all lanes, warp w has rows 16 w .. 16 w + 15 (those below N), a thread two of
+//              them with 16 keys each. P^T goes to shared memory as bf16. The reference
+//              maximum moves only when a score passes it by more than 2^8; then, and at an
+//              item's end, all four warps read their quarter of O^T's lanes (latent columns).
+//   warp 4     issues the products: the next page's scores before this page's values
+//   warp 5     finds the units of this block's run, loads pages by TMA in pairs of 64-column atoms
+//   the rest   records: convert codes * scale to bf16 (as every reader of them does). Both:
+//              in a page that some row of the item does not see whole, zero the keys that no row
+//              sees and those with a NaN or infinity, which rows that do see them get as
+//              a NaN score (a weight of zero would not keep them out of the sum).
+// All units are laid end to end and cut into equal runs, one per SM; cut items are merged.
+#include "latent_common.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kUnits = 4;                    // units described ahead
+constexpr int kPairBytes = 2 * kPage * 128;  // two atoms of 64 rows x 64 bf16
+constexpr int kRopeBytes = kPage * 128;
+constexpr int kCodeStage = kPage * 128;      // a pair's codes
+constexpr int kScaleSlots = 4;
+constexpr int kMmaWarp = 4, kLoadWarp = 5, kFixWarp0 = 6;
+constexpr uint32_t kSCol = 256;              // O^T at 0, S at 256 and 320
+constexpr uint32_t kTmem = 512;
+constexpr float kMove = 8.f;                 // log2 of what a weight may pass the reference by
+enum : int { kEdge = 8 };                    // some row of the item does not see the whole page
+
+struct __align__(16) LatentUnit {
+  int flags, rel;       // position of token 0 less the page's first position
+  int row0, rows;       // first row of the item in its request (token row / H, head row % H); rows in use
+  int slot, last;       // partial slot or -1; last key of the page that some row sees, or -1
+  int64_t out;          // global number of the item's first row
+};
+
+template <int N, int KV>
+struct LatentShape {
+  static constexpr bool kRecord = KV != kKvBf16;
+  // Rings as deep as shared memory allows. Below eight pairs the next page's scores begin with the
+  // pairs that fit beside this page's (kEarly); the others follow its values.
+  static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 64 ? 6 : 8);
+  static constexpr int kRopes = !kRecord && N == 16 ? 3 : 2;
+  static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 3 : N == 32 ? 4 : 6;
+  static constexpr int kEarly = kPairs >= 8 ? 4 : kPairs - 4;
+  static constexpr int kFixWarps = kRecord ? 8 : 4;
+  static constexpr int kThreads = 32 * (kFixWarp0 + kFixWarps);
+  static constexpr int kQBytes = 9 * N * 128, kPBytes = N * 128;
+  static constexpr int kSmem = 1024 + kQBytes + kPBytes + kRopes * kRopeBytes + kPairs * kPairBytes + kCodes * kCodeStage +
+                               (kRecord ? kScaleSlots * 1024 : 0);
+};
+
+// Requests as the items see them.
+struct LatentReq {
+  int q0, n, start;      // first token, tokens, position of the first (may be negative)
+  int tiles;
+  bool bad, none;        // none: nothing visible (inconsistent geometry)
+};
+template <int N>
+__device__ __forceinline__ LatentReq latent_req(const LatentAttendArgs& A, int b) {
+  LatentReq r;
+  const int c0 = __ldg(A.g.cu_q + b), c1 = __ldg(A.g.cu_q + b + 1), len = __ldg(A.g.seq_lens + b);
+  r.bad = c0 < 0 || c1 < c0 || c1 > A.g.T || len > A.g.max_seq_len;
+  r.q0 = min(max(c0, 0), A.g.T);
+  r.n = max(min(c1, A.g.T) - r.q0, 0);
+  r.none = r.bad || len <= 0;
+  r.start = len - r.n;
+  r.tiles = (r.n * A.H + N - 1) / N;      // (T * H stays below 2^31)
+  return r;
+}
+// Pages that tile i's last token sees; at least one unit, so that empty rows are written too.
+template <int N>
+__device__ __forceinline__ int latent_units(const LatentAttendArgs& A, const LatentReq& r, int i) {
+  if (r.none) return 1;
+  const int last = min(r.n - 1, (int)(((int64_t)i * N + N - 1) / A.H));
+  return max(r.start + last, 0) / kPage + 1;
+}
+// Units of tiles 0 .. i - 1: tile j sees page k if its last token reaches position 64 k, which
+// tiles from (64 k - start) H / N on do.
+template <int N>
+__device__ __forceinline__ int64_t latent_before(const LatentAttendArgs& A, const LatentReq& r, int i) {
+  if (r.none || i <= 0) return i;
+  const int k0 = max(r.start, 0) / kPage, k1 = max(r.start + r.n - 1, 0) / kPage;
+  int64_t s = (int64_t)i * (k0 + 1);
+  for (int k = k0 + 1; k <= k1; ++k) s += max((int64_t)i - (int64_t)(k * kPage - r.start) * A.H / N, (int64_t)0);
+  return s;
+}
+
+template <int N, int KV>
+__global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
+    latent_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_pair,
+                         const __grid_constant__ CUtensorMap map_rope, const LatentAttendArgs A, const LatentParts parts) {
+  using S = LatentShape<N, KV>;
+  constexpr bool kRecord = S::kRecord;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_buf = smem;                                  // (S reads 64 rows of each atom: up to 6 KB past the last)
+  uint8_t* p_buf = q_buf + S::kQBytes;
+  uint8_t* rope_buf = p_buf + S::kPBytes;
+  uint8_t* pair_buf = rope_buf + S::kRopes * kRopeBytes;
+  uint8_t* code_buf = pair_buf + S::kPairs * kPairBytes;
+  float* scale_buf = reinterpret_cast<float*>(code_buf + S::kCodes * kCodeStage);
+  __shared__ uint64_t u_full[kUnits], u_loaded[kUnits], u_empty[kUnits], e_full[kUnits];
+  __shared__ uint64_t pair_full[S::kPairs], pair_empty[S::kPairs], rope_full[S::kRopes], rope_empty[S::kRopes];
+  __shared__ uint64_t code_full[kRecord ? S::kCodes : 1], code_empty[kRecord ? S::kCodes : 1];
+  __shared__ uint64_t q_full, s_full[2], p_full, o_done, drain;
+  __shared__ LatentUnit s_unit[kUnits];
+  __shared__ uint32_t s_bad[kUnits][2];                   // keys with a value that is not finite
+  __shared__ float s_keep[N], s_max[N], s_sum[N];
+  __shared__ int s_count, s_abort;
+  __shared__ uint32_t s_tmem;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();
+
+  if (tid == 0) {
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(smem_u32(&u_full[i]), 1);
+      mbar_init(smem_u32(&u_loaded[i]), 1);
+      mbar_init(smem_u32(&u_empty[i]), 4 + S::kFixWarps);
+      mbar_init(smem_u32(&e_full[i]), S::kFixWarps);
+    }
+    for (int i = 0; i < S::kPairs; ++i) {
+      mbar_init(smem_u32(&pair_full[i]), kRecord ? S::kFixWarps : 1);
+      mbar_init(smem_u32(&pair_empty[i]), 1);
+    }
+    for (int i = 0; i < S::kRopes; ++i) {
+      mbar_init(smem_u32(&rope_full[i]), 1);
+      mbar_init(smem_u32(&rope_empty[i]), 1);
+    }
+    if (kRecord)
+      for (int i = 0; i < S::kCodes; ++i) {
+        mbar_init(smem_u32(&code_full[i]), 1);
+        mbar_init(smem_u32(&code_empty[i]), S::kFixWarps);
+      }
+    mbar_init(smem_u32(&q_full), 1);
+    mbar_init(smem_u32(&s_full[0]), 1);
+    mbar_init(smem_u32(&s_full[1]), 1);
+    mbar_init(smem_u32(&p_full), 4);
+    mbar_init(smem_u32(&o_done), 1);
+    mbar_init(smem_u32(&drain), 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&s_tmem), kTmem);
+    tmem_relinquish();
+  }
+  // The run [begin, end) of all units, the request it starts in and where that begins.
+  int64_t begin = 0, end = 0, base = 0, total = 0;
+  int req = 0, runs = 1;
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_pair);
+      tma_prefetch_desc(&map_rope);
+      parts.cuts[blockIdx.x].follow = 0;
+    }
+    for (int b0 = 0; b0 < A.g.B; b0 += 32) {
+      if (b0 + lane < A.g.B) {
+        const LatentReq r = latent_req<N>(A, b0 + lane);
+        total += latent_before<N>(A, r, r.tiles);
+        if (r.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    runs = (int)min((int64_t)gridDim.x, max((total + A.min_run - 1) / A.min_run, (int64_t)1));
+    if ((int)blockIdx.x < runs) {
+      begin = split_begin(blockIdx.x, total, runs);
+      end = split_begin(blockIdx.x + 1, total, runs);
+      for (int b0 = 0; b0 < A.g.B; b0 += 32) {
+        int64_t w = 0;
+        if (b0 + lane < A.g.B) {
+          const LatentReq r = latent_req<N>(A, b0 + lane);
+          w = latent_before<N>(A, r, r.tiles);
+        }
+        int64_t upto = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, base + upto > begin);
+        if (m) {
+          const int l = __ffs(m) - 1;
+          req = b0 + l;
+          base += __shfl_sync(0xffffffffu, upto - w, l);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+    if (lane == 0) s_count = (int)(end - begin);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int count = s_count;
+  const uint32_t tmem = s_tmem;
+  volatile int* abort = &s_abort;
+
+  if (count == 0) {
+    // nothing of this batch for this block
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ units and loads
+    int b = req, ti = 0, c = 0;
+    LatentReq r = latent_req<N>(A, b);
+    {
+      // the last tile that begins at or before unit `begin`
+      const int64_t o = begin - base;
+      int lo = 0, hi = r.tiles - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (latent_before<N>(A, r, mid) <= o) lo = mid; else hi = mid - 1;
+      }
+      ti = lo;
+      c = (int)(o - latent_before<N>(A, r, lo));
+    }
+    LatentUnit x{};
+    int page = -1, cnt = 0, at = 0;
+    // up to 32 units at a time, one per lane
+    auto batch = [&](int64_t u) {
+      cnt = (int)min((int64_t)32, end - u);
+      int bb = b, tt = ti, cc = c;
+      LatentReq rr = r;
+      int units = latent_units<N>(A, rr, tt);
+      for (int step = lane; step > 0 && lane < cnt;) {          // forward by `lane` units
+        const int left = units - cc;
+        if (step < left) {
+          cc += step;
+          break;
+        }
+        step -= left;
+        cc = 0;
+        if (++tt == rr.tiles) {
+          tt = 0;
+          do rr = latent_req<N>(A, ++bb);
+          while (rr.tiles == 0 && bb + 1 < A.g.B);
+        }
+        units = latent_units<N>(A, rr, tt);
+      }
+      __syncwarp();
+      if (lane < cnt) {
+        const int64_t me = u + lane, ib = me - cc, ie = ib + units;
+        x.row0 = tt * N;
+        x.rows = min(N, rr.n * A.H - x.row0);
+        x.out = (int64_t)rr.q0 * A.H + x.row0;
+        x.rel = rr.start - cc * kPage;
+        const int lo = x.row0 / A.H, hi = (x.row0 + x.rows - 1) / A.H;
+        page = -1;
+        if (!rr.none && x.rel + hi >= 0) {
+          page = gqa_page(A.g, bb, cc);
+          if (page < 0) record_error(A.err, kDevBadIndex);
+        }
+        x.last = page >= 0 ? min(x.rel + hi, kPage - 1) : -1;
+        const bool first = me == ib || me == begin, last = me + 1 == ie || me + 1 == end;
+        x.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (page >= 0 ? 0 : kVoid) |
+                  (page < 0 || x.rel + lo < kPage - 1 ? kEdge : 0);
+        const bool cut = ib < begin || ie > end;
+        x.slot = !cut ? -1 : 2 * (int)blockIdx.x + (max(ib, begin) == begin ? 0 : 1);
+        if (last && cut && ib >= begin) {
+          LatentCut k{};
+          k.follow = (int)split_owner(ie - 1, total, runs) - (int)blockIdx.x;
+          k.slot = x.slot, k.rows = x.rows, k.out = x.out;
+          parts.cuts[blockIdx.x] = k;
+        }
+      }
+      // the cursor behind the batch: its last lane's unit, one further
+      const int l = cnt - 1;
+      b = __shfl_sync(0xffffffffu, bb, l), ti = __shfl_sync(0xffffffffu, tt, l), c = __shfl_sync(0xffffffffu, cc, l) + 1;
+      r = latent_req<N>(A, b);
+      if (u + cnt < end && c == latent_units<N>(A, r, ti)) {
+        c = 0;
+        if (++ti == r.tiles) {
+          ti = 0;
+          do r = latent_req<N>(A, ++b);
+          while (r.tiles == 0 && b + 1 < A.g.B);
+        }
+      }
+      at = 0;
+    };
+    int pair = 0, rope = 0, code = 0;
+    uint32_t pair_ph = 0, rope_ph = 0, code_ph = 0;
+    bool ok = true;
+    for (int n = 0; n < count && ok; ++n) {
+      if (at == cnt) batch(begin + n);
+      const int us = n % kUnits;
+      ok = warp_wait(&u_empty[us], ((n / kUnits) & 1) ^ 1, abort, A.err);
+      if (!ok) break;
+      if (lane == at) {
+        s_unit[us] = x;
+        s_bad[us][0] = s_bad[us][1] = 0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&u_full[us]));
+      const int pg = __shfl_sync(0xffffffffu, page, at++);
+      ok = warp_wait(&rope_empty[rope], rope_ph ^ 1, abort, A.err);
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&rope_full[rope]);
+        if (pg >= 0) {
+          mbar_arrive_expect_tx(bar, kRopeBytes);
+          if (kRecord) tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, 0, pg);
+          else tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        if (kRecord) {
+          ok = warp_wait(&code_empty[code], code_ph ^ 1, abort, A.err);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&code_full[code]);
+            if (pg >= 0) {
+              mbar_arrive_expect_tx(bar, kCodeStage + (j == 0 ? 1024 : 0));
+              tma_load_3d(smem_u32(code_buf + code * kCodeStage), &map_pair, bar, 128 * j, 0, pg);
+              if (j == 0)
+                bulk_load(smem_u32(scale_buf + (n % kScaleSlots) * 256), A.kv + (int64_t)pg * kRecPageBytes + kRecScalesAt, 1024, bar);
+            } else {
+              mbar_arrive(bar);
+            }
+          }
+          if (++code == S::kCodes) code = 0, code_ph ^= 1u;
+        } else {
+          ok = warp_wait(&pair_empty[pair], pair_ph ^ 1, abort, A.err);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&pair_full[pair]);
+            if (pg >= 0) {
+              mbar_arrive_expect_tx(bar, kPairBytes);
+              tma_load_3d(smem_u32(pair_buf + pair * kPairBytes), &map_pair, bar, 0, pg * kPage, 2 * j);
+            } else {
+              mbar_arrive(bar);
+            }
+          }
+          if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
+        }
+      }
+      if (ok && lane == 0) mbar_arrive(smem_u32(&u_loaded[us]));
+    }
+    // Copies in flight land before shared memory is given back: every slot's last copy is waited
+    // for by its reader, or, when the run was given up, here.
+    if (!ok) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {}
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t idesc_s = make_idesc(64, kPage, kFmtBF16, kFmtBF16, 0, 0);
+    constexpr uint32_t idesc_o = make_idesc(128, N, kFmtBF16, kFmtBF16, 1, 0);
+    const uint64_t dq = smem_desc(smem_u32(q_buf), 0, 1024, kSwizzle128B);
+    const uint64_t dk = smem_desc(smem_u32(pair_buf), 0, 1024, kSwizzle128B);
+    const uint64_t dv = smem_desc(smem_u32(pair_buf), kPage * 128, 1024, kSwizzle128B);
+    const uint64_t dr = smem_desc(smem_u32(rope_buf), 0, 1024, kSwizzle128B);
+    const uint64_t dp = smem_desc(smem_u32(p_buf), 0, 1024, kSwizzle128B);
+    const bool issuer = elect_one();
+    bool ok = tmem == 0;                          // all 512 columns are this block's
+    if (!ok) {
+      *abort = 1;
+      record_error(A.err, kDevTimeout);
+    }
+    int sp = 0, vp = 0, rope = 0, edges = 0;      // pair slots of the scores and of the values
+    uint32_t sp_ph = 0, rope_ph = 0, q_ph = 0;
+    auto load_q = [&](int us) {
+      if (issuer) {
+        const uint32_t bar = smem_u32(&q_full);
+        mbar_arrive_expect_tx(bar, S::kQBytes);
+        tma_load_3d(smem_u32(q_buf), &map_q, bar, 0, (int)s_unit[us].out, 0);
+      }
+      __syncwarp();
+    };
+    // the scores of unit n against pairs j0 .. j1 - 1 (before the first also the rotated part)
+    auto scores = [&](int n, int j0, int j1) {
+      const uint32_t d = kSCol + (n & 1) * kPage;
+      if (j0 == 0) {
+        if (!warp_wait(&rope_full[rope], rope_ph, abort, A.err)) return false;
+        tc_fence_after();
+        if (issuer) {
+          const uint64_t kd = desc_add(dr, rope * kRopeBytes), qd = desc_add(dq, 8 * N * 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc_s, k != 0);
+          mma_commit(smem_u32(&rope_empty[rope]));
+        }
+        __syncwarp();
+        if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
+      }
+#pragma unroll 1
+      for (int j = j0; j < j1; ++j) {
+        if (!warp_wait(&pair_full[sp], sp_ph, abort, A.err)) return false;
+        if (!kRecord && j == 0 && (s_unit[n % kUnits].flags & kEdge)) {   // (records: the conversion has done it)
+          if (!warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err)) return false;
+          ++edges;
+        }
+        tc_fence_after();
+        if (issuer) {
+          const uint64_t kd = desc_add(dk, sp * kPairBytes), qd = desc_add(dq, 2 * j * N * 128);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_ss(d, desc_add(qd, (k >> 2) * N * 128 + (k & 3) * 32), desc_add(kd, (k >> 2) * (kPage * 128) + (k & 3) * 32),
+                       idesc_s, 1);
+          if (j == 3) mma_commit(smem_u32(&s_full[n & 1]));
+        }
+        __syncwarp();
+        if (++sp == S::kPairs) sp = 0, sp_ph ^= 1u;
+      }
+      return true;
+    };
+    uint32_t fresh = 0;                           // unit n begins a segment
+    for (int n = -1; n < count && ok; ++n) {
+      bool next = false, later = false;           // unit n + 1 begins a segment; its scores wait for n's values
+      if (n + 1 < count) {
+        ok = warp_wait(&u_full[(n + 1) % kUnits], ((n + 1) / kUnits) & 1, abort, A.err);
+        if (!ok) break;
+        next = (s_unit[(n + 1) % kUnits].flags & kFirst) != 0;
+        if (!next) {
+          ok = scores(n + 1, 0, S::kEarly);
+          later = S::kEarly < 4;
+          if (!ok) break;
+        }
+      }
+      if (n >= 0) {
+        ok = warp_wait(&p_full, n & 1, abort, A.err);
+        if (!ok) break;
+        tc_fence_after();
+        // unit n's scores are done (their softmax is), so the queries may be replaced
+        if (next) load_q((n + 1) % kUnits);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          if (issuer) {
+            const uint64_t vd = desc_add(dv, vp * kPairBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(dp, k * 32), idesc_o, k != 0 ? 1u : fresh ^ 1u);
+            mma_commit(smem_u32(&pair_empty[vp]));
+          }
+          __syncwarp();
+          if (++vp == S::kPairs) vp = 0;
+        }
+        if (issuer) mma_commit(smem_u32(&o_done));
+        __syncwarp();
+      } else if (next) {
+        load_q(0);
+      }
+      if (next) {
+        ok = warp_wait(&q_full, q_ph, abort, A.err);
+        q_ph ^= 1u;
+        if (ok) ok = scores(n + 1, 0, 4);
+      } else if (later) {
+        ok = scores(n + 1, S::kEarly, 4);
+      }
+      fresh = next ? 1u : 0u;
+    }
+    // Everything issued has finished before tensor and shared memory are given back.
+    __syncwarp();
+    if (issuer) {
+      mma_commit(smem_u32(&drain));
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&drain), 0)) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          *abort = 1;
+          record_error(A.err, kDevTimeout);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kFixWarp0) {
+    const int ct = tid - 32 * kFixWarp0;
+    if constexpr (kRecord) {
+      // ---------------------------------------------------------- conversion
+      int pair = 0, code = 0;
+      uint32_t pair_ph = 0, code_ph = 0;
+      bool ok = true;
+      for (int n = 0; n < count && ok; ++n) {
+        const int us = n % kUnits;
+        ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
+        if (!ok) break;
+        const bool edge = (s_unit[us].flags & kEdge) != 0;
+        const int last = s_unit[us].last;
+        const float* scales = scale_buf + (n % kScaleSlots) * 256;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          ok = warp_wait(&code_full[code], code_ph, abort, A.err) && warp_wait(&pair_empty[pair], pair_ph ^ 1, abort, A.err);
+          if (!ok) break;
+          const uint8_t* src = code_buf + code * kCodeStage;
+          uint8_t* dst = pair_buf + pair * kPairBytes;
+          // eight codes a thread: half a warp reads a row's 128, and eight threads write a row of an atom
+          constexpr int kPieces = kPage * 16 / (32 * S::kFixWarps);
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int piece = ct + i * 32 * S::kFixWarps, row = piece >> 4, ch = piece & 15;
+            const uint2 w = *reinterpret_cast<const uint2*>(src + row * 128 + ch * 8);
+            const float sc = scales[row * 4 + j];
+            uint32_t o[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a, b2;
+              codes_f16<KV == kKvInt8>(h ? w.y : w.x, a, b2);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+              const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b2));
+              const float2 s2 = make_float2(sc, sc);
+              const float2 x = __fmul2_rn(f, s2), y = __fmul2_rn(g, s2);
+              o[2 * h] = pack_bf16(x.x, x.y), o[2 * h + 1] = pack_bf16(y.x, y.y);
+            }
+            if (edge) {
+              bool bad = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) bad |= (o[e] & 0x7F80u) == 0x7F80u || (o[e] & 0x7F800000u) == 0x7F800000u;
+              if (bad && row <= last) atomicOr(&s_bad[us][row >> 5], 1u << (row & 31));
+              if (bad || row > last) o[0] = o[1] = o[2] = o[3] = 0;
+            }
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kPage * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&pair_full[pair]));
+            mbar_arrive(smem_u32(&code_empty[code]));
+            if (j == 3) mbar_arrive(smem_u32(&u_empty[us]));
+          }
+          if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
+          if (++code == S::kCodes) code = 0, code_ph ^= 1u;
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- pages not seen whole
+      int pair = 0, edges = 0;
+      uint32_t pair_ph = 0;
+      bool ok = true;
+      for (int n = 0; n < count && ok; ++n) {
+        const int us = n % kUnits;
+        // (the unit's loads have been issued, so its slots' barriers are in this unit's phase)
+        ok = warp_wait(&u_loaded[us], (n / kUnits) & 1, abort, A.err);
+        if (!ok) break;
+        const bool edge = (s_unit[us].flags & kEdge) != 0;
+        const int last = s_unit[us].last;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          if (edge) {
+            ok = ok && warp_wait(&pair_full[pair], pair_ph, abort, A.err);
+            if (!ok) break;
+            uint8_t* dst = pair_buf + pair * kPairBytes;
+            // (a row's eight chunks of an atom by eight threads: the swizzle permutes within the row)
+#pragma unroll 2
+            for (int i = ct; i < 2 * kPage * 8; i += 32 * S::kFixWarps) {
+              const int row = (i >> 3) & (kPage - 1);
+              uint4* p = reinterpret_cast<uint4*>(dst) + i;
+              const uint4 v = *p;
+              const uint32_t o[4] = {v.x, v.y, v.z, v.w};
+              bool bad = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) bad |= (o[e] & 0x7F80u) == 0x7F80u || (o[e] & 0x7F800000u) == 0x7F800000u;
+              if (bad && row <= last) atomicOr(&s_bad[us][row >> 5], 1u << (row & 31));
+              if (bad || row > last) *p = make_uint4(0, 0, 0, 0);
+            }
+          }
+          if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
+        }
+        if (!ok) break;
+        if (edge) fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (edge) mbar_arrive(smem_u32(&e_full[edges % kUnits]));
+          mbar_arrive(smem_u32(&u_empty[us]));
+        }
+        if (edge) ++edges;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const bool active = 16 * warp < N;
+    const uint32_t quarter = tmem + ((uint32_t)(32 * warp) << 16);
+    const int r0 = 16 * warp + (lane >> 2);       // this thread's rows: r0 and r0 + 8
+    const float f = fmaxf(A.scale_log2, 1.17549435e-38f);   // (a scale of 0 would make masked scores NaN)
+    float M[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+    bool ok = true;
+    for (int n = 0; n < count; ++n) {
+      const int us = n % kUnits;
+      ok = ok && warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
+      LatentUnit x{};
+      if (ok) x = s_unit[us];
+      if (x.flags & kFirst) M[0] = M[1] = kNone, l[0] = l[1] = 0.f;
+      ok = ok && warp_wait(&s_full[n & 1], (n >> 1) & 1, abort, A.err);
+      float s[32];
+      bool need = false;
+      float top[2] = {-INFINITY, -INFINITY};
+      if (active && ok) {
+        tc_fence_after();
+        tmem_ld_16x64(quarter + kSCol + (n & 1) * kPage, s);
+        tmem_ld_wait();
+        if (x.flags & kEdge) {
+          const uint64_t bad = (uint64_t)s_bad[us][0] | (uint64_t)s_bad[us][1] << 32;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = r0 + 8 * i;
+            const int lim = row < x.rows && !(x.flags & kVoid) ? x.rel + (x.row0 + row) / A.H : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = 8 * j + 2 * (lane & 3) + e;
+                float& v = s[4 * j + 2 * i + e];
+                if (key > lim) v = -INFINITY;
+                else if (bad >> key & 1) v = NAN;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float m = fmaxf(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+          for (int j = 1; j < 8; ++j) m = max3(m, s[4 * j + 2 * i], s[4 * j + 2 * i + 1]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          top[i] = m * f;
+          if (x.flags & kFirst) M[i] = fmaxf(top[i], kNone);
+          else need |= r0 + 8 * i < x.rows && top[i] > M[i] + kMove;
+        }
+      }
+      // (all four warps come here in every round, those that gave up too)
+      if (bar_any(1, 128, need || !ok)) {
+        if (active && ok) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float keep = 1.f;
+            if (top[i] > M[i] + kMove) keep = ex2(M[i] - top[i]), M[i] = top[i], l[i] *= keep;
+            if ((lane & 3) == 0) s_keep[r0 + 8 * i] = keep;
+          }
+        }
+        if (!bar_all(1, 128, ok)) break;
+        if (!(x.flags & kFirst)) {                // O so far, once its last product is done
+          ok = warp_wait(&o_done, (n - 1) & 1, abort, A.err);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < 4 * N; k += 16) {
+              float v[16];
+              tmem_ld16(quarter + k, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] *= s_keep[(k + j) % N];
+              tmem_st16(quarter + k, v);
+            }
+            tmem_st_wait();
+          }
+        }
+      }
+      uint32_t p[16];
+      if (active && ok) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float a = 0.f, c = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float u = ex2(fmaf(s[4 * j + 2 * i], f, -M[i])), w = ex2(fmaf(s[4 * j + 2 * i + 1], f, -M[i]));
+            a += u, c += w;
+            p[2 * j + i] = pack_bf16(u, w);
+          }
+          l[i] += a + c;
+        }
+      }
+      // the last page's values have left P's place
+      if (n > 0) ok = ok && warp_wait(&o_done, (n - 1) & 1, abort, A.err);
+      if (active && ok) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = r0 + 8 * i;
+          uint8_t* dst = p_buf + row * 128 + 4 * (lane & 3);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) *reinterpret_cast<uint32_t*>(dst + ((j ^ (row & 7)) << 4)) = p[2 * j + i];
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full));
+      if (x.flags & kLast) {
+        // ---- the segment's outputs, or its part
+        if (active && ok) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            if ((lane & 3) == 0) s_max[r0 + 8 * i] = M[i], s_sum[r0 + 8 * i] = l[i];
+          }
+        }
+        if (!bar_all(1, 128, ok)) break;
+        ok = warp_wait(&o_done, n & 1, abort, A.err);
+        if (ok) {
+          tc_fence_after();
+          const int t = warp * 32 + lane;
+          if (t < x.rows) {
+            const float sum = s_sum[t], mx = s_max[t];
+            if (x.slot >= 0) *reinterpret_cast<float2*>(parts.ml + ((int64_t)x.slot * N + t) * 2) = make_float2(mx, sum);
+            else if (A.lse) A.lse[x.out + t] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+          }
+#pragma unroll 1
+          for (int k = 0; k < 4 * N; k += 16) {
+            float v[16];
+            tmem_ld16(quarter + k, v);
+            tmem_ld_wait();
+            const int dim = k / N * 128 + t, row = k % N;
+            if (x.slot >= 0) {
+              float* dst = parts.o + ((int64_t)x.slot * N + row) * kDimLatent + dim;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (row + j < x.rows) dst[(int64_t)j * kDimLatent] = v[j];
+            } else {
+              // neighbouring lanes share two rows: the even one writes both columns of the first
+              __nv_bfloat16* dst = A.out + (x.out + row + (lane & 1)) * kDimLatent + (dim & ~1);
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float s0 = s_sum[row + j], s1 = s_sum[row + j + 1];
+                const float a = s0 == 0.f ? 0.f : v[j] / s0, c = s1 == 0.f ? 0.f : v[j + 1] / s1;
+                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : c, 1);
+                if (row + j + (lane & 1) < x.rows)
+                  *reinterpret_cast<uint32_t*>(dst + (int64_t)j * kDimLatent) = lane & 1 ? pack_bf16(other, c) : pack_bf16(a, other);
+              }
+            }
+          }
+          tc_fence_before();
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&u_empty[us]));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// Query rows of an item: as many as a request has in the mean, up to 64 (more rows a page read).
+int latent_rows(const GeomDev& g, int H) {
+  const int64_t rows = ((int64_t)g.T + g.B - 1) / g.B * H;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+template <int N, int KV>
+cudaError_t launch(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st) {
+  using S = LatentShape<N, KV>;
+  const LatentParts parts = latent_parts(A.scratch, num_sms, N, kDimLatent);
+  auto kern = latent_attend_kernel<N, KV>;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(kern, S::kSmem, allowed);
+  if (e != cudaSuccess) return e;
+  kern<<<num_sms, S::kThreads, S::kSmem, st>>>(m.q, m.pair, m.rope, A, parts);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : latent_merge_launch<kDimLatent>(parts, num_sms, A.out, A.lse, st);
+}
+template <int KV>
+cudaError_t launch_rows(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st) {
+  switch (latent_rows(A.g, A.H)) {
+    case 16: return launch<16, KV>(A, m, num_sms, st);
+    case 32: return launch<32, KV>(A, m, num_sms, st);
+    default: return launch<64, KV>(A, m, num_sms, st);
+  }
+}
+
+}  // namespace
+
+int latent_attend_rows(const GeomDev& g, int H) { return latent_rows(g, H); }
+
+// Enough for any smaller T as well: a buffer sized for a batch's largest step serves its others.
+size_t latent_attend_scratch_bytes(const dsa_geom_t* g, int H, int num_sms) {
+  GeomDev gd{};
+  gd.B = g->B, gd.T = g->T;
+  return latent_parts_bytes(num_sms, latent_rows(gd, H), kDimLatent);
+}
+
+cudaError_t latent_attend_launch(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st) {
+  switch (A.kv_format) {
+    case kKvBf16: return launch_rows<kKvBf16>(A, m, num_sms, st);
+    case kKvE4m3: return launch_rows<kKvE4m3>(A, m, num_sms, st);
+    default: return launch_rows<kKvInt8>(A, m, num_sms, st);
+  }
+}
+
+}  // namespace dsa

@@ -1,0 +1,125 @@
+// What the dense latent-attention kernels share (latent_*.cu; entry points in latent_api.cu).
+#pragma once
+#include <cstdint>
+#include "gqa_common.cuh"
+
+namespace dsa {
+
+// Partial results of cut items, in the workspace: two slots a run, `rows` rows of `width` each.
+// Item i's first part lies in run c's slot `slot`, the next `follow` runs each hold one in slot 0.
+struct __align__(16) LatentCut { int follow, slot, rows, pad; int64_t out, pad2; };   // out: first output row
+struct LatentParts {
+  int rows, width;
+  LatentCut* cuts;   // one per run
+  float* ml;         // [2 * runs, rows, 2] running maximum (log2 units) and sum
+  float* o;          // [2 * runs, rows, width]
+};
+inline size_t latent_parts_bytes(int runs, int rows, int width) {
+  return align_up(sizeof(LatentCut) * runs, 256) + align_up((size_t)2 * runs * rows * 2 * sizeof(float), 256) +
+         (size_t)2 * runs * rows * width * sizeof(float);
+}
+inline LatentParts latent_parts(void* scratch, int runs, int rows, int width) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(scratch);
+  LatentParts s;
+  s.rows = rows, s.width = width;
+  s.cuts = reinterpret_cast<LatentCut*>(p);
+  p += align_up(sizeof(LatentCut) * runs, 256);
+  s.ml = reinterpret_cast<float*>(p);
+  s.o = reinterpret_cast<float*>(p + align_up((size_t)2 * runs * rows * 2 * sizeof(float), 256));
+  return s;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Barrier `id` among `count` threads that also tells whether any / all of them say so.
+__device__ __forceinline__ bool bar_any(int id, int count, bool p) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"((uint32_t)p), "r"(id), "r"(count)
+               : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool bar_all(int id, int count, bool p) { return !bar_any(id, count, !p); }
+
+// 16 lanes x 64 columns, spread over the warp: thread i gets rows i / 4 (v[4j], v[4j+1]) and
+// i / 4 + 8 (v[4j+2], v[4j+3]), columns 8j + 2 (i % 4) and the next.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Merges the parts of cut items in the order of the runs: block (c, r) looks whether run c holds
+// an item's first part, and if so merges its row r; each thread has WIDTH / 128 values.
+template <int WIDTH>
+__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentParts s, __nv_bfloat16* out, float* lse) {
+  constexpr int V = WIDTH / 128;
+  griddep_wait();
+  const LatentCut k = s.cuts[blockIdx.x];
+  const int row = blockIdx.y;
+  if (k.follow <= 0 || row >= k.rows) return;
+  float M = kNone, l = 0.f, o[V] = {};
+  constexpr int kBatch = 4;                        // parts whose loads are in flight together
+  for (int p0 = 0; p0 <= k.follow; p0 += kBatch) {
+    float2 ml[kBatch];
+    float v[kBatch][V];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int p = min(p0 + i, k.follow);
+      const int64_t at = (p == 0 ? (int64_t)k.slot : 2 * (int64_t)(blockIdx.x + p)) * s.rows + row;
+      ml[i] = __ldcg(reinterpret_cast<const float2*>(s.ml + at * 2));
+      const float* src = s.o + at * WIDTH + threadIdx.x * V;
+      if constexpr (V == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+      } else {
+        v[i][0] = __ldcg(src);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (p0 + i > k.follow) break;
+      const float Mn = fmaxf(M, ml[i].x), a = ex2(M - Mn), b = ex2(ml[i].x - Mn);
+      M = Mn;
+      l = l * a + ml[i].y * b;
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = o[j] * a + v[i][j] * b;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* dst = out + (k.out + row) * WIDTH + threadIdx.x * V;
+  if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+  } else {
+    *dst = __float2bfloat16_rn(o[0] * inv);
+  }
+  if (lse && threadIdx.x == 0) lse[k.out + row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int WIDTH>
+inline cudaError_t latent_merge_launch(const LatentParts& s, int runs, __nv_bfloat16* out, float* lse, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(runs, s.rows);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<WIDTH>, s, out, lse);
+}
+
+}  // namespace dsa

@@ -492,6 +492,98 @@ dsa_status_t dsa_gqa_attend_blocks(const dsa_geom_t* geom, const dsa_gqa_cache_t
 size_t dsa_gqa_attend_blocks_workspace_size(const dsa_geom_t* geom, const dsa_gqa_cache_t* cache, int32_t H,
                                             int32_t n_sel);
 
+/*
+ * Dense latent attention: the layers, contexts and prompts that attend to every cached
+ * row instead of a selection, over the same paged latent cache (kv_cache as for
+ * dsa_sparse_mla_attend, in all three kv_dtypes; the value of a record is code*scale rounded
+ * to bf16). Padding rows, tokens at negative positions, inconsistent requests and bad page
+ * ids are treated as the grouped-query operators treat them.
+ */
+
+/* Rotary frequencies: position p turns pair i by p * turns[i] / 2^64 of a full turn.
+ * Filled by dsa_rope_init and kept by the caller (host memory). */
+typedef struct {
+  int32_t dim;          /* rotated values at the front of the 64: 16, 32, 48 or 64 */
+  int32_t interleaved;  /* pairs (2i, 2i+1); else (i, i + dim/2) */
+  float scale;          /* factor of every sine and cosine */
+  int32_t reserved;
+  uint64_t turns[32];
+} dsa_rope_t;
+
+/*
+ * dsa_rope_init -- frequencies f_i = base^(-2i/dim), scaled for contexts longer than the
+ *   model was made for (host only, enqueues nothing).
+ *   original_len 0: every f_i divided by factor (1: unscaled). original_len > 0: with
+ *   d(x) = dim * ln(original_len / (2 pi x)) / (2 ln base) the pair that turns x times over the
+ *   original length, lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), dim - 1) and
+ *   r_i = (i - lo) / max(hi - lo, 0.001) cut to [0, 1]: f_i * (1 - r_i) + f_i / factor * r_i.
+ *   In 64 bits; base > 1, factor >= 1, beta_fast >= beta_slow > 0 (ignored where original_len is
+ *   0), scale finite.
+ */
+dsa_status_t dsa_rope_init(dsa_rope_t* rope, int32_t dim, int32_t interleaved, float base, float factor,
+                           int64_t original_len, float beta_fast, float beta_slow, float scale);
+
+/*
+ * dsa_latent_append -- the new tokens' latent rows, from the projection's output into their
+ *   pages, and the rotated part of their queries, in one launch.
+ *   kv_in bf16, token t's 576 values at t*kv_stride (in elements, a multiple of 8, >= 576;
+ *     16-byte aligned): with x its first 512, y = x * r * gamma, r = (mean(x^2) + eps)^-1/2 in
+ *     fp32 from a sum that is held to 2^-46 (squares below 2^-126 count as 0, values from 2^59 up
+ *     are not meant), the product rounded after each factor; gamma [512] fp32 (16-byte aligned)
+ *     or NULL for 1; eps >= 0. The last 64 are rotated at the token's position:
+ *     u = a*c - b*s, v = b*c + a*s of each pair (a, b), c and s times rope->scale, in fp32, and
+ *     rounded to bf16; values from rope->dim on pass through.
+ *   The row goes to its page: DSA_BF16 y rounded to bf16; DSA_E4M3 / DSA_I8 codes and scales of
+ *     y as dsa_cache_append forms them (from y in fp32, not from its bf16 rounding).
+ *   kv_out [T, 576] bf16 contiguous, or NULL: the row in bf16 whatever the cache's type (what a
+ *     prompt's expanding projection takes).
+ *   q_in, q_out bf16: the 64 values of token t's head h at t*token + h*head (strides in
+ *     elements, multiples of 8, >= 64; 16-byte aligned): q_out = bf16(rotated q_in). q_out may be
+ *     q_in itself with the same strides (in place); otherwise outputs overlap no input. Both
+ *     NULL: rows alone. kv_in NULL (then kv_cache and kv_out too): queries alone. 1 <= H <= 128.
+ *   A token at a negative position is not stored; its kv_out and q_out are as at position 0.
+ *   Two requests of a call must not append to the same row. ws: 256 bytes (the header).
+ */
+dsa_status_t dsa_latent_append(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, const void* kv_in, int64_t kv_stride,
+                               const float* gamma, float eps, const dsa_rope_t* rope, void* kv_cache, void* kv_out,
+                               int32_t H, const void* q_in, int64_t q_in_token, int64_t q_in_head, void* q_out,
+                               int64_t q_out_token, int64_t q_out_head, void* ws, size_t ws_bytes, void* stream);
+size_t dsa_latent_append_workspace_size(const dsa_geom_t* geom);
+
+/*
+ * dsa_latent_attend -- causal attention in the absorbed form over the whole context.
+ *   q [T, H, 576] bf16 (the absorbed query), 1 <= H <= 128.
+ *   z_s = sm_scale * q . kv_s (576 wide) over the rows s <= pos(t):
+ *     out [T, H, 512] bf16 = sum_s softmax(z)_s * kv_s[0:512]; lse [T, H] fp32 (or NULL) =
+ *     ln(sum_s exp(z_s)). A row that sees no key gives out = 0 and lse = -inf. What lies in a
+ *     latent row that a query does not see (NaN, infinities, pages of other requests) does not
+ *     reach it; a NaN or infinity that it sees makes its outputs NaN (an infinity that meets
+ *     queries of the other sign possibly in its own column only). out overlaps no input.
+ *   Weights are rounded to bf16 before they meet the rows; all sums are fp32; out is
+ *     rounded once more, to bf16.
+ *   sm_scale >= 0, and sm_scale * log2(e) finite in fp32. T * H < 2^31.
+ */
+dsa_status_t dsa_latent_attend(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, int32_t H, const void* q,
+                               const void* kv_cache, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                               void* stream);
+/* Never less for a larger T with the other sizes as they are. */
+size_t dsa_latent_attend_workspace_size(const dsa_geom_t* geom, int32_t H);
+
+/*
+ * dsa_latent_gather -- rows of the paged cache one after another in bf16, records dequantised:
+ *   the input of the projection that expands them by head.
+ *   cu_k [B+1] int32 (device): request b's rows are out's cu_k[b] .. cu_k[b+1]-1, its positions
+ *     first[b] + 0, 1, ... (first [B] int32, or NULL for 0). geom->cu_q and T are not used.
+ *   out: row s at s*out_stride (in elements, a multiple of 8, >= 576), 576 bf16, for s < S; rows
+ *     from cu_k[B] on are left as they were. A position outside the request's seq_lens or
+ *     a bad page id gives a row of zeros and sets DSA_ERR_BAD_INDEX.
+ *   ws: 256 bytes (the header).
+ */
+dsa_status_t dsa_latent_gather(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, const void* kv_cache, const int32_t* first,
+                               const int32_t* cu_k, int32_t S, void* out, int64_t out_stride, void* ws, size_t ws_bytes,
+                               void* stream);
+size_t dsa_latent_gather_workspace_size(const dsa_geom_t* geom);
+
 /* Synchronizes `stream`, reads the device error word of `ws` (DSA_OK if none)
  * and clears it. Returns DSA_ERR_CUDA if the stream itself reports an error. */
 dsa_status_t dsa_get_error(void* ws, void* stream);
