@@ -32,6 +32,7 @@ EXPORTED = (
     "dsa_gqa_attend_blocks", "dsa_gqa_attend_blocks_workspace_size",
     "dsa_rope_init", "dsa_latent_append", "dsa_latent_append_workspace_size",
     "dsa_latent_attend", "dsa_latent_attend_workspace_size", "dsa_latent_gather", "dsa_latent_gather_workspace_size",
+    "dsa_latent_attend_expanded", "dsa_latent_attend_expanded_workspace_size",
     "dsa_get_error", "dsa_clear_error", "dsa_wait_probe", "dsa_status_string", "dsa_last_error", "dsa_abi_version",
 )
 
@@ -127,6 +128,9 @@ def load(path: str = LIB_PATH):
         "dsa_latent_attend_workspace_size": (SZ, [G, I32]),
         "dsa_latent_gather": (C.c_int, [G, C.c_int, P, P, P, I32, P, I64, P, SZ, P]),
         "dsa_latent_gather_workspace_size": (SZ, [G]),
+        "dsa_latent_attend_expanded": (C.c_int, [I32, I32, I32, P, P, I32, P, I64, I64, P, I64, I64, P, I64, I64, P, I64, F, P, P,
+                                                 P, SZ, P]),
+        "dsa_latent_attend_expanded_workspace_size": (SZ, [I32, I32, I32, I32]),
         "dsa_get_error": (C.c_int, [P, P]),
         "dsa_clear_error": (C.c_int, [P, P]),
         "dsa_wait_probe": (C.c_int, [P, SZ, C.c_uint32, P]),
@@ -612,6 +616,31 @@ def dsa_latent_gather(geom: Geometry, kv_dtype: int, kv_cache, first, cu_k, out,
     s = load().dsa_latent_gather(geom.ref, kv_dtype, cache, fp, cp, out.shape[0], op, os_, ws.data_ptr(), ws.numel(), st)
     if s:
         raise DsaError(s, "dsa_latent_gather")
+
+
+def dsa_latent_attend_expanded_workspace_size(B: int, T: int, S: int, H: int) -> int:
+    return int(load().dsa_latent_attend_expanded_workspace_size(int(B), int(T), int(S), int(H)))
+
+
+def dsa_latent_attend_expanded(cu_q, cu_k, q, k, v, k_rope, sm_scale: float, out, lse, ws, stream=None):
+    """Causal attention of q [T, H, 192] over expanded keys k [S, H, 128] with the rotated parts
+    k_rope [S, 64] of all heads and values v [S, H, 128], ragged by cu_q and cu_k [B+1], into out
+    [T, H, 128] bf16 and lse [T, H] fp32 (or None). q, k, v and k_rope may be strided views."""
+    index = cu_q.get_device()
+    st = _latent_call(ws, stream, index)
+    B, (T, H), S = cu_q.shape[0] - 1, q.shape[:2], k.shape[0]
+    cq, = _tensor("cu_q", cu_q, _I32, (B + 1,), index)
+    ck, = _tensor("cu_k", cu_k, _I32, (B + 1,), index)
+    qp, qt, qh = _tensor("q", q, _BF16, (T, H, 192), index)
+    kp, kt, kh = _tensor("k", k, _BF16, (S, H, 128), index)
+    vp, vt, vh = _tensor("v", v, _BF16, (S, H, 128), index)
+    rp, rt = _tensor("k_rope", k_rope, _BF16, (S, 64), index)
+    op, = _tensor("out", out, _BF16, (T, H, 128), index, 3)
+    lp = None if lse is None else _tensor("lse", lse, _F32, (T, H), index, 2)[0]
+    s = load().dsa_latent_attend_expanded(B, T, S, cq, ck, H, qp, qt, qh, kp, kt, kh, vp, vt, vh, rp, rt, sm_scale, op, lp,
+                                          ws.data_ptr(), ws.numel(), st)
+    if s:
+        raise DsaError(s, "dsa_latent_attend_expanded")
 
 
 def dsa_stage_copy(dst, src, nbytes: int, stream=None):

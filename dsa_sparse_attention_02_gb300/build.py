@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
 SOURCES = ["api.cu", "indexer.cu", "topk.cu", "sparse_mla.cu", "noalloc.cu", "cache_append.cu", "indexer_prep.cu", "stage_copy.cu", "wait_probe.cu",
            "gqa_api.cu", "gqa_append.cu", "gqa_select.cu", "gqa_attend.cu", "gqa_tiles.cu",
-           "latent_api.cu", "latent_rows.cu", "latent_attend.cu"]
+           "latent_api.cu", "latent_rows.cu", "latent_attend.cu", "latent_expanded.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

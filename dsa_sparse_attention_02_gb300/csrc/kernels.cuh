@@ -239,6 +239,20 @@ struct LatentAttendArgs {
 int latent_attend_rows(const GeomDev& g, int H);   // query rows of an item: the box of the queries' map
 size_t latent_attend_scratch_bytes(const dsa_geom_t* g, int H, int num_sms);
 cudaError_t latent_attend_launch(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st);
+struct LatentExpandedArgs {
+  int B, T, S, H;
+  const int* cu_q;              // [B + 1]
+  const int* cu_k;              // [B + 1]
+  float scale_log2;             // sm_scale * log2(e)
+  __nv_bfloat16* out;           // [T, H, 128]
+  float* lse;                   // [T, H] or null
+  void* scratch;
+  int min_run;                  // shortest run of units
+  int* err;
+};
+size_t latent_expanded_scratch_bytes(int num_sms);
+cudaError_t latent_expanded_launch(const LatentExpandedArgs& A, const CUtensorMap& q, const CUtensorMap& k,
+                                   const CUtensorMap& rope, const CUtensorMap& v, int num_sms, cudaStream_t st);
 
 // ---- host helpers defined in api.cu
 constexpr size_t kHeaderBytes = 256;   // workspace header: the error word comes first

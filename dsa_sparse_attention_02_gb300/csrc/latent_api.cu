@@ -176,4 +176,52 @@ dsa_status_t dsa_latent_attend(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, int
   return from_cuda(latent_attend_launch(A, m, num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t dsa_latent_attend_expanded_workspace_size(int32_t B, int32_t T, int32_t S, int32_t H) {
+  if (B < 1 || T < 1 || S < 0 || H < 1 || H > kMaxHeads) return kHeaderBytes;
+  return kHeaderBytes + align_up(latent_expanded_scratch_bytes(num_sms()), 256);
+}
+
+dsa_status_t dsa_latent_attend_expanded(int32_t B, int32_t T, int32_t S, const int32_t* cu_q, const int32_t* cu_k, int32_t H,
+                                        const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                                        int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                                        const void* k_rope, int64_t rope_token, float sm_scale, void* out, float* lse,
+                                        void* ws, size_t ws_bytes, void* stream) {
+  if (B < 0 || T < 0 || S < 0 || (T > 0 && B < 1) || H < 1 || H > kMaxHeads) return DSA_ERR_INVALID_ARG;
+  LatentExpandedArgs A{};
+  const float scale_log2 = sm_scale * 1.4426950408889634f;   // scores in powers of two
+  if (!std::isfinite(scale_log2) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
+  if (T > INT32_MAX - 65536 || S > INT32_MAX - 65536) return DSA_ERR_UNSUPPORTED;   // (rounded up to tiles in 32 bits)
+  if (!ws_ok(ws, ws_bytes, dsa_latent_attend_expanded_workspace_size(B, T, S, H))) return DSA_ERR_WORKSPACE;
+  if (T == 0) return DSA_OK;
+  if (!cu_q || !cu_k || !aligned4(cu_q) || !aligned4(cu_k) || !q || !out || !aligned16(q) || !aligned16(out) ||
+      (lse && !aligned4(lse)) || !stride_ok(q_token, 192) || !stride_ok(q_head, 192))
+    return DSA_ERR_INVALID_ARG;
+  if (S > 0 && (!k || !v || !k_rope || !aligned16(k) || !aligned16(v) || !aligned16(k_rope) || !stride_ok(k_token, 128) ||
+                !stride_ok(k_head, 128) || !stride_ok(v_token, 128) || !stride_ok(v_head, 128) || !stride_ok(rope_token, 64)))
+    return DSA_ERR_INVALID_ARG;
+  A.B = B, A.T = T, A.S = S, A.H = H;
+  A.cu_q = cu_q;
+  A.cu_k = cu_k;
+  A.scale_log2 = scale_log2;
+  A.out = reinterpret_cast<__nv_bfloat16*>(out);
+  A.lse = lse;
+  A.scratch = reinterpret_cast<uint8_t*>(ws) + kHeaderBytes;
+  A.min_run = 1;
+  A.err = reinterpret_cast<int*>(ws);
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t h = (uint64_t)H, t = (uint64_t)T, n = (uint64_t)S;
+  CUtensorMap mq, mk, mr, mv;
+  if (!encode_tensor_map_3d(&mq, bf16, q, {192, h, t}, {(uint64_t)q_head * 2, (uint64_t)q_token * 2}, {64, 1, 128}, true))
+    return DSA_ERR_CUDA;
+  if (S > 0) {
+    if (!encode_tensor_map_3d(&mk, bf16, k, {128, h, n}, {(uint64_t)k_head * 2, (uint64_t)k_token * 2}, {64, 1, 128}, true) ||
+        !encode_tensor_map_3d(&mv, bf16, v, {128, h, n}, {(uint64_t)v_head * 2, (uint64_t)v_token * 2}, {64, 1, 64}, true) ||
+        !encode_tensor_map_2d(&mr, bf16, k_rope, 64, n, (uint64_t)rope_token * 2, 64, 128))
+      return DSA_ERR_CUDA;
+  } else {
+    mk = mv = mr = mq;               // (no unit loads through them)
+  }
+  return from_cuda(latent_expanded_launch(A, mq, mk, mr, mv, num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

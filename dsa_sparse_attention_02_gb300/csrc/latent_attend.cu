@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         if (last && cut && ib >= begin) {
           LatentCut k{};
           k.follow = (int)split_owner(ie - 1, total, runs) - (int)blockIdx.x;
-          k.slot = x.slot, k.rows = x.rows, k.out = x.out;
+          k.slot = x.slot, k.rows = x.rows, k.step = 1, k.out = x.out;
           parts.cuts[blockIdx.x] = k;
         }
       }

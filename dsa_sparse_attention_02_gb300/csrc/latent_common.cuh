@@ -7,7 +7,7 @@ namespace dsa {
 
 // Partial results of cut items, in the workspace: two slots a run, `rows` rows of `width` each.
 // Item i's first part lies in run c's slot `slot`, the next `follow` runs each hold one in slot 0.
-struct __align__(16) LatentCut { int follow, slot, rows, pad; int64_t out, pad2; };   // out: first output row
+struct __align__(16) LatentCut { int follow, slot, rows, step; int64_t out, pad; };   // output rows out, out + step, ...
 struct LatentParts {
   int rows, width;
   LatentCut* cuts;   // one per run
@@ -61,32 +61,30 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Merges the parts of cut items in the order of the runs: block (c, r) looks whether run c holds
-// an item's first part, and if so merges its row r; each thread has WIDTH / 128 values.
+// Merges the parts of cut items in the order of the runs: block (c, y) looks whether run c holds
+// an item's first part, and if so merges eight of its rows, one a warp.
+constexpr int kLatentMergeWarps = 8;
+
 template <int WIDTH>
-__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentParts s, __nv_bfloat16* out, float* lse) {
-  constexpr int V = WIDTH / 128;
+__global__ void __launch_bounds__(32 * kLatentMergeWarps) latent_merge_kernel(const LatentParts s, __nv_bfloat16* out,
+                                                                              float* lse) {
+  constexpr int V = WIDTH / 128;                   // float4 pieces a lane has, 128 values apart
+  constexpr int kBatch = V == 1 ? 8 : 4;           // parts whose loads are in flight together
   griddep_wait();
   const LatentCut k = s.cuts[blockIdx.x];
-  const int row = blockIdx.y;
+  const int row = blockIdx.y * kLatentMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (k.follow <= 0 || row >= k.rows) return;
-  float M = kNone, l = 0.f, o[V] = {};
-  constexpr int kBatch = 4;                        // parts whose loads are in flight together
+  float M = kNone, l = 0.f, o[4 * V] = {};
   for (int p0 = 0; p0 <= k.follow; p0 += kBatch) {
     float2 ml[kBatch];
-    float v[kBatch][V];
+    float4 v[kBatch][V];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int p = min(p0 + i, k.follow);
       const int64_t at = (p == 0 ? (int64_t)k.slot : 2 * (int64_t)(blockIdx.x + p)) * s.rows + row;
       ml[i] = __ldcg(reinterpret_cast<const float2*>(s.ml + at * 2));
-      const float* src = s.o + at * WIDTH + threadIdx.x * V;
-      if constexpr (V == 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
-      } else {
-        v[i][0] = __ldcg(src);
-      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[i][j] = __ldcg(reinterpret_cast<const float4*>(s.o + at * WIDTH) + 32 * j + lane);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -95,24 +93,26 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const LatentParts s, 
       M = Mn;
       l = l * a + ml[i].y * b;
 #pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = o[j] * a + v[i][j] * b;
+      for (int j = 0; j < V; ++j) {
+        o[4 * j] = o[4 * j] * a + v[i][j].x * b, o[4 * j + 1] = o[4 * j + 1] * a + v[i][j].y * b;
+        o[4 * j + 2] = o[4 * j + 2] * a + v[i][j].z * b, o[4 * j + 3] = o[4 * j + 3] * a + v[i][j].w * b;
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* dst = out + (k.out + row) * WIDTH + threadIdx.x * V;
-  if constexpr (V == 4) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-  } else {
-    *dst = __float2bfloat16_rn(o[0] * inv);
-  }
-  if (lse && threadIdx.x == 0) lse[k.out + row] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+  const int64_t at = k.out + (int64_t)row * k.step;
+  uint2* dst = reinterpret_cast<uint2*>(out + at * WIDTH) + lane;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    dst[32 * j] = make_uint2(pack_bf16(o[4 * j] * inv, o[4 * j + 1] * inv), pack_bf16(o[4 * j + 2] * inv, o[4 * j + 3] * inv));
+  if (lse && lane == 0) lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int WIDTH>
 inline cudaError_t latent_merge_launch(const LatentParts& s, int runs, __nv_bfloat16* out, float* lse, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(runs, s.rows);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(runs, s.rows / kLatentMergeWarps);
+  cfg.blockDim = dim3(32 * kLatentMergeWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

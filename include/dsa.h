@@ -584,6 +584,32 @@ dsa_status_t dsa_latent_gather(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, con
                                void* stream);
 size_t dsa_latent_gather_workspace_size(const dsa_geom_t* geom);
 
+/*
+ * dsa_latent_attend_expanded -- causal attention over keys and values expanded by head, for
+ *   prompts: ragged keys in plain rows, no cache.
+ *   Request b has the query tokens cu_q[b] .. cu_q[b+1]-1 (of T) and the keys cu_k[b] ..
+ *   cu_k[b+1]-1 (of S; cu_q, cu_k [B+1] int32, device), the queries at the end: query j of n_q
+ *   sees keys 0 .. n_k - n_q + j.
+ *   q [T, H, 192] bf16: 128 values that meet the head's own key, then 64 that meet the rotated part;
+ *     k [S, H, 128], v [S, H, 128], k_rope [S, 64] (all heads') bf16. Token t's head h at
+ *     t*token + h*head, k_rope's row at s*rope_token (strides in elements, multiples of 8, token
+ *     and head each at least a head's width; 16-byte aligned): halves of one projection's output
+ *     and columns of latent rows are taken as they are. 1 <= H <= 128.
+ *   z_s = sm_scale * (q[0:128] . k_s + q[128:192] . k_rope_s):
+ *     out [T, H, 128] bf16 = sum_s softmax(z)_s * v_s, lse [T, H] fp32 (or NULL) = ln(sum_s exp(z_s)).
+ *   A row that sees no key gives out = 0 and lse = -inf; rows t >= cu_q[B] are left as they
+ *   were. A request whose cu_q or cu_k decreases or passes T or S sets DSA_ERR_BAD_INDEX, its rows
+ *   see no key. What lies in a key or value that a row does not see (NaN, infinities) does not
+ *   reach it; a NaN or infinity among the values that it sees gives NaN or an infinity in its column.
+ *   Rounding, sm_scale and overlaps as for dsa_latent_attend.
+ */
+dsa_status_t dsa_latent_attend_expanded(int32_t B, int32_t T, int32_t S, const int32_t* cu_q, const int32_t* cu_k, int32_t H,
+                                        const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                                        int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                                        const void* k_rope, int64_t rope_token, float sm_scale, void* out, float* lse,
+                                        void* ws, size_t ws_bytes, void* stream);
+size_t dsa_latent_attend_expanded_workspace_size(int32_t B, int32_t T, int32_t S, int32_t H);
+
 /* Synchronizes `stream`, reads the device error word of `ws` (DSA_OK if none)
  * and clears it. Returns DSA_ERR_CUDA if the stream itself reports an error. */
 dsa_status_t dsa_get_error(void* ws, void* stream);
