@@ -35,7 +35,6 @@ constexpr int kRopeBytes = kPage * 128;
 constexpr int kCodeStage = kPage * 128;      // a pair's codes
 constexpr int kScaleSlots = 4;
 constexpr int kMmaWarp = 4, kLoadWarp = 5, kFixWarp0 = 6;
-constexpr uint32_t kSCol = 256;              // O^T at 0, S at 256 and 320
 constexpr uint32_t kTmem = 512;
 constexpr float kMove = 8.f;                 // log2 of what a weight may pass the reference by
 enum : int { kEdge = 8 };                    // some row of the item does not see the whole page
@@ -54,14 +53,41 @@ struct LatentShape {
   // pairs that fit beside this page's (kEarly); the others follow its values.
   static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 64 ? 6 : 8);
   static constexpr int kRopes = !kRecord && N == 16 ? 3 : 2;
-  static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 3 : N == 32 ? 4 : 6;
+  static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 2 : N == 32 ? 4 : 6;
   static constexpr int kEarly = kPairs >= 8 ? 4 : kPairs - 4;
+  // Scores: a page's of bf16 rows in one place, two pages at a time; of records in one place for
+  // each scale (and the rotated part), in a ring. P: one of a page, or a ring of one for each scale.
+  static constexpr int kSlots = !kRecord ? 2 : N == 64 ? 4 : 6;
+  static constexpr uint32_t kSCol = !kRecord || N == 64 ? 256 : 128;
+  static constexpr int kPs = !kRecord ? 1 : N == 16 ? 4 : 2;
   static constexpr int kFixWarps = kRecord ? 8 : 4;
   static constexpr int kThreads = 32 * (kFixWarp0 + kFixWarps);
-  static constexpr int kQBytes = 9 * N * 128, kPBytes = N * 128;
-  static constexpr int kSmem = 1024 + kQBytes + kPBytes + kRopes * kRopeBytes + kPairs * kPairBytes + kCodes * kCodeStage +
+  static constexpr int kQBytes = 9 * N * 128, kPBytes = N * 128;   // of one P
+  static constexpr int kSmem = 1024 + kQBytes + kPs * kPBytes + kRopes * kRopeBytes + kPairs * kPairBytes + kCodes * kCodeStage +
                                (kRecord ? kScaleSlots * 1024 : 0);
+  static_assert(kSmem <= 227 * 1024 - 1536, "and barriers, units and row statistics beside it");
 };
+
+// bf16 pairs of a word's four codes, exact: (byte 0, byte 1) and (byte 2, byte 3).
+template <int KV>
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KV == kKvInt8) {
+    // 0x43vv is 128 + vv of the low seven bits, 0x4300 or 0x4380 (by the sign bit) 128 or 256
+    auto two = [](uint32_t x) {
+      const uint32_t v = (x & 0x007F007Fu) | 0x43004300u, s = (x & 0x00800080u) | 0x43004300u;
+      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&s));
+      return *reinterpret_cast<const uint32_t*>(&d);
+    };
+    lo = two(__byte_perm(w, 0, 0x4140));
+    hi = two(__byte_perm(w, 0, 0x4342));
+  } else {
+    uint32_t a, b;
+    codes_f16<false>(w, a, b);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    lo = pack_bf16(f.x, f.y), hi = pack_bf16(g.x, g.y);
+  }
+}
 
 // Requests as the items see them.
 struct LatentReq {
@@ -109,14 +135,15 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_buf = smem;                                  // (S reads 64 rows of each atom: up to 6 KB past the last)
   uint8_t* p_buf = q_buf + S::kQBytes;
-  uint8_t* rope_buf = p_buf + S::kPBytes;
+  uint8_t* rope_buf = p_buf + S::kPs * S::kPBytes;
   uint8_t* pair_buf = rope_buf + S::kRopes * kRopeBytes;
   uint8_t* code_buf = pair_buf + S::kPairs * kPairBytes;
   float* scale_buf = reinterpret_cast<float*>(code_buf + S::kCodes * kCodeStage);
   __shared__ uint64_t u_full[kUnits], u_loaded[kUnits], u_empty[kUnits], e_full[kUnits];
   __shared__ uint64_t pair_full[S::kPairs], pair_empty[S::kPairs], rope_full[S::kRopes], rope_empty[S::kRopes];
   __shared__ uint64_t code_full[kRecord ? S::kCodes : 1], code_empty[kRecord ? S::kCodes : 1];
-  __shared__ uint64_t q_full, s_full[2], p_full, o_done, drain;
+  __shared__ uint64_t scale_full[kRecord ? kScaleSlots : 1];
+  __shared__ uint64_t q_full, s_full[S::kSlots], s_empty[S::kSlots], p_full[S::kPs], p_empty[S::kPs], o_done[2], drain;   // o_done: of even and odd units
   __shared__ LatentUnit s_unit[kUnits];
   __shared__ uint32_t s_bad[kUnits][2];                   // keys with a value that is not finite
   __shared__ float s_keep[N], s_max[N], s_sum[N];
@@ -140,16 +167,24 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       mbar_init(smem_u32(&rope_full[i]), 1);
       mbar_init(smem_u32(&rope_empty[i]), 1);
     }
-    if (kRecord)
+    if (kRecord) {
+      for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&scale_full[i]), 1);
       for (int i = 0; i < S::kCodes; ++i) {
         mbar_init(smem_u32(&code_full[i]), 1);
         mbar_init(smem_u32(&code_empty[i]), S::kFixWarps);
       }
+    }
     mbar_init(smem_u32(&q_full), 1);
-    mbar_init(smem_u32(&s_full[0]), 1);
-    mbar_init(smem_u32(&s_full[1]), 1);
-    mbar_init(smem_u32(&p_full), 4);
-    mbar_init(smem_u32(&o_done), 1);
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_empty[i]), N / 16);
+    }
+    for (int i = 0; i < S::kPs; ++i) {
+      mbar_init(smem_u32(&p_full[i]), kRecord ? N / 16 : 4);
+      mbar_init(smem_u32(&p_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&o_done[0]), 1);
+    mbar_init(smem_u32(&o_done[1]), 1);
     mbar_init(smem_u32(&drain), 1);
     s_abort = 0;
     fence_mbar_init();
@@ -319,6 +354,15 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
       }
       if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
+      if (kRecord && lane == 0) {                 // (the slot's last reader has given back its unit)
+        const uint32_t bar = smem_u32(&scale_full[n % kScaleSlots]);
+        if (pg >= 0) {
+          mbar_arrive_expect_tx(bar, 1024);
+          bulk_load(smem_u32(scale_buf + (n % kScaleSlots) * 256), A.kv + (int64_t)pg * kRecPageBytes + kRecScalesAt, 1024, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         if (kRecord) {
@@ -327,10 +371,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           if (lane == 0) {
             const uint32_t bar = smem_u32(&code_full[code]);
             if (pg >= 0) {
-              mbar_arrive_expect_tx(bar, kCodeStage + (j == 0 ? 1024 : 0));
+              mbar_arrive_expect_tx(bar, kCodeStage);
               tma_load_3d(smem_u32(code_buf + code * kCodeStage), &map_pair, bar, 128 * j, 0, pg);
-              if (j == 0)
-                bulk_load(smem_u32(scale_buf + (n % kScaleSlots) * 256), A.kv + (int64_t)pg * kRecPageBytes + kRecScalesAt, 1024, bar);
             } else {
               mbar_arrive(bar);
             }
@@ -376,6 +418,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     }
     int sp = 0, vp = 0, rope = 0, edges = 0;      // pair slots of the scores and of the values
     uint32_t sp_ph = 0, rope_ph = 0, q_ph = 0;
+    int slot = 0, ps = 0;                         // records: places of scores and of P
+    uint32_t slot_ph = 0, ps_ph = 0;
     auto load_q = [&](int us) {
       if (issuer) {
         const uint32_t bar = smem_u32(&q_full);
@@ -386,8 +430,18 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     };
     // the scores of unit n against pairs j0 .. j1 - 1 (before the first also the rotated part)
     auto scores = [&](int n, int j0, int j1) {
-      const uint32_t d = kSCol + (n & 1) * kPage;
+      uint32_t d = S::kSCol + (n & 1) * kPage;
+      auto place = [&]() {                        // records: each part's scores go to a place of their own
+        if (!warp_wait(&s_empty[slot], slot_ph ^ 1, abort, A.err)) return false;
+        d = S::kSCol + slot * kPage;
+        return true;
+      };
+      auto placed = [&]() {
+        if (issuer) mma_commit(smem_u32(&s_full[slot]));
+        if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
+      };
       if (j0 == 0) {
+        if (kRecord && !place()) return false;
         if (!warp_wait(&rope_full[rope], rope_ph, abort, A.err)) return false;
         tc_fence_after();
         if (issuer) {
@@ -396,11 +450,13 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc_s, k != 0);
           mma_commit(smem_u32(&rope_empty[rope]));
         }
+        if (kRecord) placed();
         __syncwarp();
         if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
       }
 #pragma unroll 1
       for (int j = j0; j < j1; ++j) {
+        if (kRecord && !place()) return false;
         if (!warp_wait(&pair_full[sp], sp_ph, abort, A.err)) return false;
         if (!kRecord && j == 0 && (s_unit[n % kUnits].flags & kEdge)) {   // (records: the conversion has done it)
           if (!warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err)) return false;
@@ -412,9 +468,10 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_f16_ss(d, desc_add(qd, (k >> 2) * N * 128 + (k & 3) * 32), desc_add(kd, (k >> 2) * (kPage * 128) + (k & 3) * 32),
-                       idesc_s, 1);
-          if (j == 3) mma_commit(smem_u32(&s_full[n & 1]));
+                       idesc_s, !kRecord || k != 0);
+          if (!kRecord && j == 3) mma_commit(smem_u32(&s_full[n & 1]));
         }
+        if (kRecord) placed();
         __syncwarp();
         if (++sp == S::kPairs) sp = 0, sp_ph ^= 1u;
       }
@@ -434,25 +491,34 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
       }
       if (n >= 0) {
-        ok = warp_wait(&p_full, n & 1, abort, A.err);
+        ok = warp_wait(&p_full[ps], ps_ph, abort, A.err);
         if (!ok) break;
         tc_fence_after();
         // unit n's scores are done (their softmax is), so the queries may be replaced
         if (next) load_q((n + 1) % kUnits);
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
+          if (kRecord && j > 0) {
+            ok = warp_wait(&p_full[ps], ps_ph, abort, A.err);
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (issuer) {
-            const uint64_t vd = desc_add(dv, vp * kPairBytes);
+            const uint64_t vd = desc_add(dv, vp * kPairBytes), pd = desc_add(dp, ps * S::kPBytes);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(dp, k * 32), idesc_o, k != 0 ? 1u : fresh ^ 1u);
+              mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc_o, k != 0 ? 1u : fresh ^ 1u);
             mma_commit(smem_u32(&pair_empty[vp]));
+            if (j == 3) mma_commit(smem_u32(&o_done[n & 1]));
+            if (kRecord) mma_commit(smem_u32(&p_empty[ps]));
           }
           __syncwarp();
           if (++vp == S::kPairs) vp = 0;
+          if (kRecord || j == 3) {
+            if (++ps == S::kPs) ps = 0, ps_ph ^= 1u;
+          }
         }
-        if (issuer) mma_commit(smem_u32(&o_done));
-        __syncwarp();
+        if (!ok) break;
       } else if (next) {
         load_q(0);
       }
@@ -492,7 +558,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         if (!ok) break;
         const bool edge = (s_unit[us].flags & kEdge) != 0;
         const int last = s_unit[us].last;
-        const float* scales = scale_buf + (n % kScaleSlots) * 256;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
           ok = warp_wait(&code_full[code], code_ph, abort, A.err) && warp_wait(&pair_empty[pair], pair_ph ^ 1, abort, A.err);
@@ -504,26 +569,15 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
             const int piece = ct + i * 32 * S::kFixWarps, row = piece >> 4, ch = piece & 15;
-            const uint2 w = *reinterpret_cast<const uint2*>(src + row * 128 + ch * 8);
-            const float sc = scales[row * 4 + j];
+            uint2 w = *reinterpret_cast<const uint2*>(src + row * 128 + ch * 8);
+            if (KV == kKvE4m3 && edge) {
+              const uint32_t b0 = __vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), b1 = __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              if ((b0 | b1) && row <= last) atomicOr(&s_bad[us][row >> 5], 1u << (row & 31));
+              w.x &= ~b0, w.y &= ~b1;
+            }
             uint32_t o[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t a, b2;
-              codes_f16<KV == kKvInt8>(h ? w.y : w.x, a, b2);
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
-              const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b2));
-              const float2 s2 = make_float2(sc, sc);
-              const float2 x = __fmul2_rn(f, s2), y = __fmul2_rn(g, s2);
-              o[2 * h] = pack_bf16(x.x, x.y), o[2 * h + 1] = pack_bf16(y.x, y.y);
-            }
-            if (edge) {
-              bool bad = false;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) bad |= (o[e] & 0x7F80u) == 0x7F80u || (o[e] & 0x7F800000u) == 0x7F800000u;
-              if (bad && row <= last) atomicOr(&s_bad[us][row >> 5], 1u << (row & 31));
-              if (bad || row > last) o[0] = o[1] = o[2] = o[3] = 0;
-            }
+            codes_bf16<KV>(w.x, o[0], o[1]);
+            codes_bf16<KV>(w.y, o[2], o[3]);
             *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kPage * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
                 make_uint4(o[0], o[1], o[2], o[3]);
           }
@@ -589,34 +643,68 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     const int r0 = 16 * warp + (lane >> 2);       // this thread's rows: r0 and r0 + 8
     const float f = fmaxf(A.scale_log2, 1.17549435e-38f);   // (a scale of 0 would make masked scores NaN)
     float M[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
+    int slot = 0, ps = 0;                         // records: places of scores and of P
+    uint32_t slot_ph = 0, ps_ph = 0;
     bool ok = true;
     for (int n = 0; n < count; ++n) {
       const int us = n % kUnits;
+      const float* scales = scale_buf + (n % kScaleSlots) * 256 + 8 * (lane & 3);   // of this thread's keys
       ok = ok && warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
       LatentUnit x{};
       if (ok) x = s_unit[us];
       if (x.flags & kFirst) M[0] = M[1] = kNone, l[0] = l[1] = 0.f;
-      ok = ok && warp_wait(&s_full[n & 1], (n >> 1) & 1, abort, A.err);
       float s[32];
+      if constexpr (!kRecord) {
+        ok = ok && warp_wait(&s_full[n & 1], (n >> 1) & 1, abort, A.err);
+        if (active && ok) {
+          tc_fence_after();
+          tmem_ld_16x64(quarter + S::kSCol + (n & 1) * kPage, s);
+          tmem_ld_wait();
+        }
+      } else if (active) {
+        ok = ok && warp_wait(&scale_full[n % kScaleSlots], (n / kScaleSlots) & 1, abort, A.err);
+#pragma unroll 1
+        for (int g = -1; g < 4 && ok; ++g) {      // the rotated part, then each scale's
+          ok = warp_wait(&s_full[slot], slot_ph, abort, A.err);
+          if (!ok) break;
+          tc_fence_after();
+          float t[32];
+          tmem_ld_16x64(quarter + S::kSCol + slot * kPage, t);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_empty[slot]));
+          if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
+          if (g < 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = t[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float c0 = scales[32 * j + g], c1 = scales[32 * j + 4 + g];
+              s[4 * j] = fmaf(t[4 * j], c0, s[4 * j]), s[4 * j + 1] = fmaf(t[4 * j + 1], c1, s[4 * j + 1]);
+              s[4 * j + 2] = fmaf(t[4 * j + 2], c0, s[4 * j + 2]), s[4 * j + 3] = fmaf(t[4 * j + 3], c1, s[4 * j + 3]);
+            }
+          }
+        }
+      }
+      int lim[2] = {kPage, kPage};                // last key that the rows see
       bool need = false;
       float top[2] = {-INFINITY, -INFINITY};
       if (active && ok) {
-        tc_fence_after();
-        tmem_ld_16x64(quarter + kSCol + (n & 1) * kPage, s);
-        tmem_ld_wait();
         if (x.flags & kEdge) {
           const uint64_t bad = (uint64_t)s_bad[us][0] | (uint64_t)s_bad[us][1] << 32;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int row = r0 + 8 * i;
-            const int lim = row < x.rows && !(x.flags & kVoid) ? x.rel + (x.row0 + row) / A.H : -1;
+            lim[i] = row < x.rows && !(x.flags & kVoid) ? x.rel + (x.row0 + row) / A.H : -1;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int key = 8 * j + 2 * (lane & 3) + e;
                 float& v = s[4 * j + 2 * i + e];
-                if (key > lim) v = -INFINITY;
+                if (key > lim[i]) v = -INFINITY;
                 else if (bad >> key & 1) v = NAN;
               }
             }
@@ -646,7 +734,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
         if (!bar_all(1, 128, ok)) break;
         if (!(x.flags & kFirst)) {                // O so far, once its last product is done
-          ok = warp_wait(&o_done, (n - 1) & 1, abort, A.err);
+          ok = warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
           if (ok) {
             tc_fence_after();
 #pragma unroll 1
@@ -662,35 +750,61 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           }
         }
       }
-      uint32_t p[16];
       if (active && ok) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float a = 0.f, c = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float u = ex2(fmaf(s[4 * j + 2 * i], f, -M[i])), w = ex2(fmaf(s[4 * j + 2 * i + 1], f, -M[i]));
+            float &u = s[4 * j + 2 * i], &w = s[4 * j + 2 * i + 1];
+            u = ex2(fmaf(u, f, -M[i])), w = ex2(fmaf(w, f, -M[i]));
             a += u, c += w;
-            p[2 * j + i] = pack_bf16(u, w);
           }
           l[i] += a + c;
         }
       }
-      // the last page's values have left P's place
-      if (n > 0) ok = ok && warp_wait(&o_done, (n - 1) & 1, abort, A.err);
-      if (active && ok) {
+      uint8_t* p_row = p_buf + r0 * 128 + 4 * (lane & 3);   // (r0 + 8 has the same swizzle)
+      if constexpr (!kRecord) {
+        // the last page's values have left P's place
+        if (n > 0) ok = ok && warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
+        if (active && ok) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = r0 + 8 * i;
-          uint8_t* dst = p_buf + row * 128 + 4 * (lane & 3);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) *reinterpret_cast<uint32_t*>(dst + ((j ^ (row & 7)) << 4)) = p[2 * j + i];
+          for (int j = 0; j < 8; ++j) {
+            uint8_t* dst = p_row + ((j ^ (r0 & 7)) << 4);
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(s[4 * j], s[4 * j + 1]);
+            *reinterpret_cast<uint32_t*>(dst + 8 * 128) = pack_bf16(s[4 * j + 2], s[4 * j + 3]);
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full[0]));
+      } else if (active) {
+#pragma unroll 1
+        for (int g = 0; g < 4 && ok; ++g) {       // each scale's codes get its weights
+          ok = warp_wait(&p_empty[ps], ps_ph ^ 1, abort, A.err);
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float c0 = scales[32 * j + g], c1 = scales[32 * j + 4 + g];
+            float v[4] = {s[4 * j] * c0, s[4 * j + 1] * c1, s[4 * j + 2] * c0, s[4 * j + 3] * c1};
+            if (x.flags & kEdge) {                // (an unseen key's scale may be anything)
+              const int key = 8 * j + 2 * (lane & 3);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key + (e & 1) > lim[e >> 1]) v[e] = 0.f;
+            }
+            uint8_t* dst = p_row + ps * S::kPBytes + ((j ^ (r0 & 7)) << 4);
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v[0], v[1]);
+            *reinterpret_cast<uint32_t*>(dst + 8 * 128) = pack_bf16(v[2], v[3]);
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&p_full[ps]));
+          if (++ps == S::kPs) ps = 0, ps_ph ^= 1u;
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full));
       if (x.flags & kLast) {
         // ---- the segment's outputs, or its part
         if (active && ok) {
@@ -702,7 +816,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           }
         }
         if (!bar_all(1, 128, ok)) break;
-        ok = warp_wait(&o_done, n & 1, abort, A.err);
+        // (two barriers, for a warp may come here before unit n - 1's values are done or after unit n's)
+        ok = warp_wait(&o_done[n & 1], (n >> 1) & 1, abort, A.err);
         if (ok) {
           tc_fence_after();
           const int t = warp * 32 + lane;
