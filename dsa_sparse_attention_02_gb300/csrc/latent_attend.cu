@@ -16,8 +16,9 @@
 //              them with 16 keys each. P^T goes to shared memory as bf16. The reference
 //              maximum moves only when a score passes it by more than 2^8; then, and at an
 //              item's end, all four warps read their quarter of O^T's lanes (latent columns).
-//   warp 4     issues the products: the next page's scores before this page's values
-//   warp 5     finds the units of this block's run, loads pages by TMA in pairs of 64-column atoms
+//   warps 4, 5 issue the products, one the scores', one the values': an MMA costs its issuer some
+//              50 clocks, more than it costs the tensor cores at these shapes (32 and 40 to 48)
+//   warp 6     finds the units of this block's run, loads pages by TMA in pairs of 64-column atoms
 //   the rest   records: convert codes * scale to bf16 (as every reader of them does). Both:
 //              in a page that some row of the item does not see whole, zero the keys that no row
 //              sees and those with a NaN or infinity, which rows that do see them get as
@@ -34,7 +35,7 @@ constexpr int kPairBytes = 2 * kPage * 128;  // two atoms of 64 rows x 64 bf16
 constexpr int kRopeBytes = kPage * 128;
 constexpr int kCodeStage = kPage * 128;      // a pair's codes
 constexpr int kScaleSlots = 4;
-constexpr int kMmaWarp = 4, kLoadWarp = 5, kFixWarp0 = 6;
+constexpr int kMmaWarp = 4, kValueWarp = 5, kLoadWarp = 6, kFixWarp0 = 7;
 constexpr uint32_t kTmem = 512;
 constexpr float kMove = 8.f;                 // log2 of what a weight may pass the reference by
 enum : int { kEdge = 8 };                    // some row of the item does not see the whole page
@@ -49,12 +50,10 @@ struct __align__(16) LatentUnit {
 template <int N, int KV>
 struct LatentShape {
   static constexpr bool kRecord = KV != kKvBf16;
-  // Rings as deep as shared memory allows. Below eight pairs the next page's scores begin with the
-  // pairs that fit beside this page's (kEarly); the others follow its values.
+  // Rings as deep as shared memory allows.
   static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 64 ? 6 : 8);
   static constexpr int kRopes = !kRecord && N == 16 ? 3 : 2;
   static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 2 : N == 32 ? 4 : 6;
-  static constexpr int kEarly = kPairs >= 8 ? 4 : kPairs - 4;
   // Scores: a page's of bf16 rows in one place, two pages at a time; of records in one place for
   // each scale (and the rotated part), in a ring. P: one of a page, or a ring of one for each scale.
   static constexpr int kSlots = !kRecord ? 2 : N == 64 ? 4 : 6;
@@ -143,7 +142,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ uint64_t pair_full[S::kPairs], pair_empty[S::kPairs], rope_full[S::kRopes], rope_empty[S::kRopes];
   __shared__ uint64_t code_full[kRecord ? S::kCodes : 1], code_empty[kRecord ? S::kCodes : 1];
   __shared__ uint64_t scale_full[kRecord ? kScaleSlots : 1];
-  __shared__ uint64_t q_full, s_full[S::kSlots], s_empty[S::kSlots], p_full[S::kPs], p_empty[S::kPs], o_done[2], drain;   // o_done: of even and odd units
+  __shared__ uint64_t q_full, s_full[S::kSlots], s_empty[S::kSlots], p_full[S::kPs], p_empty[S::kPs], o_done[2], drain[2];   // o_done: of even and odd units
   __shared__ LatentUnit s_unit[kUnits];
   __shared__ uint32_t s_bad[kUnits][2];                   // keys with a value that is not finite
   __shared__ float s_keep[N], s_max[N], s_sum[N];
@@ -185,7 +184,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     }
     mbar_init(smem_u32(&o_done[0]), 1);
     mbar_init(smem_u32(&o_done[1]), 1);
-    mbar_init(smem_u32(&drain), 1);
+    mbar_init(smem_u32(&drain[0]), 1);
+    mbar_init(smem_u32(&drain[1]), 1);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -401,142 +401,124 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 1000000ull) {}
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issue
-    constexpr uint32_t idesc_s = make_idesc(64, kPage, kFmtBF16, kFmtBF16, 0, 0);
-    constexpr uint32_t idesc_o = make_idesc(128, N, kFmtBF16, kFmtBF16, 1, 0);
-    const uint64_t dq = smem_desc(smem_u32(q_buf), 0, 1024, kSwizzle128B);
-    const uint64_t dk = smem_desc(smem_u32(pair_buf), 0, 1024, kSwizzle128B);
-    const uint64_t dv = smem_desc(smem_u32(pair_buf), kPage * 128, 1024, kSwizzle128B);
-    const uint64_t dr = smem_desc(smem_u32(rope_buf), 0, 1024, kSwizzle128B);
-    const uint64_t dp = smem_desc(smem_u32(p_buf), 0, 1024, kSwizzle128B);
+  } else if (warp == kMmaWarp || warp == kValueWarp) {
+    // ------------------------------------------------------------ MMA issue: scores, values
     const bool issuer = elect_one();
     bool ok = tmem == 0;                          // all 512 columns are this block's
     if (!ok) {
       *abort = 1;
       record_error(A.err, kDevTimeout);
     }
-    int sp = 0, vp = 0, rope = 0, edges = 0;      // pair slots of the scores and of the values
-    uint32_t sp_ph = 0, rope_ph = 0, q_ph = 0;
-    int slot = 0, ps = 0;                         // records: places of scores and of P
-    uint32_t slot_ph = 0, ps_ph = 0;
-    auto load_q = [&](int us) {
-      if (issuer) {
-        const uint32_t bar = smem_u32(&q_full);
-        mbar_arrive_expect_tx(bar, S::kQBytes);
-        tma_load_3d(smem_u32(q_buf), &map_q, bar, 0, (int)s_unit[us].out, 0);
-      }
-      __syncwarp();
-    };
-    // the scores of unit n against pairs j0 .. j1 - 1 (before the first also the rotated part)
-    auto scores = [&](int n, int j0, int j1) {
-      uint32_t d = S::kSCol + (n & 1) * kPage;
-      auto place = [&]() {                        // records: each part's scores go to a place of their own
-        if (!warp_wait(&s_empty[slot], slot_ph ^ 1, abort, A.err)) return false;
-        d = S::kSCol + slot * kPage;
-        return true;
-      };
+    if (warp == kMmaWarp) {
+      constexpr uint32_t idesc = make_idesc(64, kPage, kFmtBF16, kFmtBF16, 0, 0);
+      const uint64_t dq = smem_desc(smem_u32(q_buf), 0, 1024, kSwizzle128B);
+      const uint64_t dk = smem_desc(smem_u32(pair_buf), 0, 1024, kSwizzle128B);
+      const uint64_t dr = smem_desc(smem_u32(rope_buf), 0, 1024, kSwizzle128B);
+      int pair = 0, rope = 0, slot = 0, edges = 0;
+      uint32_t pair_ph = 0, rope_ph = 0, slot_ph = 0, q_ph = 0;
+      // the next place of scores is free / is done
+      auto place = [&]() { return warp_wait(&s_empty[slot], slot_ph ^ 1, abort, A.err); };
       auto placed = [&]() {
         if (issuer) mma_commit(smem_u32(&s_full[slot]));
         if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
       };
-      if (j0 == 0) {
-        if (kRecord && !place()) return false;
-        if (!warp_wait(&rope_full[rope], rope_ph, abort, A.err)) return false;
+      for (int n = 0; n < count && ok; ++n) {
+        const int us = n % kUnits;
+        ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
+        if (!ok) break;
+        const int flags = s_unit[us].flags;
+        if (flags & kFirst) {
+          // the last segment's scores have left the queries' place
+          if (n > 0) ok = slot > 0 ? warp_wait(&s_full[slot - 1], slot_ph, abort, A.err)
+                                   : warp_wait(&s_full[S::kSlots - 1], slot_ph ^ 1, abort, A.err);
+          if (ok && issuer) {
+            const uint32_t bar = smem_u32(&q_full);
+            mbar_arrive_expect_tx(bar, S::kQBytes);
+            tma_load_3d(smem_u32(q_buf), &map_q, bar, 0, (int)s_unit[us].out, 0);
+          }
+          __syncwarp();
+          ok = ok && warp_wait(&q_full, q_ph, abort, A.err);
+          q_ph ^= 1u;
+        }
+        ok = ok && place() && warp_wait(&rope_full[rope], rope_ph, abort, A.err);
+        if (!ok) break;
+        uint32_t d = S::kSCol + slot * kPage;
         tc_fence_after();
         if (issuer) {
           const uint64_t kd = desc_add(dr, rope * kRopeBytes), qd = desc_add(dq, 8 * N * 128);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc_s, k != 0);
+          for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc, k != 0);
           mma_commit(smem_u32(&rope_empty[rope]));
         }
-        if (kRecord) placed();
+        if (kRecord) placed();                    // records: each scale's scores go to a place of their own
         __syncwarp();
         if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
-      }
-#pragma unroll 1
-      for (int j = j0; j < j1; ++j) {
-        if (kRecord && !place()) return false;
-        if (!warp_wait(&pair_full[sp], sp_ph, abort, A.err)) return false;
-        if (!kRecord && j == 0 && (s_unit[n % kUnits].flags & kEdge)) {   // (records: the conversion has done it)
-          if (!warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err)) return false;
-          ++edges;
-        }
-        tc_fence_after();
-        if (issuer) {
-          const uint64_t kd = desc_add(dk, sp * kPairBytes), qd = desc_add(dq, 2 * j * N * 128);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_f16_ss(d, desc_add(qd, (k >> 2) * N * 128 + (k & 3) * 32), desc_add(kd, (k >> 2) * (kPage * 128) + (k & 3) * 32),
-                       idesc_s, !kRecord || k != 0);
-          if (!kRecord && j == 3) mma_commit(smem_u32(&s_full[n & 1]));
-        }
-        if (kRecord) placed();
-        __syncwarp();
-        if (++sp == S::kPairs) sp = 0, sp_ph ^= 1u;
-      }
-      return true;
-    };
-    uint32_t fresh = 0;                           // unit n begins a segment
-    for (int n = -1; n < count && ok; ++n) {
-      bool next = false, later = false;           // unit n + 1 begins a segment; its scores wait for n's values
-      if (n + 1 < count) {
-        ok = warp_wait(&u_full[(n + 1) % kUnits], ((n + 1) / kUnits) & 1, abort, A.err);
-        if (!ok) break;
-        next = (s_unit[(n + 1) % kUnits].flags & kFirst) != 0;
-        if (!next) {
-          ok = scores(n + 1, 0, S::kEarly);
-          later = S::kEarly < 4;
-          if (!ok) break;
-        }
-      }
-      if (n >= 0) {
-        ok = warp_wait(&p_full[ps], ps_ph, abort, A.err);
-        if (!ok) break;
-        tc_fence_after();
-        // unit n's scores are done (their softmax is), so the queries may be replaced
-        if (next) load_q((n + 1) % kUnits);
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
-          if (kRecord && j > 0) {
-            ok = warp_wait(&p_full[ps], ps_ph, abort, A.err);
-            if (!ok) break;
-            tc_fence_after();
+          if (kRecord) {
+            ok = place();
+            d = S::kSCol + slot * kPage;
           }
+          ok = ok && warp_wait(&pair_full[pair], pair_ph, abort, A.err);
+          if (!kRecord && j == 0 && (flags & kEdge) && ok) {   // (records: the conversion has done it)
+            ok = warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err);
+            ++edges;
+          }
+          if (!ok) break;
+          tc_fence_after();
           if (issuer) {
-            const uint64_t vd = desc_add(dv, vp * kPairBytes), pd = desc_add(dp, ps * S::kPBytes);
+            const uint64_t kd = desc_add(dk, pair * kPairBytes), qd = desc_add(dq, 2 * j * N * 128);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ss(d, desc_add(qd, (k >> 2) * N * 128 + (k & 3) * 32),
+                         desc_add(kd, (k >> 2) * (kPage * 128) + (k & 3) * 32), idesc, !kRecord || k != 0);
+          }
+          if (kRecord || j == 3) placed();
+          __syncwarp();
+          if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
+        }
+      }
+    } else {
+      constexpr uint32_t idesc = make_idesc(128, N, kFmtBF16, kFmtBF16, 1, 0);
+      const uint64_t dv = smem_desc(smem_u32(pair_buf), kPage * 128, 1024, kSwizzle128B);
+      const uint64_t dp = smem_desc(smem_u32(p_buf), 0, 1024, kSwizzle128B);
+      int pair = 0, ps = 0;
+      uint32_t ps_ph = 0;
+      for (int n = 0; n < count && ok; ++n) {
+        const int us = n % kUnits;
+        ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
+        if (!ok) break;
+        const uint32_t kept = s_unit[us].flags & kFirst ? 0u : 1u;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          // (P is behind the scores, and so behind the pairs' arrival)
+          if (kRecord || j == 0) ok = warp_wait(&p_full[ps], ps_ph, abort, A.err);
+          if (!ok) break;
+          tc_fence_after();
+          if (issuer) {
+            const uint64_t vd = desc_add(dv, pair * kPairBytes), pd = desc_add(dp, ps * S::kPBytes);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc_o, k != 0 ? 1u : fresh ^ 1u);
-            mma_commit(smem_u32(&pair_empty[vp]));
+              mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
+            mma_commit(smem_u32(&pair_empty[pair]));
             if (j == 3) mma_commit(smem_u32(&o_done[n & 1]));
             if (kRecord) mma_commit(smem_u32(&p_empty[ps]));
           }
           __syncwarp();
-          if (++vp == S::kPairs) vp = 0;
+          if (++pair == S::kPairs) pair = 0;
           if (kRecord || j == 3) {
             if (++ps == S::kPs) ps = 0, ps_ph ^= 1u;
           }
         }
-        if (!ok) break;
-      } else if (next) {
-        load_q(0);
       }
-      if (next) {
-        ok = warp_wait(&q_full, q_ph, abort, A.err);
-        q_ph ^= 1u;
-        if (ok) ok = scores(n + 1, 0, 4);
-      } else if (later) {
-        ok = scores(n + 1, S::kEarly, 4);
-      }
-      fresh = next ? 1u : 0u;
     }
     // Everything issued has finished before tensor and shared memory are given back.
     __syncwarp();
     if (issuer) {
-      mma_commit(smem_u32(&drain));
+      const uint32_t bar = smem_u32(&drain[warp - kMmaWarp]);
+      mma_commit(bar);
       const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&drain), 0)) {
+      while (!mbar_try_wait(bar, 0)) {
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
           *abort = 1;
           record_error(A.err, kDevTimeout);
@@ -654,14 +636,19 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       if (ok) x = s_unit[us];
       if (x.flags & kFirst) M[0] = M[1] = kNone, l[0] = l[1] = 0.f;
       float s[32];
-      if constexpr (!kRecord) {
+      // (warps without rows do not look at the scores' barriers, which may be two pages ahead of them)
+      if (!active) {
+      } else if constexpr (!kRecord) {
         ok = ok && warp_wait(&s_full[n & 1], (n >> 1) & 1, abort, A.err);
-        if (active && ok) {
+        if (ok) {
           tc_fence_after();
           tmem_ld_16x64(quarter + S::kSCol + (n & 1) * kPage, s);
           tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_empty[n & 1]));
         }
-      } else if (active) {
+      } else {
         ok = ok && warp_wait(&scale_full[n % kScaleSlots], (n / kScaleSlots) & 1, abort, A.err);
 #pragma unroll 1
         for (int g = -1; g < 4 && ok; ++g) {      // the rotated part, then each scale's
