@@ -24,28 +24,14 @@
 //              sees and those with a NaN or infinity, which rows that do see them get as
 //              a NaN score (a weight of zero would not keep them out of the sum).
 // All units are laid end to end and cut into equal runs, one per SM; cut items are merged.
-#include "latent_common.cuh"
+#include "latent_units.cuh"
 
 namespace dsa {
 
 namespace {
 
-constexpr int kUnits = 4;                    // units described ahead
-constexpr int kPairBytes = 2 * kPage * 128;  // two atoms of 64 rows x 64 bf16
-constexpr int kRopeBytes = kPage * 128;
-constexpr int kCodeStage = kPage * 128;      // a pair's codes
-constexpr int kScaleSlots = 4;
 constexpr int kMmaWarp = 4, kValueWarp = 5, kLoadWarp = 6, kFixWarp0 = 7;
-constexpr uint32_t kTmem = 512;
 constexpr float kMove = 8.f;                 // log2 of what a weight may pass the reference by
-enum : int { kEdge = 8 };                    // some row of the item does not see the whole page
-
-struct __align__(16) LatentUnit {
-  int flags, rel;       // position of token 0 less the page's first position
-  int row0, rows;       // first row of the item in its request (token row / H, head row % H); rows in use
-  int slot, last;       // partial slot or -1; last key of the page that some row sees, or -1
-  int64_t out;          // global number of the item's first row
-};
 
 template <int N, int KV>
 struct LatentShape {
@@ -66,63 +52,6 @@ struct LatentShape {
                                (kRecord ? kScaleSlots * 1024 : 0);
   static_assert(kSmem <= 227 * 1024 - 1536, "and barriers, units and row statistics beside it");
 };
-
-// bf16 pairs of a word's four codes, exact: (byte 0, byte 1) and (byte 2, byte 3).
-template <int KV>
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (KV == kKvInt8) {
-    // 0x43vv is 128 + vv of the low seven bits, 0x4300 or 0x4380 (by the sign bit) 128 or 256
-    auto two = [](uint32_t x) {
-      const uint32_t v = (x & 0x007F007Fu) | 0x43004300u, s = (x & 0x00800080u) | 0x43004300u;
-      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&s));
-      return *reinterpret_cast<const uint32_t*>(&d);
-    };
-    lo = two(__byte_perm(w, 0, 0x4140));
-    hi = two(__byte_perm(w, 0, 0x4342));
-  } else {
-    uint32_t a, b;
-    codes_f16<false>(w, a, b);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    lo = pack_bf16(f.x, f.y), hi = pack_bf16(g.x, g.y);
-  }
-}
-
-// Requests as the items see them.
-struct LatentReq {
-  int q0, n, start;      // first token, tokens, position of the first (may be negative)
-  int tiles;
-  bool bad, none;        // none: nothing visible (inconsistent geometry)
-};
-template <int N>
-__device__ __forceinline__ LatentReq latent_req(const LatentAttendArgs& A, int b) {
-  LatentReq r;
-  const int c0 = __ldg(A.g.cu_q + b), c1 = __ldg(A.g.cu_q + b + 1), len = __ldg(A.g.seq_lens + b);
-  r.bad = c0 < 0 || c1 < c0 || c1 > A.g.T || len > A.g.max_seq_len;
-  r.q0 = min(max(c0, 0), A.g.T);
-  r.n = max(min(c1, A.g.T) - r.q0, 0);
-  r.none = r.bad || len <= 0;
-  r.start = len - r.n;
-  r.tiles = (r.n * A.H + N - 1) / N;      // (T * H stays below 2^31)
-  return r;
-}
-// Pages that tile i's last token sees; at least one unit, so that empty rows are written too.
-template <int N>
-__device__ __forceinline__ int latent_units(const LatentAttendArgs& A, const LatentReq& r, int i) {
-  if (r.none) return 1;
-  const int last = min(r.n - 1, (int)(((int64_t)i * N + N - 1) / A.H));
-  return max(r.start + last, 0) / kPage + 1;
-}
-// Units of tiles 0 .. i - 1: tile j sees page k if its last token reaches position 64 k, which
-// tiles from (64 k - start) H / N on do.
-template <int N>
-__device__ __forceinline__ int64_t latent_before(const LatentAttendArgs& A, const LatentReq& r, int i) {
-  if (r.none || i <= 0) return i;
-  const int k0 = max(r.start, 0) / kPage, k1 = max(r.start + r.n - 1, 0) / kPage;
-  int64_t s = (int64_t)i * (k0 + 1);
-  for (int k = k0 + 1; k <= k1; ++k) s += max((int64_t)i - (int64_t)(k * kPage - r.start) * A.H / N, (int64_t)0);
-  return s;
-}
 
 template <int N, int KV>
 __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
@@ -146,7 +75,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ LatentUnit s_unit[kUnits];
   __shared__ uint32_t s_bad[kUnits][2];                   // keys with a value that is not finite
   __shared__ float s_keep[N], s_max[N], s_sum[N];
-  __shared__ int s_count, s_abort;
+  __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
@@ -193,154 +122,40 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     tmem_alloc(smem_u32(&s_tmem), kTmem);
     tmem_relinquish();
   }
-  // The run [begin, end) of all units, the request it starts in and where that begins.
-  int64_t begin = 0, end = 0, base = 0, total = 0;
-  int req = 0, runs = 1;
-  if (warp == kLoadWarp) {
-    if (lane == 0) {
-      tma_prefetch_desc(&map_pair);
-      tma_prefetch_desc(&map_rope);
-      parts.cuts[blockIdx.x].follow = 0;
-    }
-    for (int b0 = 0; b0 < A.g.B; b0 += 32) {
-      if (b0 + lane < A.g.B) {
-        const LatentReq r = latent_req<N>(A, b0 + lane);
-        total += latent_before<N>(A, r, r.tiles);
-        if (r.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    runs = (int)min((int64_t)gridDim.x, max((total + A.min_run - 1) / A.min_run, (int64_t)1));
-    if ((int)blockIdx.x < runs) {
-      begin = split_begin(blockIdx.x, total, runs);
-      end = split_begin(blockIdx.x + 1, total, runs);
-      for (int b0 = 0; b0 < A.g.B; b0 += 32) {
-        int64_t w = 0;
-        if (b0 + lane < A.g.B) {
-          const LatentReq r = latent_req<N>(A, b0 + lane);
-          w = latent_before<N>(A, r, r.tiles);
-        }
-        int64_t upto = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += v;
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, base + upto > begin);
-        if (m) {
-          const int l = __ffs(m) - 1;
-          req = b0 + l;
-          base += __shfl_sync(0xffffffffu, upto - w, l);
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
-    if (lane == 0) s_count = (int)(end - begin);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const int count = s_count;
   const uint32_t tmem = s_tmem;
   volatile int* abort = &s_abort;
 
-  if (count == 0) {
-    // nothing of this batch for this block
-  } else if (warp == kLoadWarp) {
+  if (warp == kLoadWarp) {
     // ------------------------------------------------------------ units and loads
-    int b = req, ti = 0, c = 0;
-    LatentReq r = latent_req<N>(A, b);
-    {
-      // the last tile that begins at or before unit `begin`
-      const int64_t o = begin - base;
-      int lo = 0, hi = r.tiles - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (latent_before<N>(A, r, mid) <= o) lo = mid; else hi = mid - 1;
-      }
-      ti = lo;
-      c = (int)(o - latent_before<N>(A, r, lo));
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_pair);
+      tma_prefetch_desc(&map_rope);
     }
-    LatentUnit x{};
-    int page = -1, cnt = 0, at = 0;
-    // up to 32 units at a time, one per lane
-    auto batch = [&](int64_t u) {
-      cnt = (int)min((int64_t)32, end - u);
-      int bb = b, tt = ti, cc = c;
-      LatentReq rr = r;
-      int units = latent_units<N>(A, rr, tt);
-      for (int step = lane; step > 0 && lane < cnt;) {          // forward by `lane` units
-        const int left = units - cc;
-        if (step < left) {
-          cc += step;
-          break;
-        }
-        step -= left;
-        cc = 0;
-        if (++tt == rr.tiles) {
-          tt = 0;
-          do rr = latent_req<N>(A, ++bb);
-          while (rr.tiles == 0 && bb + 1 < A.g.B);
-        }
-        units = latent_units<N>(A, rr, tt);
-      }
-      __syncwarp();
-      if (lane < cnt) {
-        const int64_t me = u + lane, ib = me - cc, ie = ib + units;
-        x.row0 = tt * N;
-        x.rows = min(N, rr.n * A.H - x.row0);
-        x.out = (int64_t)rr.q0 * A.H + x.row0;
-        x.rel = rr.start - cc * kPage;
-        const int lo = x.row0 / A.H, hi = (x.row0 + x.rows - 1) / A.H;
-        page = -1;
-        if (!rr.none && x.rel + hi >= 0) {
-          page = gqa_page(A.g, bb, cc);
-          if (page < 0) record_error(A.err, kDevBadIndex);
-        }
-        x.last = page >= 0 ? min(x.rel + hi, kPage - 1) : -1;
-        const bool first = me == ib || me == begin, last = me + 1 == ie || me + 1 == end;
-        x.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (page >= 0 ? 0 : kVoid) |
-                  (page < 0 || x.rel + lo < kPage - 1 ? kEdge : 0);
-        const bool cut = ib < begin || ie > end;
-        x.slot = !cut ? -1 : 2 * (int)blockIdx.x + (max(ib, begin) == begin ? 0 : 1);
-        if (last && cut && ib >= begin) {
-          LatentCut k{};
-          k.follow = (int)split_owner(ie - 1, total, runs) - (int)blockIdx.x;
-          k.slot = x.slot, k.rows = x.rows, k.step = 1, k.out = x.out;
-          parts.cuts[blockIdx.x] = k;
-        }
-      }
-      // the cursor behind the batch: its last lane's unit, one further
-      const int l = cnt - 1;
-      b = __shfl_sync(0xffffffffu, bb, l), ti = __shfl_sync(0xffffffffu, tt, l), c = __shfl_sync(0xffffffffu, cc, l) + 1;
-      r = latent_req<N>(A, b);
-      if (u + cnt < end && c == latent_units<N>(A, r, ti)) {
-        c = 0;
-        if (++ti == r.tiles) {
-          ti = 0;
-          do r = latent_req<N>(A, ++b);
-          while (r.tiles == 0 && b + 1 < A.g.B);
-        }
-      }
-      at = 0;
-    };
+    LatentCursor<N> at(A, parts, blockIdx.x, gridDim.x, true);
+    const int count = (int)(at.end - at.begin);
+    if (count == 0 && lane == 0) {
+      s_unit[0].flags = kStop;
+      mbar_arrive(smem_u32(&u_full[0]));
+    }
     int pair = 0, rope = 0, code = 0;
     uint32_t pair_ph = 0, rope_ph = 0, code_ph = 0;
     bool ok = true;
     for (int n = 0; n < count && ok; ++n) {
-      if (at == cnt) batch(begin + n);
+      if (at.at == at.cnt) at.batch(at.begin + n);
       const int us = n % kUnits;
       ok = warp_wait(&u_empty[us], ((n / kUnits) & 1) ^ 1, abort, A.err);
       if (!ok) break;
-      if (lane == at) {
-        s_unit[us] = x;
+      if (lane == at.at) {
+        s_unit[us] = at.x;
         s_bad[us][0] = s_bad[us][1] = 0;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&u_full[us]));
-      const int pg = __shfl_sync(0xffffffffu, page, at++);
+      const int pg = __shfl_sync(0xffffffffu, at.page, at.at++);
       ok = warp_wait(&rope_empty[rope], rope_ph ^ 1, abort, A.err);
       if (!ok) break;
       if (lane == 0) {
@@ -422,11 +237,12 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         if (issuer) mma_commit(smem_u32(&s_full[slot]));
         if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
       };
-      for (int n = 0; n < count && ok; ++n) {
+      for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
         ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
         if (!ok) break;
-        const int flags = s_unit[us].flags;
+        flags = s_unit[us].flags;
+        if (flags & kStop) break;
         if (flags & kFirst) {
           // the last segment's scores have left the queries' place
           if (n > 0) ok = slot > 0 ? warp_wait(&s_full[slot - 1], slot_ph, abort, A.err)
@@ -484,11 +300,13 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       const uint64_t dp = smem_desc(smem_u32(p_buf), 0, 1024, kSwizzle128B);
       int pair = 0, ps = 0;
       uint32_t ps_ph = 0;
-      for (int n = 0; n < count && ok; ++n) {
+      for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
         ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
         if (!ok) break;
-        const uint32_t kept = s_unit[us].flags & kFirst ? 0u : 1u;
+        flags = s_unit[us].flags;
+        if (flags & kStop) break;
+        const uint32_t kept = flags & kFirst ? 0u : 1u;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
           // (P is behind the scores, and so behind the pairs' arrival)
@@ -534,11 +352,13 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       int pair = 0, code = 0;
       uint32_t pair_ph = 0, code_ph = 0;
       bool ok = true;
-      for (int n = 0; n < count && ok; ++n) {
+      for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
         ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
         if (!ok) break;
-        const bool edge = (s_unit[us].flags & kEdge) != 0;
+        flags = s_unit[us].flags;
+        if (flags & kStop) break;
+        const bool edge = (flags & kEdge) != 0;
         const int last = s_unit[us].last;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
@@ -579,12 +399,16 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       int pair = 0, edges = 0;
       uint32_t pair_ph = 0;
       bool ok = true;
-      for (int n = 0; n < count && ok; ++n) {
+      for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
-        // (the unit's loads have been issued, so its slots' barriers are in this unit's phase)
+        ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
+        if (!ok) break;
+        flags = s_unit[us].flags;
+        if (flags & kStop) break;
+        const bool edge = (flags & kEdge) != 0;
+        // (once the unit's loads have been issued, its slots' barriers are in its phase)
         ok = warp_wait(&u_loaded[us], (n / kUnits) & 1, abort, A.err);
         if (!ok) break;
-        const bool edge = (s_unit[us].flags & kEdge) != 0;
         const int last = s_unit[us].last;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
@@ -628,7 +452,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     int slot = 0, ps = 0;                         // records: places of scores and of P
     uint32_t slot_ph = 0, ps_ph = 0;
     bool ok = true;
-    for (int n = 0; n < count; ++n) {
+    for (int n = 0;; ++n) {
       const int us = n % kUnits;
       const float* scales = scale_buf + (n % kScaleSlots) * 256 + 8 * (lane & 3);   // of this thread's keys
       ok = ok && warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
@@ -637,7 +461,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       if (x.flags & kFirst) M[0] = M[1] = kNone, l[0] = l[1] = 0.f;
       float s[32];
       // (warps without rows do not look at the scores' barriers, which may be two pages ahead of them)
-      if (!active) {
+      if (!active || (x.flags & kStop)) {
       } else if constexpr (!kRecord) {
         ok = ok && warp_wait(&s_full[n & 1], (n >> 1) & 1, abort, A.err);
         if (ok) {
@@ -678,7 +502,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       int lim[2] = {kPage, kPage};                // last key that the rows see
       bool need = false;
       float top[2] = {-INFINITY, -INFINITY};
-      if (active && ok) {
+      if (active && ok && !(x.flags & kStop)) {
         if (x.flags & kEdge) {
           const uint64_t bad = (uint64_t)s_bad[us][0] | (uint64_t)s_bad[us][1] << 32;
 #pragma unroll
@@ -720,7 +544,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           }
         }
         if (!bar_all(1, 128, ok)) break;
-        if (!(x.flags & kFirst)) {                // O so far, once its last product is done
+        if (!(x.flags & (kFirst | kStop))) {      // O so far, once its last product is done
           ok = warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
           if (ok) {
             tc_fence_after();
@@ -737,6 +561,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           }
         }
       }
+      if (x.flags & kStop) break;
       if (active && ok) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -842,6 +667,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(smem_u32(&u_empty[us]));
+      // (past the round's vote all four warps know the unit, and so leave together)
+      if (x.flags & kEnd) break;
     }
   }
   tc_fence_before();
