@@ -30,7 +30,7 @@ namespace dsa {
 
 namespace {
 
-constexpr int kMmaWarp = 4, kValueWarp = 5, kLoadWarp = 6, kFixWarp0 = 7;
+constexpr int kSoftWarps = 8, kScoreWarp0 = 8, kValueWarp0 = 10;
 constexpr float kMove = 8.f;                 // log2 of what a weight may pass the reference by
 
 template <int N, int KV>
@@ -43,14 +43,30 @@ struct LatentShape {
   // Scores: a page's of bf16 rows in one place, two pages at a time; of records in one place for
   // each scale (and the rotated part), in a ring. P: one of a page, or a ring of one for each scale.
   static constexpr int kSlots = !kRecord ? 2 : N == 64 ? 4 : 6;
-  static constexpr uint32_t kSCol = !kRecord || N == 64 ? 256 : 128;
+  static constexpr uint32_t kSCol = !kRecord || N == 64 ? 256 : 128, kSlotCols = kRecord ? kPage : 2 * kPage;
   static constexpr int kPs = !kRecord ? 1 : N == 16 ? 4 : 2;
-  static constexpr int kFixWarps = kRecord ? 8 : 4;
+  // (20 and 16 warps: a whole number for each quarter of the SM, whose registers they share)
+  static constexpr int kValueWarps = kRecord ? 1 : 2, kFixWarps = kRecord ? 8 : 3;
+  static constexpr int kLoadWarp = kValueWarp0 + kValueWarps, kFixWarp0 = kLoadWarp + 1;
   static constexpr int kThreads = 32 * (kFixWarp0 + kFixWarps);
   static constexpr int kQBytes = 9 * N * 128, kPBytes = N * 128;   // of one P
   static constexpr int kSmem = 1024 + kQBytes + kPs * kPBytes + kRopes * kRopeBytes + kPairs * kPairBytes + kCodes * kCodeStage +
                                (kRecord ? kScaleSlots * 1024 : 0);
-  static_assert(kSmem <= 227 * 1024 - 1536, "and barriers, units and row statistics beside it");
+  static_assert(kSmem <= 227 * 1024 - 2048, "and barriers, units and row statistics beside it");
+};
+
+// Place and phase of a ring's user that takes more than one step at a time.
+template <int K>
+struct Ring {
+  int at;
+  uint32_t ph = 0;
+  __device__ __forceinline__ explicit Ring(int first) : at(0) { step(first); }
+  __device__ __forceinline__ void step(int k) {
+    at += k;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at >= K) at -= K, ph ^= 1u;
+  }
 };
 
 template <int N, int KV>
@@ -59,6 +75,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
                          const __grid_constant__ CUtensorMap map_rope, const LatentAttendArgs A, const LatentParts parts) {
   using S = LatentShape<N, KV>;
   constexpr bool kRecord = S::kRecord;
+  constexpr int kLoadWarp = S::kLoadWarp, kFixWarp0 = S::kFixWarp0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_buf = smem;                                  // (S reads 64 rows of each atom: up to 6 KB past the last)
@@ -71,10 +88,11 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ uint64_t pair_full[S::kPairs], pair_empty[S::kPairs], rope_full[S::kRopes], rope_empty[S::kRopes];
   __shared__ uint64_t code_full[kRecord ? S::kCodes : 1], code_empty[kRecord ? S::kCodes : 1];
   __shared__ uint64_t scale_full[kRecord ? kScaleSlots : 1];
-  __shared__ uint64_t q_full, s_full[S::kSlots], s_empty[S::kSlots], p_full[S::kPs], p_empty[S::kPs], o_done[2], drain[2];   // o_done: of even and odd units
+  __shared__ uint64_t q_full, q_free, s_full[S::kSlots], s_empty[S::kSlots], p_full[S::kPs], p_empty[S::kPs];
+  __shared__ uint64_t o_done[2], drain[4];                // o_done: of even and odd units
   __shared__ LatentUnit s_unit[kUnits];
   __shared__ uint32_t s_bad[kUnits][2];                   // keys with a value that is not finite
-  __shared__ float s_keep[N], s_max[N], s_sum[N];
+  __shared__ float s_keep[N], s_top[2][N], s_sum[2][N];
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -84,7 +102,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(smem_u32(&u_full[i]), 1);
       mbar_init(smem_u32(&u_loaded[i]), 1);
-      mbar_init(smem_u32(&u_empty[i]), 4 + S::kFixWarps);
+      mbar_init(smem_u32(&u_empty[i]), kSoftWarps + S::kFixWarps);
       mbar_init(smem_u32(&e_full[i]), S::kFixWarps);
     }
     for (int i = 0; i < S::kPairs; ++i) {
@@ -103,22 +121,22 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       }
     }
     mbar_init(smem_u32(&q_full), 1);
+    mbar_init(smem_u32(&q_free), 2);
     for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_empty[i]), N / 16);
+      mbar_init(smem_u32(&s_full[i]), kRecord ? 1 : 2);
+      mbar_init(smem_u32(&s_empty[i]), N / 8);
     }
     for (int i = 0; i < S::kPs; ++i) {
-      mbar_init(smem_u32(&p_full[i]), kRecord ? N / 16 : 4);
+      mbar_init(smem_u32(&p_full[i]), kRecord ? N / 8 : kSoftWarps);
       mbar_init(smem_u32(&p_empty[i]), 1);
     }
-    mbar_init(smem_u32(&o_done[0]), 1);
-    mbar_init(smem_u32(&o_done[1]), 1);
-    mbar_init(smem_u32(&drain[0]), 1);
-    mbar_init(smem_u32(&drain[1]), 1);
+    mbar_init(smem_u32(&o_done[0]), S::kValueWarps);
+    mbar_init(smem_u32(&o_done[1]), S::kValueWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&drain[i]), 1);
     s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp0) {
     tmem_alloc(smem_u32(&s_tmem), kTmem);
     tmem_relinquish();
   }
@@ -216,27 +234,25 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 1000000ull) {}
     }
-  } else if (warp == kMmaWarp || warp == kValueWarp) {
+  } else if (warp >= kScoreWarp0 && warp < kLoadWarp) {
     // ------------------------------------------------------------ MMA issue: scores, values
     const bool issuer = elect_one();
+    const int half = (warp - kScoreWarp0) & 1;    // pairs half and half + 2 of a page; the first has the rotated part
     bool ok = tmem == 0;                          // all 512 columns are this block's
     if (!ok) {
       *abort = 1;
       record_error(A.err, kDevTimeout);
     }
-    if (warp == kMmaWarp) {
+    if (warp < kValueWarp0) {
+      Ring<S::kPairs> pair(half);
       constexpr uint32_t idesc = make_idesc(64, kPage, kFmtBF16, kFmtBF16, 0, 0);
       const uint64_t dq = smem_desc(smem_u32(q_buf), 0, 1024, kSwizzle128B);
       const uint64_t dk = smem_desc(smem_u32(pair_buf), 0, 1024, kSwizzle128B);
       const uint64_t dr = smem_desc(smem_u32(rope_buf), 0, 1024, kSwizzle128B);
-      int pair = 0, rope = 0, slot = 0, edges = 0;
-      uint32_t pair_ph = 0, rope_ph = 0, slot_ph = 0, q_ph = 0;
-      // the next place of scores is free / is done
-      auto place = [&]() { return warp_wait(&s_empty[slot], slot_ph ^ 1, abort, A.err); };
-      auto placed = [&]() {
-        if (issuer) mma_commit(smem_u32(&s_full[slot]));
-        if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
-      };
+      Ring<S::kRopes> rope(0);
+      Ring<S::kSlots> slot(kRecord ? 2 * half : 0);   // records: places 0 (the rotated part's), 1 and 3, or 2 and 4 of a page's five
+      int edges = 0;
+      uint32_t seg = 0;
       for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
         ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
@@ -244,62 +260,72 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         flags = s_unit[us].flags;
         if (flags & kStop) break;
         if (flags & kFirst) {
-          // the last segment's scores have left the queries' place
-          if (n > 0) ok = slot > 0 ? warp_wait(&s_full[slot - 1], slot_ph, abort, A.err)
-                                   : warp_wait(&s_full[S::kSlots - 1], slot_ph ^ 1, abort, A.err);
-          if (ok && issuer) {
-            const uint32_t bar = smem_u32(&q_full);
-            mbar_arrive_expect_tx(bar, S::kQBytes);
-            tma_load_3d(smem_u32(q_buf), &map_q, bar, 0, (int)s_unit[us].out, 0);
+          if (half == 0) {
+            // the last segment's scores have left the queries' place
+            if (seg > 0) ok = warp_wait(&q_free, (seg - 1) & 1, abort, A.err);
+            if (ok && issuer) {
+              const uint32_t bar = smem_u32(&q_full);
+              mbar_arrive_expect_tx(bar, S::kQBytes);
+              tma_load_3d(smem_u32(q_buf), &map_q, bar, 0, (int)s_unit[us].out, 0);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          ok = ok && warp_wait(&q_full, q_ph, abort, A.err);
-          q_ph ^= 1u;
+          ok = ok && warp_wait(&q_full, seg & 1, abort, A.err);
+          ++seg;
         }
-        ok = ok && place() && warp_wait(&rope_full[rope], rope_ph, abort, A.err);
-        if (!ok) break;
-        uint32_t d = S::kSCol + slot * kPage;
-        tc_fence_after();
-        if (issuer) {
-          const uint64_t kd = desc_add(dr, rope * kRopeBytes), qd = desc_add(dq, 8 * N * 128);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc, k != 0);
-          mma_commit(smem_u32(&rope_empty[rope]));
-        }
-        if (kRecord) placed();                    // records: each scale's scores go to a place of their own
-        __syncwarp();
-        if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          if (kRecord) {
-            ok = place();
-            d = S::kSCol + slot * kPage;
-          }
-          ok = ok && warp_wait(&pair_full[pair], pair_ph, abort, A.err);
-          if (!kRecord && j == 0 && (flags & kEdge) && ok) {   // (records: the conversion has done it)
-            ok = warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err);
-            ++edges;
-          }
+        if (!kRecord || half == 0) ok = ok && warp_wait(&s_empty[slot.at], slot.ph ^ 1, abort, A.err);
+        uint32_t d = S::kSCol + slot.at * S::kSlotCols + (kRecord ? 0 : half * kPage);
+        if (half == 0) {
+          ok = ok && warp_wait(&rope_full[rope.at], rope.ph, abort, A.err);
           if (!ok) break;
           tc_fence_after();
           if (issuer) {
-            const uint64_t kd = desc_add(dk, pair * kPairBytes), qd = desc_add(dq, 2 * j * N * 128);
+            const uint64_t kd = desc_add(dr, rope.at * kRopeBytes), qd = desc_add(dq, 8 * N * 128);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc, k != 0);
+            mma_commit(smem_u32(&rope_empty[rope.at]));
+            if (kRecord) mma_commit(smem_u32(&s_full[slot.at]));
+          }
+          __syncwarp();
+          rope.step(1);
+          if (kRecord) slot.step(1);
+        }
+        if (!kRecord && (flags & kEdge)) {        // (records: the conversion has done it)
+          ok = ok && warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err);
+          ++edges;
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; ++i) {
+          const int j = half + 2 * i;
+          if (kRecord) {                          // each scale's scores go to a place of their own
+            ok = warp_wait(&s_empty[slot.at], slot.ph ^ 1, abort, A.err);
+            d = S::kSCol + slot.at * S::kSlotCols;
+          }
+          ok = ok && warp_wait(&pair_full[pair.at], pair.ph, abort, A.err);
+          if (!ok) break;
+          tc_fence_after();
+          if (issuer) {
+            const uint64_t kd = desc_add(dk, pair.at * kPairBytes), qd = desc_add(dq, 2 * j * N * 128);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               mma_f16_ss(d, desc_add(qd, (k >> 2) * N * 128 + (k & 3) * 32),
-                         desc_add(kd, (k >> 2) * (kPage * 128) + (k & 3) * 32), idesc, !kRecord || k != 0);
+                         desc_add(kd, (k >> 2) * (kPage * 128) + (k & 3) * 32), idesc, kRecord || (half && i == 0) ? k != 0 : 1);
+            if (kRecord || i == 1) mma_commit(smem_u32(&s_full[slot.at]));
+            if (i == 1 && (flags & kLast)) mma_commit(smem_u32(&q_free));
           }
-          if (kRecord || j == 3) placed();
           __syncwarp();
-          if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
+          pair.step(2);
+          if (kRecord) slot.step(i == 0 ? 2 : half ? 3 : 2);   // (to place 3 or 4, then to the next page's first)
+          else if (i == 1) slot.step(1);
         }
       }
     } else {
       constexpr uint32_t idesc = make_idesc(128, N, kFmtBF16, kFmtBF16, 1, 0);
       const uint64_t dv = smem_desc(smem_u32(pair_buf), kPage * 128, 1024, kSwizzle128B);
       const uint64_t dp = smem_desc(smem_u32(p_buf), 0, 1024, kSwizzle128B);
-      int pair = 0, ps = 0;
-      uint32_t ps_ph = 0;
+      constexpr int kStep = S::kValueWarps;       // a warp's pairs: half and every kStep-th from there
+      Ring<S::kPairs> pair(half);
+      Ring<S::kPs> ps(kRecord ? half : 0);
       for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
         ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
@@ -308,32 +334,31 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         if (flags & kStop) break;
         const uint32_t kept = flags & kFirst ? 0u : 1u;
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
+        for (int j = half; j < 4; j += kStep) {
           // (P is behind the scores, and so behind the pairs' arrival)
-          if (kRecord || j == 0) ok = warp_wait(&p_full[ps], ps_ph, abort, A.err);
+          if (kRecord || j == half) ok = warp_wait(&p_full[ps.at], ps.ph, abort, A.err);
           if (!ok) break;
           tc_fence_after();
           if (issuer) {
-            const uint64_t vd = desc_add(dv, pair * kPairBytes), pd = desc_add(dp, ps * S::kPBytes);
+            const uint64_t vd = desc_add(dv, pair.at * kPairBytes), pd = desc_add(dp, ps.at * S::kPBytes);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
-            mma_commit(smem_u32(&pair_empty[pair]));
-            if (j == 3) mma_commit(smem_u32(&o_done[n & 1]));
-            if (kRecord) mma_commit(smem_u32(&p_empty[ps]));
+            mma_commit(smem_u32(&pair_empty[pair.at]));
+            if (kRecord) mma_commit(smem_u32(&p_empty[ps.at]));
+            if (j + kStep >= 4) mma_commit(smem_u32(&o_done[n & 1]));
           }
           __syncwarp();
-          if (++pair == S::kPairs) pair = 0;
-          if (kRecord || j == 3) {
-            if (++ps == S::kPs) ps = 0, ps_ph ^= 1u;
-          }
+          pair.step(kStep);
+          if (kRecord) ps.step(kStep);
+          else if (j + kStep >= 4) ps.step(1);
         }
       }
     }
     // Everything issued has finished before tensor and shared memory are given back.
     __syncwarp();
     if (issuer) {
-      const uint32_t bar = smem_u32(&drain[warp - kMmaWarp]);
+      const uint32_t bar = smem_u32(&drain[warp - kScoreWarp0]);
       mma_commit(bar);
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(bar, 0)) {
@@ -444,64 +469,72 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const bool active = 16 * warp < N;
-    const uint32_t quarter = tmem + ((uint32_t)(32 * warp) << 16);
-    const int r0 = 16 * warp + (lane >> 2);       // this thread's rows: r0 and r0 + 8
+    const int w4 = warp & 3, half = warp >> 2;    // lane quarter; keys 32 * half and on
+    const bool active = 16 * w4 < N;
+    const uint32_t quarter = tmem + ((uint32_t)(32 * w4) << 16);
+    const int r0 = 16 * w4 + (lane >> 2);         // this thread's rows: r0 and r0 + 8
+    const int key0 = 32 * half + 2 * (lane & 3);  // and keys: key0 + 8 j and the next, j < 4
     const float f = fmaxf(A.scale_log2, 1.17549435e-38f);   // (a scale of 0 would make masked scores NaN)
     float M[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
-    int slot = 0, ps = 0;                         // records: places of scores and of P
-    uint32_t slot_ph = 0, ps_ph = 0;
+    Ring<S::kSlots> slot(0);
+    Ring<S::kPs> ps(0);
     bool ok = true;
     for (int n = 0;; ++n) {
       const int us = n % kUnits;
-      const float* scales = scale_buf + (n % kScaleSlots) * 256 + 8 * (lane & 3);   // of this thread's keys
       ok = ok && warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
       LatentUnit x{};
       if (ok) x = s_unit[us];
       if (x.flags & kFirst) M[0] = M[1] = kNone, l[0] = l[1] = 0.f;
-      float s[32];
+      float s[16];
+      float4 c[kRecord ? 8 : 1];                  // the four scales of this thread's keys
       // (warps without rows do not look at the scores' barriers, which may be two pages ahead of them)
       if (!active || (x.flags & kStop)) {
       } else if constexpr (!kRecord) {
-        ok = ok && warp_wait(&s_full[n & 1], (n >> 1) & 1, abort, A.err);
+        ok = ok && warp_wait(&s_full[slot.at], slot.ph, abort, A.err);
         if (ok) {
+          float t[16];
           tc_fence_after();
-          tmem_ld_16x64(quarter + S::kSCol + (n & 1) * kPage, s);
+          tmem_ld_16x32(quarter + S::kSCol + slot.at * S::kSlotCols + 32 * half, s);
+          tmem_ld_16x32(quarter + S::kSCol + slot.at * S::kSlotCols + kPage + 32 * half, t);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s_empty[n & 1]));
+          if (lane == 0) mbar_arrive(smem_u32(&s_empty[slot.at]));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) s[j] += t[j];
         }
+        slot.step(1);
       } else {
         ok = ok && warp_wait(&scale_full[n % kScaleSlots], (n / kScaleSlots) & 1, abort, A.err);
-#pragma unroll 1
-        for (int g = -1; g < 4 && ok; ++g) {      // the rotated part, then each scale's
-          ok = warp_wait(&s_full[slot], slot_ph, abort, A.err);
-          if (!ok) break;
-          tc_fence_after();
-          float t[32];
-          tmem_ld_16x64(quarter + S::kSCol + slot * kPage, t);
-          tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s_empty[slot]));
-          if (++slot == S::kSlots) slot = 0, slot_ph ^= 1u;
-          if (g < 0) {
+        const float4* scales = reinterpret_cast<const float4*>(scale_buf) + (n % kScaleSlots) * kPage + key0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = t[j];
-          } else {
+        for (int j = 0; j < 4; ++j) c[2 * j] = scales[8 * j], c[2 * j + 1] = scales[8 * j + 1];
+#pragma unroll
+        for (int g = -1; g < 4; ++g) {            // the rotated part, then each scale's
+          ok = ok && warp_wait(&s_full[slot.at], slot.ph, abort, A.err);
+          if (ok) {
+            float t[16];
+            tc_fence_after();
+            tmem_ld_16x32(quarter + S::kSCol + slot.at * S::kSlotCols + 32 * half, t);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_empty[slot.at]));
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float c0 = scales[32 * j + g], c1 = scales[32 * j + 4 + g];
-              s[4 * j] = fmaf(t[4 * j], c0, s[4 * j]), s[4 * j + 1] = fmaf(t[4 * j + 1], c1, s[4 * j + 1]);
-              s[4 * j + 2] = fmaf(t[4 * j + 2], c0, s[4 * j + 2]), s[4 * j + 3] = fmaf(t[4 * j + 3], c1, s[4 * j + 3]);
+              const float k = g < 0 ? 1.f : reinterpret_cast<const float*>(&c[j])[g < 0 ? 0 : g];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float& v = s[4 * (j >> 1) + 2 * i + (j & 1)];
+                v = g < 0 ? t[4 * (j >> 1) + 2 * i + (j & 1)] : fmaf(t[4 * (j >> 1) + 2 * i + (j & 1)], k, v);
+              }
             }
           }
+          slot.step(1);
         }
       }
       int lim[2] = {kPage, kPage};                // last key that the rows see
       bool need = false;
-      float top[2] = {-INFINITY, -INFINITY};
       if (active && ok && !(x.flags & kStop)) {
         if (x.flags & kEdge) {
           const uint64_t bad = (uint64_t)s_bad[us][0] | (uint64_t)s_bad[us][1] << 32;
@@ -510,10 +543,10 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             const int row = r0 + 8 * i;
             lim[i] = row < x.rows && !(x.flags & kVoid) ? x.rel + (x.row0 + row) / A.H : -1;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int key = 8 * j + 2 * (lane & 3) + e;
+                const int key = key0 + 8 * j + e;
                 float& v = s[4 * j + 2 * i + e];
                 if (key > lim[i]) v = -INFINITY;
                 else if (bad >> key & 1) v = NAN;
@@ -525,31 +558,33 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
           float m = fmaxf(s[2 * i], s[2 * i + 1]);
 #pragma unroll
-          for (int j = 1; j < 8; ++j) m = max3(m, s[4 * j + 2 * i], s[4 * j + 2 * i + 1]);
+          for (int j = 1; j < 4; ++j) m = max3(m, s[4 * j + 2 * i], s[4 * j + 2 * i + 1]);
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          top[i] = m * f;
-          if (x.flags & kFirst) M[i] = fmaxf(top[i], kNone);
-          else need |= r0 + 8 * i < x.rows && top[i] > M[i] + kMove;
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2)) * f;
+          if ((lane & 3) == 0) s_top[half][r0 + 8 * i] = m;
+          need |= r0 + 8 * i < x.rows && m > M[i] + kMove;
         }
       }
-      // (all four warps come here in every round, those that gave up too)
-      if (bar_any(1, 128, need || !ok)) {
-        if (active && ok) {
+      // The reference moves. (All eight warps come here in every round, those that gave up too;
+      // an item's first unit comes here whether or not a row sees a key of it.)
+      if (bar_any(1, 32 * kSoftWarps, need || !ok || (x.flags & kFirst))) {
+        if (active && ok && !(x.flags & kStop)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
+            const float m = fmaxf(s_top[0][r0 + 8 * i], s_top[1][r0 + 8 * i]);
             float keep = 1.f;
-            if (top[i] > M[i] + kMove) keep = ex2(M[i] - top[i]), M[i] = top[i], l[i] *= keep;
-            if ((lane & 3) == 0) s_keep[r0 + 8 * i] = keep;
+            if (x.flags & kFirst) M[i] = fmaxf(m, kNone);
+            else if (m > M[i] + kMove) keep = ex2(M[i] - m), M[i] = m, l[i] *= keep;
+            if (half == 0 && (lane & 3) == 0) s_keep[r0 + 8 * i] = keep;
           }
         }
-        if (!bar_all(1, 128, ok)) break;
+        if (!bar_all(1, 32 * kSoftWarps, ok)) break;
         if (!(x.flags & (kFirst | kStop))) {      // O so far, once its last product is done
           ok = warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
           if (ok) {
             tc_fence_after();
 #pragma unroll 1
-            for (int k = 0; k < 4 * N; k += 16) {
+            for (int k = 2 * N * half; k < 2 * N * (half + 1); k += 16) {
               float v[16];
               tmem_ld16(quarter + k, v);
               tmem_ld_wait();
@@ -558,63 +593,63 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
               tmem_st16(quarter + k, v);
             }
             tmem_st_wait();
+            tc_fence_before();
           }
+          // (records: warps without rows hand over no weights, so the others wait for theirs)
+          if (kRecord && N < 64 && !bar_all(1, 32 * kSoftWarps, ok)) break;
         }
       }
       if (x.flags & kStop) break;
       if (active && ok) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float a = 0.f, c = 0.f;
+          float a = 0.f, b = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             float &u = s[4 * j + 2 * i], &w = s[4 * j + 2 * i + 1];
             u = ex2(fmaf(u, f, -M[i])), w = ex2(fmaf(w, f, -M[i]));
-            a += u, c += w;
+            a += u, b += w;
           }
-          l[i] += a + c;
+          l[i] += a + b;
         }
       }
-      uint8_t* p_row = p_buf + r0 * 128 + 4 * (lane & 3);   // (r0 + 8 has the same swizzle)
+      // this lane's row of a 16 x 32 piece's four 8 x 8 matrices (stored with rows r0 of all, then r0 + 8)
+      const uint32_t p_row = smem_u32(p_buf) + (16 * w4 + (lane & 7)) * 128 + (((4 * half + (lane >> 3)) ^ (lane & 7)) << 4);
       if constexpr (!kRecord) {
         // the last page's values have left P's place
         if (n > 0) ok = ok && warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
         if (active && ok) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint8_t* dst = p_row + ((j ^ (r0 & 7)) << 4);
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(s[4 * j], s[4 * j + 1]);
-            *reinterpret_cast<uint32_t*>(dst + 8 * 128) = pack_bf16(s[4 * j + 2], s[4 * j + 3]);
-          }
+          for (int i = 0; i < 2; ++i)
+            store_matrices(p_row + i * 1024, pack_bf16(s[2 * i], s[2 * i + 1]), pack_bf16(s[4 + 2 * i], s[5 + 2 * i]),
+                           pack_bf16(s[8 + 2 * i], s[9 + 2 * i]), pack_bf16(s[12 + 2 * i], s[13 + 2 * i]));
           fence_proxy_async_smem();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full[0]));
       } else if (active) {
-#pragma unroll 1
-        for (int g = 0; g < 4 && ok; ++g) {       // each scale's codes get its weights
-          ok = warp_wait(&p_empty[ps], ps_ph ^ 1, abort, A.err);
-          if (!ok) break;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float c0 = scales[32 * j + g], c1 = scales[32 * j + 4 + g];
-            float v[4] = {s[4 * j] * c0, s[4 * j + 1] * c1, s[4 * j + 2] * c0, s[4 * j + 3] * c1};
-            if (x.flags & kEdge) {                // (an unseen key's scale may be anything)
-              const int key = 8 * j + 2 * (lane & 3);
+        for (int g = 0; g < 4; ++g) {             // each scale's codes get its weights
+          ok = ok && warp_wait(&p_empty[ps.at], ps.ph ^ 1, abort, A.err);
+          if (ok) {
+            float v[16];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (key + (e & 1) > lim[e >> 1]) v[e] = 0.f;
+            for (int j = 0; j < 16; ++j) {
+              v[j] = s[j] * reinterpret_cast<const float*>(&c[2 * (j >> 2) + (j & 1)])[g];
+              // (an unseen key's scale may be anything)
+              if ((x.flags & kEdge) && key0 + 8 * (j >> 2) + (j & 1) > lim[j >> 1 & 1]) v[j] = 0.f;
             }
-            uint8_t* dst = p_row + ps * S::kPBytes + ((j ^ (r0 & 7)) << 4);
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v[0], v[1]);
-            *reinterpret_cast<uint32_t*>(dst + 8 * 128) = pack_bf16(v[2], v[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              store_matrices(p_row + ps.at * S::kPBytes + i * 1024, pack_bf16(v[2 * i], v[2 * i + 1]), pack_bf16(v[4 + 2 * i], v[5 + 2 * i]),
+                             pack_bf16(v[8 + 2 * i], v[9 + 2 * i]), pack_bf16(v[12 + 2 * i], v[13 + 2 * i]));
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[ps.at]));
           }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&p_full[ps]));
-          if (++ps == S::kPs) ps = 0, ps_ph ^= 1u;
+          ps.step(1);
         }
       }
       if (x.flags & kLast) {
@@ -624,22 +659,27 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           for (int i = 0; i < 2; ++i) {
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if ((lane & 3) == 0) s_max[r0 + 8 * i] = M[i], s_sum[r0 + 8 * i] = l[i];
+            if ((lane & 3) == 0) s_sum[half][r0 + 8 * i] = l[i];
           }
         }
-        if (!bar_all(1, 128, ok)) break;
+        if (!bar_all(1, 32 * kSoftWarps, ok)) break;
         // (two barriers, for a warp may come here before unit n - 1's values are done or after unit n's)
         ok = warp_wait(&o_done[n & 1], (n >> 1) & 1, abort, A.err);
         if (ok) {
           tc_fence_after();
-          const int t = warp * 32 + lane;
-          if (t < x.rows) {
-            const float sum = s_sum[t], mx = s_max[t];
-            if (x.slot >= 0) *reinterpret_cast<float2*>(parts.ml + ((int64_t)x.slot * N + t) * 2) = make_float2(mx, sum);
-            else if (A.lse) A.lse[x.out + t] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+          const int t = w4 * 32 + lane;
+          if (half == 0 && active && (lane & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = r0 + 8 * i;
+              const float sum = s_sum[0][row] + s_sum[1][row];
+              if (row >= x.rows) continue;
+              if (x.slot >= 0) *reinterpret_cast<float2*>(parts.ml + ((int64_t)x.slot * N + row) * 2) = make_float2(M[i], sum);
+              else if (A.lse) A.lse[x.out + row] = sum == 0.f ? -INFINITY : (M[i] + log2f(sum)) * 0.6931471805599453f;
+            }
           }
 #pragma unroll 1
-          for (int k = 0; k < 4 * N; k += 16) {
+          for (int k = 2 * N * half; k < 2 * N * (half + 1); k += 16) {
             float v[16];
             tmem_ld16(quarter + k, v);
             tmem_ld_wait();
@@ -654,11 +694,11 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
               __nv_bfloat16* dst = A.out + (x.out + row + (lane & 1)) * kDimLatent + (dim & ~1);
 #pragma unroll
               for (int j = 0; j < 16; j += 2) {
-                const float s0 = s_sum[row + j], s1 = s_sum[row + j + 1];
-                const float a = s0 == 0.f ? 0.f : v[j] / s0, c = s1 == 0.f ? 0.f : v[j + 1] / s1;
-                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : c, 1);
+                const float s0 = s_sum[0][row + j] + s_sum[1][row + j], s1 = s_sum[0][row + j + 1] + s_sum[1][row + j + 1];
+                const float a = s0 == 0.f ? 0.f : v[j] / s0, b = s1 == 0.f ? 0.f : v[j + 1] / s1;
+                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
                 if (row + j + (lane & 1) < x.rows)
-                  *reinterpret_cast<uint32_t*>(dst + (int64_t)j * kDimLatent) = lane & 1 ? pack_bf16(other, c) : pack_bf16(a, other);
+                  *reinterpret_cast<uint32_t*>(dst + (int64_t)j * kDimLatent) = lane & 1 ? pack_bf16(other, b) : pack_bf16(a, other);
               }
             }
           }
@@ -667,13 +707,13 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(smem_u32(&u_empty[us]));
-      // (past the round's vote all four warps know the unit, and so leave together)
+      // (past the round's vote all eight warps know the unit, and so leave together)
       if (x.flags & kEnd) break;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmem);
   }
