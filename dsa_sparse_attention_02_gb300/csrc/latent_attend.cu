@@ -39,7 +39,7 @@ struct LatentShape {
   // Rings as deep as shared memory allows.
   static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 64 ? 6 : 8);
   static constexpr int kRopes = !kRecord && N == 16 ? 3 : 2;
-  static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 2 : N == 32 ? 4 : 6;
+  static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 2 : N == 32 ? 3 : 6;
   // Scores: a page's of bf16 rows in one place, two pages at a time; of records in one place for
   // each scale (and the rotated part), in a ring. P: one of a page, or a ring of one for each scale.
   static constexpr int kSlots = !kRecord ? 2 : N == 64 ? 4 : 6;
@@ -52,8 +52,40 @@ struct LatentShape {
   static constexpr int kQBytes = 9 * N * 128, kPBytes = N * 128;   // of one P
   static constexpr int kSmem = 1024 + kQBytes + kPs * kPBytes + kRopes * kRopeBytes + kPairs * kPairBytes + kCodes * kCodeStage +
                                (kRecord ? kScaleSlots * 1024 : 0);
-  static_assert(kSmem <= 227 * 1024 - 2048, "and barriers, units and row statistics beside it");
+  static_assert(kSmem <= 227 * 1024 - (kRecord ? 3328 : 2048), "and barriers, units and row statistics beside it");
 };
+
+// Queries of records: the latent part of N rows in shared memory, bf16 to f16, each row by a power of
+// two that brings its largest magnitude into [2^13, 2^14) (what lies 2^31 below that may round; the
+// rest is exact). factor[row] undoes it. For 256 threads.
+template <int N>
+__device__ __forceinline__ void queries_f16(uint8_t* q_buf, int tid, float* factor) {
+  constexpr int kPer = 32 * kSoftWarps / N, kChunks = 64 / kPer;   // threads of a row, its 16-byte chunks a thread has
+  const int row = tid / kPer, c0 = tid % kPer;
+  auto chunk = [&](int i) {
+    const int c = c0 + i * kPer;
+    return reinterpret_cast<uint4*>(q_buf + (c >> 3) * (N * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+  };
+  uint32_t top = 0;                              // largest magnitude, as bf16 bits
+#pragma unroll 4
+  for (int i = 0; i < kChunks; ++i) {
+    const uint4 v = *chunk(i);
+    const uint32_t o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max(o[e] & 0x7FFFu, o[e] >> 16 & 0x7FFFu));
+  }
+#pragma unroll
+  for (int o = 1; o < kPer; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int e = min(max((int)(top >> 7) - 127, -60), 127);
+  const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+  if (c0 == 0) factor[row] = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+#pragma unroll 4
+  for (int i = 0; i < kChunks; ++i) {
+    const uint4 v = *chunk(i);
+    *chunk(i) = make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                           pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+  }
+}
 
 // Place and phase of a ring's user that takes more than one step at a time.
 template <int K>
@@ -76,6 +108,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   using S = LatentShape<N, KV>;
   constexpr bool kRecord = S::kRecord;
   constexpr int kLoadWarp = S::kLoadWarp, kFixWarp0 = S::kFixWarp0;
+  constexpr uint32_t kFmt = kRecord ? kFmtF16 : kFmtBF16;   // of latents, and of weights
+  // Weights in f16 use its range upwards as well: 2^7 at the reference, and so below 2^16.
+  constexpr float kLift = kRecord ? 7.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_buf = smem;                                  // (S reads 64 rows of each atom: up to 6 KB past the last)
@@ -89,10 +124,11 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ uint64_t code_full[kRecord ? S::kCodes : 1], code_empty[kRecord ? S::kCodes : 1];
   __shared__ uint64_t scale_full[kRecord ? kScaleSlots : 1];
   __shared__ uint64_t q_full, q_free, s_full[S::kSlots], s_empty[S::kSlots], p_full[S::kPs], p_empty[S::kPs];
+  __shared__ uint64_t q_ready;                            // records: the queries are in f16
   __shared__ uint64_t o_done[2], drain[4];                // o_done: of even and odd units
   __shared__ LatentUnit s_unit[kUnits];
   __shared__ uint32_t s_bad[kUnits][2];                   // keys with a value that is not finite
-  __shared__ float s_keep[N], s_top[2][N], s_sum[2][N];
+  __shared__ float s_keep[N], s_top[2][N], s_sum[2][N], s_qf[kRecord ? N : 1], s_lg[kRecord ? kUnits : 1][kPage];
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -122,6 +158,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     }
     mbar_init(smem_u32(&q_full), 1);
     mbar_init(smem_u32(&q_free), 2);
+    mbar_init(smem_u32(&q_ready), kSoftWarps);
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(smem_u32(&s_full[i]), kRecord ? 1 : 2);
       mbar_init(smem_u32(&s_empty[i]), N / 8);
@@ -245,7 +282,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     }
     if (warp < kValueWarp0) {
       Ring<S::kPairs> pair(half);
-      constexpr uint32_t idesc = make_idesc(64, kPage, kFmtBF16, kFmtBF16, 0, 0);
+      constexpr uint32_t idesc_rope = make_idesc(64, kPage, kFmtBF16, kFmtBF16, 0, 0);
+      constexpr uint32_t idesc = make_idesc(64, kPage, kFmt, kFmt, 0, 0);
       const uint64_t dq = smem_desc(smem_u32(q_buf), 0, 1024, kSwizzle128B);
       const uint64_t dk = smem_desc(smem_u32(pair_buf), 0, 1024, kSwizzle128B);
       const uint64_t dr = smem_desc(smem_u32(rope_buf), 0, 1024, kSwizzle128B);
@@ -270,7 +308,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             }
             __syncwarp();
           }
-          ok = ok && warp_wait(&q_full, seg & 1, abort, A.err);
+          ok = ok && warp_wait(kRecord ? &q_ready : &q_full, seg & 1, abort, A.err);
           ++seg;
         }
         if (!kRecord || half == 0) ok = ok && warp_wait(&s_empty[slot.at], slot.ph ^ 1, abort, A.err);
@@ -282,7 +320,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           if (issuer) {
             const uint64_t kd = desc_add(dr, rope.at * kRopeBytes), qd = desc_add(dq, 8 * N * 128);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc, k != 0);
+            for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc_rope, k != 0);
             mma_commit(smem_u32(&rope_empty[rope.at]));
             if (kRecord) mma_commit(smem_u32(&s_full[slot.at]));
           }
@@ -320,7 +358,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
       }
     } else {
-      constexpr uint32_t idesc = make_idesc(128, N, kFmtBF16, kFmtBF16, 1, 0);
+      constexpr uint32_t idesc = make_idesc(128, N, kFmt, kFmt, 1, 0);
       const uint64_t dv = smem_desc(smem_u32(pair_buf), kPage * 128, 1024, kSwizzle128B);
       const uint64_t dp = smem_desc(smem_u32(p_buf), 0, 1024, kSwizzle128B);
       constexpr int kStep = S::kValueWarps;       // a warp's pairs: half and every kStep-th from there
@@ -385,28 +423,50 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         if (flags & kStop) break;
         const bool edge = (flags & kEdge) != 0;
         const int last = s_unit[us].last;
+        // Each key's largest scale, for the weights' reference. In a page not seen whole: scales of keys that no
+        // row sees become 0, and so do those of a key with a NaN or infinity, which is noted.
+        ok = warp_wait(&scale_full[n % kScaleSlots], (n / kScaleSlots) & 1, abort, A.err);
+        if (!ok) break;
+        if (ct < kPage) {
+          float4* at = reinterpret_cast<float4*>(scale_buf) + (n % kScaleSlots) * kPage + ct;
+          const float4 c = *at;
+          const float top = fmaxf(max3(fabsf(c.x), fabsf(c.y), fabsf(c.z)), fabsf(c.w));
+          if (edge) {
+            const bool bad = !(fabsf(c.x) + fabsf(c.y) + fabsf(c.z) + fabsf(c.w) < INFINITY);
+            if (bad && ct <= last) atomicOr(&s_bad[us][ct >> 5], 1u << (ct & 31));
+            if (bad || ct > last) *at = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          s_lg[us][ct] = lg2(fmaxf(top, 7.8886091e-31f));   // (2^-100: all four may be 0)
+        }
+        // eight codes a thread and round: half a warp reads a row's 128, and eight threads write a row of an atom
+        constexpr int kRounds = kPage * 16 / (32 * S::kFixWarps), kRows = 2 * S::kFixWarps;
+        const int row = ct >> 4, ch = ct & 15;
+        const int from = row * 128 + ch * 8, to = (ch >> 3) * (kPage * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+        static_assert(kRows % 8 == 0, "rows of a round have the swizzle of the first");
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
           ok = warp_wait(&code_full[code], code_ph, abort, A.err) && warp_wait(&pair_empty[pair], pair_ph ^ 1, abort, A.err);
           if (!ok) break;
-          const uint8_t* src = code_buf + code * kCodeStage;
-          uint8_t* dst = pair_buf + pair * kPairBytes;
-          // eight codes a thread: half a warp reads a row's 128, and eight threads write a row of an atom
-          constexpr int kPieces = kPage * 16 / (32 * S::kFixWarps);
+          const uint8_t* src = code_buf + code * kCodeStage + from;
+          uint8_t* dst = pair_buf + pair * kPairBytes + to;
+          uint2 w[kRounds];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const int piece = ct + i * 32 * S::kFixWarps, row = piece >> 4, ch = piece & 15;
-            uint2 w = *reinterpret_cast<const uint2*>(src + row * 128 + ch * 8);
-            if (KV == kKvE4m3 && edge) {
-              const uint32_t b0 = __vcmpeq4(w.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), b1 = __vcmpeq4(w.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-              if ((b0 | b1) && row <= last) atomicOr(&s_bad[us][row >> 5], 1u << (row & 31));
-              w.x &= ~b0, w.y &= ~b1;
+          for (int i = 0; i < kRounds; ++i) w[i] = *reinterpret_cast<const uint2*>(src + i * kRows * 128);
+          if (KV == kKvE4m3 && edge) {
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) {
+              const uint32_t b0 = __vcmpeq4(w[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), b1 = __vcmpeq4(w[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              const int key = row + i * kRows;
+              if ((b0 | b1) && key <= last) atomicOr(&s_bad[us][key >> 5], 1u << (key & 31));
+              w[i].x &= ~b0, w[i].y &= ~b1;
             }
-            uint32_t o[4];
-            codes_bf16<KV>(w.x, o[0], o[1]);
-            codes_bf16<KV>(w.y, o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kPage * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+#pragma unroll
+          for (int i = 0; i < kRounds; ++i) {
+            uint4 o;
+            codes_f16<KV == kKvInt8>(w[i].x, o.x, o.y);
+            codes_f16<KV == kKvInt8>(w[i].y, o.z, o.w);
+            *reinterpret_cast<uint4*>(dst + i * kRows * 128) = o;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -478,15 +538,31 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     float M[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
     Ring<S::kSlots> slot(0);
     Ring<S::kPs> ps(0);
+    float qf[2], up[2];                           // records: factors of the rows' scores, and of the rotated part's to theirs
+    uint32_t seg = 0;
     bool ok = true;
     for (int n = 0;; ++n) {
       const int us = n % kUnits;
       ok = ok && warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
       LatentUnit x{};
       if (ok) x = s_unit[us];
-      if (x.flags & kFirst) M[0] = M[1] = kNone, l[0] = l[1] = 0.f;
+      if (x.flags & kFirst) {
+        M[0] = M[1] = kNone, l[0] = l[1] = 0.f;
+        if constexpr (kRecord) {
+          ok = ok && warp_wait(&q_full, seg & 1, abort, A.err);
+          if (ok) queries_f16<N>(q_buf, tid, s_qf);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(smem_u32(&q_ready));
+          ok = ok && warp_wait(&q_ready, seg++ & 1, abort, A.err);
+          if (active) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) qf[i] = s_qf[r0 + 8 * i], up[i] = __frcp_rn(qf[i]), qf[i] *= f;
+          }
+        }
+      }
       float s[16];
-      float4 c[kRecord ? 8 : 1];                  // the four scales of this thread's keys
+      const float* scales = scale_buf + ((n % kScaleSlots) * kPage + key0) * 4;   // of this thread's keys
       // (warps without rows do not look at the scores' barriers, which may be two pages ahead of them)
       if (!active || (x.flags & kStop)) {
       } else if constexpr (!kRecord) {
@@ -505,35 +581,50 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
         slot.step(1);
       } else {
-        ok = ok && warp_wait(&scale_full[n % kScaleSlots], (n / kScaleSlots) & 1, abort, A.err);
-        const float4* scales = reinterpret_cast<const float4*>(scale_buf) + (n % kScaleSlots) * kPage + key0;
+        // (the scales are there, and as the conversion leaves them: the first one's scores are behind it)
+        // the rotated part and the first scale's, the next two, the last (two at a time: it is the
+        // waits that take long)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[2 * j] = scales[8 * j], c[2 * j + 1] = scales[8 * j + 1];
-#pragma unroll
-        for (int g = -1; g < 4; ++g) {            // the rotated part, then each scale's
-          ok = ok && warp_wait(&s_full[slot.at], slot.ph, abort, A.err);
+        for (int g = -1; g < 4; g += 2) {
+          constexpr int kLast2 = 3;
+          float t[2][16];
+          const int s0 = slot.at;
+          ok = ok && warp_wait(&s_full[s0], slot.ph, abort, A.err);
+          slot.step(1);
+          const int s1 = slot.at;
+          if (g < kLast2) {
+            ok = ok && warp_wait(&s_full[s1], slot.ph, abort, A.err);
+            slot.step(1);
+          }
           if (ok) {
-            float t[16];
             tc_fence_after();
-            tmem_ld_16x32(quarter + S::kSCol + slot.at * S::kSlotCols + 32 * half, t);
+            tmem_ld_16x32(quarter + S::kSCol + s0 * S::kSlotCols + 32 * half, t[0]);
+            if (g < kLast2) tmem_ld_16x32(quarter + S::kSCol + s1 * S::kSlotCols + 32 * half, t[1]);
+            float c[2][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float* at = scales + 4 * (8 * (j >> 1) + (j & 1));
+              if (g < 0) c[1][j] = at[0];
+              else if (g < kLast2) c[0][j] = at[g], c[1][j] = at[g + 1];
+              else c[0][j] = at[g];
+            }
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_empty[slot.at]));
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&s_empty[s0]));
+              if (g < kLast2) mbar_arrive(smem_u32(&s_empty[s1]));
+            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float k = g < 0 ? 1.f : reinterpret_cast<const float*>(&c[j])[g < 0 ? 0 : g];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float& v = s[4 * (j >> 1) + 2 * i + (j & 1)];
-                v = g < 0 ? t[4 * (j >> 1) + 2 * i + (j & 1)] : fmaf(t[4 * (j >> 1) + 2 * i + (j & 1)], k, v);
-              }
+            for (int j = 0; j < 16; ++j) {
+              const int k = 2 * (j >> 2) + (j & 1);
+              s[j] = g < 0 ? t[0][j] * up[j >> 1 & 1] : fmaf(t[0][j], c[0][k], s[j]);
+              if (g < kLast2) s[j] = fmaf(t[1][j], c[1][k], s[j]);
+              else s[j] *= qf[j >> 1 & 1];        // in powers of two
             }
           }
-          slot.step(1);
         }
       }
-      int lim[2] = {kPage, kPage};                // last key that the rows see
       bool need = false;
       if (active && ok && !(x.flags & kStop)) {
         if (x.flags & kEdge) {
@@ -541,28 +632,40 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int row = r0 + 8 * i;
-            lim[i] = row < x.rows && !(x.flags & kVoid) ? x.rel + (x.row0 + row) / A.H : -1;
+            const int lim = row < x.rows && !(x.flags & kVoid) ? x.rel + (x.row0 + row) / A.H : -1;   // last key that it sees
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int key = key0 + 8 * j + e;
                 float& v = s[4 * j + 2 * i + e];
-                if (key > lim[i]) v = -INFINITY;
+                if (key > lim) v = -INFINITY;
                 else if (bad >> key & 1) v = NAN;
               }
             }
           }
         }
+        float lg[8] = {};
+        if constexpr (kRecord) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = *reinterpret_cast<const float2*>(&s_lg[us][key0 + 8 * j]);
+            lg[2 * j] = v.x, lg[2 * j + 1] = v.y;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float m = fmaxf(s[2 * i], s[2 * i + 1]);
+          float m = -INFINITY;
 #pragma unroll
-          for (int j = 1; j < 4; ++j) m = max3(m, s[4 * j + 2 * i], s[4 * j + 2 * i + 1]);
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (kRecord) m = max3(m, s[4 * j + 2 * i] + lg[2 * j], s[4 * j + 2 * i + 1] + lg[2 * j + 1]);
+            else m = max3(m, s[4 * j + 2 * i], s[4 * j + 2 * i + 1]);
+          }
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2)) * f;
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          if (!kRecord) m *= f;
           if ((lane & 3) == 0) s_top[half][r0 + 8 * i] = m;
-          need |= r0 + 8 * i < x.rows && m > M[i] + kMove;
+          need |= r0 + 8 * i < x.rows && m - kLift > M[i] + kMove;
         }
       }
       // The reference moves. (All eight warps come here in every round, those that gave up too;
@@ -571,7 +674,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         if (active && ok && !(x.flags & kStop)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float m = fmaxf(s_top[0][r0 + 8 * i], s_top[1][r0 + 8 * i]);
+            const float m = fmaxf(s_top[0][r0 + 8 * i], s_top[1][r0 + 8 * i]) - kLift;
             float keep = 1.f;
             if (x.flags & kFirst) M[i] = fmaxf(m, kNone);
             else if (m > M[i] + kMove) keep = ex2(M[i] - m), M[i] = m, l[i] *= keep;
@@ -607,7 +710,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float &u = s[4 * j + 2 * i], &w = s[4 * j + 2 * i + 1];
-            u = ex2(fmaf(u, f, -M[i])), w = ex2(fmaf(w, f, -M[i]));
+            u = ex2(kRecord ? u - M[i] : fmaf(u, f, -M[i])), w = ex2(kRecord ? w - M[i] : fmaf(w, f, -M[i]));
             a += u, b += w;
           }
           l[i] += a + b;
@@ -630,26 +733,39 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full[0]));
       } else if (active) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {             // each scale's codes get its weights
-          ok = ok && warp_wait(&p_empty[ps.at], ps.ph ^ 1, abort, A.err);
+        for (int g = 0; g < 4; g += 2) {          // each scale's codes get its weights
+          const int p0 = ps.at;
+          ok = ok && warp_wait(&p_empty[p0], ps.ph ^ 1, abort, A.err);
+          ps.step(1);
+          const int p1 = ps.at;
+          ok = ok && warp_wait(&p_empty[p1], ps.ph ^ 1, abort, A.err);
+          ps.step(1);
           if (ok) {
-            float v[16];
+            float c[2][8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              v[j] = s[j] * reinterpret_cast<const float*>(&c[2 * (j >> 2) + (j & 1)])[g];
-              // (an unseen key's scale may be anything)
-              if ((x.flags & kEdge) && key0 + 8 * (j >> 2) + (j & 1) > lim[j >> 1 & 1]) v[j] = 0.f;
+            for (int j = 0; j < 8; ++j) {
+              const float* at = scales + 4 * (8 * (j >> 1) + (j & 1));
+              c[0][j] = at[g], c[1][j] = at[g + 1];
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              store_matrices(p_row + ps.at * S::kPBytes + i * 1024, pack_bf16(v[2 * i], v[2 * i + 1]), pack_bf16(v[4 + 2 * i], v[5 + 2 * i]),
-                             pack_bf16(v[8 + 2 * i], v[9 + 2 * i]), pack_bf16(v[12 + 2 * i], v[13 + 2 * i]));
+            for (int h = 0; h < 2; ++h) {
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = s[j] * c[h][2 * (j >> 2) + (j & 1)];
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                store_matrices(p_row + (h ? p1 : p0) * S::kPBytes + i * 1024, pack_weights(v[2 * i], v[2 * i + 1]),
+                               pack_weights(v[4 + 2 * i], v[5 + 2 * i]), pack_weights(v[8 + 2 * i], v[9 + 2 * i]),
+                               pack_weights(v[12 + 2 * i], v[13 + 2 * i]));
+            }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_full[ps.at]));
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&p_full[p0]));
+              mbar_arrive(smem_u32(&p_full[p1]));
+            }
           }
-          ps.step(1);
         }
       }
       if (x.flags & kLast) {

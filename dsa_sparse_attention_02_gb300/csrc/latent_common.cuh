@@ -34,6 +34,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Barrier `id` among `count` threads that also tells whether any / all of them say so.
 __device__ __forceinline__ bool bar_any(int id, int count, bool p) {
   uint32_t r;

@@ -23,27 +23,6 @@ struct __align__(16) LatentUnit {
   int64_t out;          // global number of the item's first row
 };
 
-// bf16 pairs of a word's four codes, exact: (byte 0, byte 1) and (byte 2, byte 3).
-template <int KV>
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (KV == kKvInt8) {
-    // 0x43vv is 128 + vv of the low seven bits, 0x4300 or 0x4380 (by the sign bit) 128 or 256
-    auto two = [](uint32_t x) {
-      const uint32_t v = (x & 0x007F007Fu) | 0x43004300u, s = (x & 0x00800080u) | 0x43004300u;
-      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&s));
-      return *reinterpret_cast<const uint32_t*>(&d);
-    };
-    lo = two(__byte_perm(w, 0, 0x4140));
-    hi = two(__byte_perm(w, 0, 0x4342));
-  } else {
-    uint32_t a, b;
-    codes_f16<false>(w, a, b);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
-    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    lo = pack_bf16(f.x, f.y), hi = pack_bf16(g.x, g.y);
-  }
-}
-
 // Requests as the items see them.
 struct LatentReq {
   int q0, n, start;      // first token, tokens, position of the first (may be negative)

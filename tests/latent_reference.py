@@ -69,6 +69,13 @@ class Case:
             x = torch.cat([c.view(-1, LATENT), rope[p, s].double()], 1)
         return x, good
 
+    def codes(self, b, n):
+        """fp64 codes [n, 512] and scales [n, 4] of request b's first n positions (records)."""
+        pos = torch.arange(n)
+        p, s = self.block_table[b][pos // PAGE].long().clamp(0, self.P - 1), pos % PAGE
+        code, scale, _ = planes(self.cache)
+        return code[p, s].view(CODE[self.kind]).double().numpy(), scale[p, s].double().numpy()
+
     def tokens(self):
         """(t, b, pos) of every real token (pos may be negative)."""
         t = 0
@@ -109,6 +116,15 @@ def attend(c, scale, ts=None):
             continue
         q = c.q[t].double().numpy()
         res[t] = soften(scale * (q @ k.T), k[:, :LATENT], scale * (np.abs(q) @ np.abs(k).T), ROW)
+        if c.kind != "bf16":
+            # Records' weights w = a e^z s (s: a scale of the key) may be held in f16 as long as the largest of a row
+            # is 2^7 at least. Below 2^-14 f16's half step is 2^-25, whatever the weight: off by 2^-25 |code| / (a sum e^z)
+            # for each key; and with m the key of the largest, a e^z_m s_m >= 2^7 makes 1 / (a sum e^z) <= 2^-7 p_m s_m.
+            code, sc = c.codes(b, len(keep))
+            code, sc = code[keep], sc[keep]
+            z = scale * (q @ k.T)
+            p = np.exp(z - res[t][1][:, None])
+            res[t][2][...] += 2.0 ** -32 * (p * sc.max(1)).max(1)[:, None] * np.abs(code).sum(0)[None]
     return res
 
 
