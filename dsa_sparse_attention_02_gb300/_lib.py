@@ -529,6 +529,15 @@ def _latent_cache(kv_dtype, kv_cache, geom, index):
 def _tensor(name, t, dtype, shape, index, inner=1):
     """Address of a tensor of this type and shape whose innermost `inner` dimensions lie side by
     side, and its other strides."""
+    # (on the way of a call that fits, nothing is looked at twice: some of these calls take microseconds)
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape:
+        if inner == len(shape):
+            if t.is_contiguous():
+                return (t.data_ptr(),)
+        elif inner == 1 and 1 not in shape:
+            *outer, last = t.stride()
+            if last == 1:
+                return (t.data_ptr(), *outer)
     if t is None:
         raise TypeError(f"{name} is missing")
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
