@@ -233,7 +233,6 @@ struct LatentAttendArgs {
   __nv_bfloat16* out;           // [T, H, 512]
   float* lse;                   // [T, H] or null
   void* scratch;
-  int min_run;                  // shortest run of units
   int* err;
 };
 int latent_attend_rows(const GeomDev& g, int H);   // query rows of an item: the box of the queries' map
@@ -247,7 +246,6 @@ struct LatentExpandedArgs {
   __nv_bfloat16* out;           // [T, H, 128]
   float* lse;                   // [T, H] or null
   void* scratch;
-  int min_run;                  // shortest run of units
   int* err;
 };
 size_t latent_expanded_scratch_bytes(int num_sms);

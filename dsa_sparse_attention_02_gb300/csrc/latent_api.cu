@@ -157,7 +157,6 @@ dsa_status_t dsa_latent_attend(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, int
   A.out = reinterpret_cast<__nv_bfloat16*>(out);
   A.lse = lse;
   A.scratch = reinterpret_cast<uint8_t*>(ws) + kHeaderBytes;
-  A.min_run = 1;
   A.err = reinterpret_cast<int*>(ws);
   LatentMaps m;
   const uint64_t rows = (uint64_t)geom->T * H, pages = (uint64_t)geom->num_pages;
@@ -206,7 +205,6 @@ dsa_status_t dsa_latent_attend_expanded(int32_t B, int32_t T, int32_t S, const i
   A.out = reinterpret_cast<__nv_bfloat16*>(out);
   A.lse = lse;
   A.scratch = reinterpret_cast<uint8_t*>(ws) + kHeaderBytes;
-  A.min_run = 1;
   A.err = reinterpret_cast<int*>(ws);
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const uint64_t h = (uint64_t)H, t = (uint64_t)T, n = (uint64_t)S;

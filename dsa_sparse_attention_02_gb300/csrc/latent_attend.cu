@@ -177,6 +177,16 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     tmem_alloc(smem_u32(&s_tmem), kTmem);
     tmem_relinquish();
   }
+  LatentCursor<N> at(A, parts, blockIdx.x, true);
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_q);
+      tma_prefetch_desc(&map_pair);
+      tma_prefetch_desc(&map_rope);
+    }
+    at.find(gridDim.x);
+    if (at.begin < at.end) at.batch(at.begin);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -185,12 +195,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ units and loads
-    if (lane == 0) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_pair);
-      tma_prefetch_desc(&map_rope);
-    }
-    LatentCursor<N> at(A, parts, blockIdx.x, gridDim.x, true);
     const int count = (int)(at.end - at.begin);
     if (count == 0 && lane == 0) {
       s_unit[0].flags = kStop;

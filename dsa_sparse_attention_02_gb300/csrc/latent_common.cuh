@@ -29,6 +29,14 @@ inline LatentParts latent_parts(void* scratch, int runs, int rows, int width) {
   return s;
 }
 
+// Run c of g starts at unit run_begin of n; unit x lies in run run_owner. (As split_begin and
+// split_owner, but 64-bit divisions, some 200 clocks each, only where the numbers need them.)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {   // of numbers >= 0
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t run_begin(int64_t c, int64_t n, int64_t g) { return quotient(c * n, g); }
+__device__ __forceinline__ int64_t run_owner(int64_t x, int64_t n, int64_t g) { return quotient((x + 1) * g - 1, n); }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -119,6 +127,18 @@ __global__ void __launch_bounds__(32 * kLatentMergeWarps) latent_merge_kernel(co
 
 template <int WIDTH>
 inline cudaError_t latent_merge_launch(const LatentParts& s, int runs, __nv_bfloat16* out, float* lse, cudaStream_t st) {
+  // As much shared memory as the attention kernels ask for: between two kernels that want different
+  // shares of it, an SM has to run empty and set its memory up anew.
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(latent_merge_kernel<WIDTH>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(runs, s.rows / kLatentMergeWarps);
   cfg.blockDim = dim3(32 * kLatentMergeWarps);

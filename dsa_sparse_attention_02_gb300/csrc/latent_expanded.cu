@@ -182,10 +182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    runs = (int)min((int64_t)gridDim.x, max((total + A.min_run - 1) / A.min_run, (int64_t)1));
+    runs = (int)min((int64_t)gridDim.x, max(total, (int64_t)1));
     if ((int)blockIdx.x < runs) {
-      begin = split_begin(blockIdx.x, total, runs);
-      end = split_begin(blockIdx.x + 1, total, runs);
+      begin = run_begin(blockIdx.x, total, runs);
+      end = run_begin(blockIdx.x + 1, total, runs);
       for (int b0 = 0; b0 < A.B; b0 += 32) {
         const int64_t w = b0 + lane < A.B ? A.H * exp_head(exp_req(A, b0 + lane)) : 0;
         int64_t upto = w;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.slot = !cut ? -1 : 2 * (int)blockIdx.x + (max(ib, begin) == begin ? 0 : 1);
           if (last && cut && ib >= begin) {
             LatentCut k{};
-            k.follow = (int)split_owner(ie - 1, total, runs) - (int)blockIdx.x;
+            k.follow = (int)run_owner(ie - 1, total, runs) - (int)blockIdx.x;
             k.slot = x.slot, k.rows = x.rows, k.step = A.H, k.out = (int64_t)x.q0 * A.H + hh;
             parts.cuts[blockIdx.x] = k;
           }

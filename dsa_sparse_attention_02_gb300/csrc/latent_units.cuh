@@ -45,7 +45,7 @@ __device__ __forceinline__ LatentReq latent_req(const LatentAttendArgs& A, int b
 template <int N>
 __device__ __forceinline__ int latent_units(const LatentAttendArgs& A, const LatentReq& r, int i) {
   if (r.none) return 1;
-  const int last = min(r.n - 1, (int)(((int64_t)i * N + N - 1) / A.H));
+  const int last = min((uint32_t)(r.n - 1), ((uint32_t)i * N + N - 1) / (uint32_t)A.H);
   return max(r.start + last, 0) / kPage + 1;
 }
 // Units of tiles 0 .. i - 1: tile j sees page k if its last token reaches position 64 k, which
@@ -69,32 +69,43 @@ struct LatentCursor {
   int64_t begin = 0, end = 0, base = 0, total = 0;
   int runs = 1;
   int b = 0, ti = 0, c = 0;                  // request, tile and page of the next batch's first unit
-  LatentReq r;
+  LatentReq r{};
   LatentUnit x{};                            // the batch: this lane's unit and its page
   int page = -1, cnt = 0, at = 0;
 
-  __device__ __forceinline__ LatentCursor(const LatentAttendArgs& args, const LatentParts& p, int id_, int grid, bool writer_)
-      : A(args), parts(p), id(id_), writer(writer_) {
+  __device__ __forceinline__ LatentCursor(const LatentAttendArgs& args, const LatentParts& p, int id_, bool writer_)
+      : A(args), parts(p), id(id_), writer(writer_) {}
+
+  // Finds the run. (What the requests say is read once where there are 32 at most: each look takes
+  // half a microsecond, before which no load of a page can begin.)
+  __device__ __forceinline__ void find(int grid) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0 && writer) parts.cuts[id].follow = 0;
+    LatentReq front{};                       // of request `lane`
+    int64_t w_front = 0;
     for (int b0 = 0; b0 < A.g.B; b0 += 32) {
       if (b0 + lane < A.g.B) {
         const LatentReq q = latent_req<N>(A, b0 + lane);
-        total += latent_before<N>(A, q, q.tiles);
+        const int64_t w = latent_before<N>(A, q, q.tiles);
+        if (b0 == 0) front = q, w_front = w;
+        total += w;
         if (q.bad && id == 0 && writer) record_error(A.err, kDevBadIndex);
       }
     }
+    if (lane == 0 && writer) parts.cuts[id].follow = 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    runs = (int)min((int64_t)grid, max((total + A.min_run - 1) / A.min_run, (int64_t)1));
+    runs = (int)min((int64_t)grid, max(total, (int64_t)1));
     if (id >= runs || total == 0) return;
-    begin = split_begin(id, total, runs);
-    end = split_begin(id + 1, total, runs);
+    begin = run_begin(id, total, runs);
+    end = run_begin(id + 1, total, runs);
     for (int b0 = 0; b0 < A.g.B; b0 += 32) {
-      int64_t w = 0;
-      if (b0 + lane < A.g.B) {
-        const LatentReq q = latent_req<N>(A, b0 + lane);
-        w = latent_before<N>(A, q, q.tiles);
+      int64_t w = w_front;
+      if (b0 > 0) {
+        w = 0;
+        if (b0 + lane < A.g.B) {
+          front = latent_req<N>(A, b0 + lane);
+          w = latent_before<N>(A, front, front.tiles);
+        }
       }
       int64_t upto = w;
 #pragma unroll
@@ -107,12 +118,14 @@ struct LatentCursor {
         const int l = __ffs(m) - 1;
         b = b0 + l;
         base += __shfl_sync(0xffffffffu, upto - w, l);
+        r.q0 = __shfl_sync(0xffffffffu, front.q0, l), r.n = __shfl_sync(0xffffffffu, front.n, l);
+        r.start = __shfl_sync(0xffffffffu, front.start, l), r.tiles = __shfl_sync(0xffffffffu, front.tiles, l);
+        r.bad = __shfl_sync(0xffffffffu, front.bad, l), r.none = __shfl_sync(0xffffffffu, front.none, l);
         break;
       }
       base += __shfl_sync(0xffffffffu, upto, 31);
     }
     // the last tile that begins at or before unit `begin`
-    r = latent_req<N>(A, b);
     const int64_t o = begin - base;
     int lo = 0, hi = r.tiles - 1;
     while (lo < hi) {
@@ -154,7 +167,7 @@ struct LatentCursor {
       x.rows = min(N, rr.n * A.H - x.row0);
       x.out = (int64_t)rr.q0 * A.H + x.row0;
       x.rel = rr.start - cc * kPage;
-      const int lo = x.row0 / A.H, hi = (x.row0 + x.rows - 1) / A.H;
+      const int lo = (uint32_t)x.row0 / (uint32_t)A.H, hi = (uint32_t)(x.row0 + x.rows - 1) / (uint32_t)A.H;
       page = -1;
       if (!rr.none && x.rel + hi >= 0) {
         page = gqa_page(A.g, bb, cc);
@@ -168,20 +181,21 @@ struct LatentCursor {
       x.slot = !cut ? -1 : 2 * id + (max(ib, begin) == begin ? 0 : 1);
       if (last && cut && ib >= begin && writer) {
         LatentCut k{};
-        k.follow = (int)split_owner(ie - 1, total, runs) - id;
+        k.follow = (int)run_owner(ie - 1, total, runs) - id;
         k.slot = x.slot, k.rows = x.rows, k.step = 1, k.out = x.out;
         parts.cuts[id] = k;
       }
     }
+    at = 0;
+    if (u + cnt == end) return;
     // the cursor behind the batch: its last lane's unit, one further
     const int l = cnt - 1;
     b = __shfl_sync(0xffffffffu, bb, l), ti = __shfl_sync(0xffffffffu, tt, l), c = __shfl_sync(0xffffffffu, cc, l) + 1;
     r = latent_req<N>(A, b);
-    if (u + cnt < end && c == latent_units<N>(A, r, ti)) {
+    if (c == latent_units<N>(A, r, ti)) {
       c = 0;
       turn(b, ti, r);
     }
-    at = 0;
   }
 };
 
