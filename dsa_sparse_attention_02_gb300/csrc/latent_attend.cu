@@ -293,7 +293,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       const uint64_t dr = smem_desc(smem_u32(rope_buf), 0, 1024, kSwizzle128B);
       Ring<S::kRopes> rope(0);
       Ring<S::kSlots> slot(kRecord ? 2 * half : 0);   // records: places 0 (the rotated part's), 1 and 3, or 2 and 4 of a page's five
-      int edges = 0;
       uint32_t seg = 0;
       for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
@@ -331,10 +330,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           __syncwarp();
           rope.step(1);
           if (kRecord) slot.step(1);
-        }
-        if (!kRecord && (flags & kEdge)) {        // (records: the conversion has done it)
-          ok = ok && warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err);
-          ++edges;
         }
 #pragma unroll 1
         for (int i = 0; i < 2 && ok; ++i) {
@@ -504,19 +499,26 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           if (edge) {
             ok = ok && warp_wait(&pair_full[pair], pair_ph, abort, A.err);
             if (!ok) break;
-            uint8_t* dst = pair_buf + pair * kPairBytes;
+            uint4* at = reinterpret_cast<uint4*>(pair_buf + pair * kPairBytes);
             // (a row's eight chunks of an atom by eight threads: the swizzle permutes within the row)
-#pragma unroll 2
-            for (int i = ct; i < 2 * kPage * 8; i += 32 * S::kFixWarps) {
-              const int row = (i >> 3) & (kPage - 1);
-              uint4* p = reinterpret_cast<uint4*>(dst) + i;
-              const uint4 v = *p;
-              const uint32_t o[4] = {v.x, v.y, v.z, v.w};
-              bool bad = false;
+            constexpr int kChunks = kPage * 8, kStep = 32 * S::kFixWarps;
+            for (int i = 8 * (last + 1) + ct; i < kChunks; i += kStep) at[i] = at[kChunks + i] = make_uint4(0, 0, 0, 0);
+            // where all rows see the same keys, the others may do as they like
+            if (flags & kMixed) {
+              for (int i = ct; i < 8 * (last + 1); i += kStep) {
+                const uint4 v[2] = {at[i], at[kChunks + i]};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) bad |= (o[e] & 0x7F80u) == 0x7F80u || (o[e] & 0x7F800000u) == 0x7F800000u;
-              if (bad && row <= last) atomicOr(&s_bad[us][row >> 5], 1u << (row & 31));
-              if (bad || row > last) *p = make_uint4(0, 0, 0, 0);
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t o[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+                  bool bad = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) bad |= (o[e] & 0x7F80u) == 0x7F80u || (o[e] & 0x7F800000u) == 0x7F800000u;
+                  if (bad) {
+                    atomicOr(&s_bad[us][i >> 8], 1u << (i >> 3 & 31));
+                    at[h * kChunks + i] = make_uint4(0, 0, 0, 0);
+                  }
+                }
+              }
             }
           }
           if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
@@ -544,6 +546,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     Ring<S::kPs> ps(0);
     float qf[2], up[2];                           // records: factors of the rows' scores, and of the rotated part's to theirs
     uint32_t seg = 0;
+    int edges = 0;
     bool ok = true;
     for (int n = 0;; ++n) {
       const int us = n % kUnits;
@@ -632,6 +635,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       bool need = false;
       if (active && ok && !(x.flags & kStop)) {
         if (x.flags & kEdge) {
+          // bf16: what rows that do not see them must not meet has left the values (the scores need no
+          // waiting: those of such keys are replaced here). Records: the conversion has done it.
+          if (!kRecord) ok = warp_wait(&e_full[edges % kUnits], (edges / kUnits) & 1, abort, A.err);
           const uint64_t bad = (uint64_t)s_bad[us][0] | (uint64_t)s_bad[us][1] << 32;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -672,6 +678,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           need |= r0 + 8 * i < x.rows && m - kLift > M[i] + kMove;
         }
       }
+      if (x.flags & kEdge) ++edges;
       // The reference moves. (All eight warps come here in every round, those that gave up too;
       // an item's first unit comes here whether or not a row sees a key of it.)
       if (bar_any(1, 32 * kSoftWarps, need || !ok || (x.flags & kFirst))) {

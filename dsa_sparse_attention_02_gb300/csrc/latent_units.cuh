@@ -13,8 +13,8 @@ constexpr int kCodeStage = kPage * 128;      // a pair's codes
 constexpr int kScaleSlots = 4;
 constexpr uint32_t kTmem = 512;
 // Beside first, last and void: some row of the item does not see the whole page; the run's last
-// unit; a run without units (nothing in it to do).
-enum : int { kEdge = 8, kEnd = 16, kStop = 32 };
+// unit; a run without units (nothing in it to do); a key that some rows see and others do not.
+enum : int { kEdge = 8, kEnd = 16, kStop = 32, kMixed = 64 };
 
 struct __align__(16) LatentUnit {
   int flags, rel;       // position of token 0 less the page's first position
@@ -176,7 +176,8 @@ struct LatentCursor {
       x.last = page >= 0 ? min(x.rel + hi, kPage - 1) : -1;
       const bool first = me == ib || me == begin, last = me + 1 == ie || me + 1 == end;
       x.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (page >= 0 ? 0 : kVoid) |
-                (page < 0 || x.rel + lo < kPage - 1 ? kEdge : 0) | (me + 1 == end ? kEnd : 0);
+                (page < 0 || x.rel + lo < kPage - 1 ? kEdge : 0) | (page >= 0 && max(x.rel + lo, -1) < x.last ? kMixed : 0) |
+                (me + 1 == end ? kEnd : 0);
       const bool cut = ib < begin || ie > end;
       x.slot = !cut ? -1 : 2 * id + (max(ib, begin) == begin ? 0 : 1);
       if (last && cut && ib >= begin && writer) {
