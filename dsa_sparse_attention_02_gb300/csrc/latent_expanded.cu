@@ -28,11 +28,19 @@ namespace dsa {
 
 namespace {
 
-constexpr int kKeys = 128, kRows = 256, kTile = 128, kV = 128;
+constexpr int kKeys = 128, kTile = 128, kV = 128;
 constexpr int kAtom = 128 * 128;               // 128 rows x 64 bf16
 constexpr int kKBytes = 3 * kAtom, kVHalf = 2 * 64 * 128, kQTile = 3 * kAtom;
 constexpr int kKStages = 2;
-constexpr int kSmem = 1024 + 2 * kQTile + kKStages * kKBytes + 2 * kVHalf;
+// Tiles of an item, and stages of values beside them. With one tile its units go alternately through
+// the two places in tensor memory, each with the softmax warps, issuer, maximum, sum and O of
+// its own (joined at the item's end): the products of one unit again run during the other's
+// softmax, and a second stage of values has the second tile's place in shared memory.
+template <int TILES>
+struct ExpShape {
+  static constexpr int kRows = TILES * kTile, kVStages = TILES == 1 ? 2 : 1;
+  static constexpr int kSmem = 1024 + TILES * kQTile + kKStages * kKBytes + kVStages * 2 * kVHalf;
+};
 constexpr int kUnits = 4;                      // units described ahead
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kValueWarp = 11, kFixWarp0 = 12;   // 0-3, 4-7: softmax of tile 0, 1
 constexpr int kFixWarps = 4;
@@ -53,6 +61,7 @@ struct ExpReq {
   int tiles;
   bool bad, none;
 };
+template <int kRows>
 __device__ __forceinline__ ExpReq exp_req(const LatentExpandedArgs& A, int b) {
   ExpReq r;
   const int c0 = __ldg(A.cu_q + b), c1 = __ldg(A.cu_q + b + 1), k0 = __ldg(A.cu_k + b), k1 = __ldg(A.cu_k + b + 1);
@@ -66,13 +75,15 @@ __device__ __forceinline__ ExpReq exp_req(const LatentExpandedArgs& A, int b) {
   return r;
 }
 // Units that tile i's last token sees (at least one: empty rows are written too).
+template <int kRows>
 __device__ __forceinline__ int exp_units(const ExpReq& r, int i) {
   if (r.none) return 1;
   return max(r.start + min(r.n - 1, i * kRows + kRows - 1), 0) / kKeys + 1;
 }
+template <int kRows>
 __device__ __forceinline__ int64_t exp_head(const ExpReq& r) {
   int64_t s = 0;
-  for (int i = 0; i < r.tiles; ++i) s += exp_units(r, i);
+  for (int i = 0; i < r.tiles; ++i) s += exp_units<kRows>(r, i);
   return s;
 }
 
@@ -114,20 +125,25 @@ __device__ __forceinline__ void note_min(uint32_t* notes, int col, int key) {
   }
 }
 
+template <int TILES>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_expanded_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                            const __grid_constant__ CUtensorMap map_rope, const __grid_constant__ CUtensorMap map_v,
                            const LatentExpandedArgs A, const LatentParts parts) {
+  constexpr int kRows = ExpShape<TILES>::kRows, kVStages = ExpShape<TILES>::kVStages;
+  constexpr bool kSplit = TILES == 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_buf = smem;
-  uint8_t* k_buf = q_buf + 2 * kQTile;
+  uint8_t* k_buf = q_buf + TILES * kQTile;
   uint8_t* v_buf = k_buf + kKStages * kKBytes;
   __shared__ uint64_t u_full[kUnits], u_loaded[kUnits], u_empty[kUnits], e_full[kUnits];
-  __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2];
+  __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages][2], v_empty[kVStages][2];
   __shared__ uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_done[2], drain[2];
+  __shared__ uint64_t x_full, x_done;            // one tile: both places' results of an item are there, have been read
   __shared__ ExpUnit s_unit[kUnits];
   __shared__ uint32_t s_note[kUnits][kV / 2];
+  __shared__ float2 s_ml[kSplit ? 2 : 1][kSplit ? kTile : 1];
   __shared__ int s_count, s_abort;
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -142,19 +158,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(smem_u32(&k_full[i]), 1);
-      mbar_init(smem_u32(&k_empty[i]), 2);
+      mbar_init(smem_u32(&k_empty[i]), TILES);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&v_full[i]), 1);
-      mbar_init(smem_u32(&v_empty[i]), 2);
+      for (int j = 0; j < kVStages; ++j) {
+        mbar_init(smem_u32(&v_full[j][i]), 1);
+        mbar_init(smem_u32(&v_empty[j][i]), TILES);
+      }
       mbar_init(smem_u32(&q_full[i]), 1);
-      mbar_init(smem_u32(&q_free[i]), 1);
+      mbar_init(smem_u32(&q_free[i]), kSplit ? 2 : 1);
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&p_full[i][0]), 4);
       mbar_init(smem_u32(&p_full[i][1]), 4);
       mbar_init(smem_u32(&o_done[i]), 1);
       mbar_init(smem_u32(&drain[i]), 1);
     }
+    mbar_init(smem_u32(&x_full), 8);
+    mbar_init(smem_u32(&x_done), 8);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -175,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b0 = 0; b0 < A.B; b0 += 32) {
       if (b0 + lane < A.B) {
-        const ExpReq r = exp_req(A, b0 + lane);
-        total += A.H * exp_head(r);
+        const ExpReq r = exp_req<kRows>(A, b0 + lane);
+        total += A.H * exp_head<kRows>(r);
         if (r.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
       }
     }
@@ -187,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       begin = run_begin(blockIdx.x, total, runs);
       end = run_begin(blockIdx.x + 1, total, runs);
       for (int b0 = 0; b0 < A.B; b0 += 32) {
-        const int64_t w = b0 + lane < A.B ? A.H * exp_head(exp_req(A, b0 + lane)) : 0;
+        const int64_t w = b0 + lane < A.B ? A.H * exp_head<kRows>(exp_req<kRows>(A, b0 + lane)) : 0;
         int64_t upto = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -219,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- units, keys and queries
       int b = req, h = 0, ti = 0, c = 0;
-      ExpReq r = exp_req(A, b);
+      ExpReq r = exp_req<kRows>(A, b);
       {
-        const int64_t per = exp_head(r);
+        const int64_t per = exp_head<kRows>(r);
         int64_t o = begin - base;
         h = (int)(o / per);
         o -= h * per;
-        while (o >= exp_units(r, ti)) o -= exp_units(r, ti++);
+        while (o >= exp_units<kRows>(r, ti)) o -= exp_units<kRows>(r, ti++);
         c = (int)o;
       }
       ExpUnit x{};
@@ -235,13 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         cnt = (int)min((int64_t)32, end - u);
         int bb = b, hh = h, tt = ti, cc = c;
         ExpReq rr = r;
-        int units = exp_units(rr, tt);
+        int units = exp_units<kRows>(rr, tt);
         auto turn = [&](int& b_, int& h_, int& t_, ExpReq& r_) {      // the item behind this one
           if (++t_ < r_.tiles) return;
           t_ = 0;
           if (++h_ < A.H) return;
           h_ = 0;
-          do r_ = exp_req(A, ++b_);
+          do r_ = exp_req<kRows>(A, ++b_);
           while (r_.tiles == 0 && b_ + 1 < A.B);
         };
         for (int step = lane; step > 0 && lane < cnt;) {              // forward by `lane` units
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           step -= left;
           cc = 0;
           turn(bb, hh, tt, rr);
-          units = exp_units(rr, tt);
+          units = exp_units<kRows>(rr, tt);
         }
         __syncwarp();
         if (lane < cnt) {
@@ -280,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int l = cnt - 1;
         b = __shfl_sync(0xffffffffu, bb, l), h = __shfl_sync(0xffffffffu, hh, l);
         ti = __shfl_sync(0xffffffffu, tt, l), c = __shfl_sync(0xffffffffu, cc, l) + 1;
-        r = exp_req(A, b);
-        if (u + cnt < end && c == exp_units(r, ti)) {
+        r = exp_req<kRows>(A, b);
+        if (u + cnt < end && c == exp_units<kRows>(r, ti)) {
           c = 0;
           turn(b, h, ti, r);
         }
@@ -316,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (flags & kFirst) {                     // the last segment's scores have left the queries' place
-          for (int i = 0; i < 2 && ok; ++i) {
+          for (int i = 0; i < TILES && ok; ++i) {
             ok = seg == 0 || warp_wait(&q_free[i], (seg - 1) & 1, abort, A.err);
             if (ok && lane == 0) {
               const uint32_t bar = smem_u32(&q_full[i]), dst = smem_u32(q_buf + i * kQTile);
@@ -344,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const int flags = s_unit[us].flags, head = s_unit[us].h, key0 = s_unit[us].key0;
         for (int i = 0; i < 2 && ok; ++i) {
-          ok = warp_wait(&v_empty[i], (n & 1) ^ 1, abort, A.err);
+          ok = warp_wait(&v_empty[n % kVStages][i], ((n / kVStages) & 1) ^ 1, abort, A.err);
           if (ok && lane == 0) {
-            const uint32_t bar = smem_u32(&v_full[i]), dst = smem_u32(v_buf + i * kVHalf);
+            const uint32_t bar = smem_u32(&v_full[n % kVStages][i]), dst = smem_u32(v_buf + (n % kVStages * 2 + i) * kVHalf);
             if (!(flags & kVoid)) {
               mbar_arrive_expect_tx(bar, kVHalf);
               tma_load_3d(dst, &map_v, bar, 0, head, key0 + 64 * (1 - i));
@@ -367,12 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (globaltimer_ns() - t0 < 1000000ull) {}
       }
     } else if (warp < kLoadWarp) {
-      // ---------------------------------------------------------- MMA issue, a warp per tile
+      // ---------------------------------------------------------- MMA issue, a warp per tile (or place)
       constexpr uint32_t idesc_s = make_idesc(kTile, kKeys, kFmtBF16, kFmtBF16, 0, 0);
       constexpr uint32_t idesc_o = make_idesc(kTile, kV, kFmtBF16, kFmtBF16, 0, 1);
       const int i = warp - kMmaWarp;
       const uint32_t col = i * kTileCols;         // all 512 columns are this block's: they start at 0
-      const uint64_t dq = smem_desc(smem_u32(q_buf) + i * kQTile, 0, 1024, kSwizzle128B);
+      const uint64_t dq = smem_desc(smem_u32(q_buf) + (kSplit ? 0 : i * kQTile), 0, 1024, kSwizzle128B);
       const uint64_t dk = smem_desc(smem_u32(k_buf), 0, 1024, kSwizzle128B);
       const uint64_t dv = smem_desc(smem_u32(v_buf), kVHalf / 2, 1024, kSwizzle128B);
       const bool issuer = elect_one();
@@ -381,14 +401,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort = 1;
         record_error(A.err, kDevTimeout);
       }
-      uint32_t seg = 0;
+      uint32_t seg = 0, kept = 0;                 // kept: O holds something of this item
       int edges = 0;
       for (int n = 0; n < count && ok; ++n) {
         const int us = n % kUnits, ks = n % kKStages;
         ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
         if (!ok) break;
         const int flags = s_unit[us].flags;
-        if (flags & kFirst) ok = warp_wait(&q_full[i], seg++ & 1, abort, A.err);
+        const uint32_t par = (kSplit ? n >> 1 : n) & 1;
+        if (flags & kFirst) {
+          ok = warp_wait(&q_full[kSplit ? 0 : i], seg++ & 1, abort, A.err);
+          kept = 0;
+        }
+        if (kSplit && (n & 1) != i) {             // the other's unit
+          if (flags & kEdge) ++edges;
+          if ((flags & kLast) && issuer) mma_commit(smem_u32(&q_free[0]));
+          __syncwarp();
+          continue;
+        }
         ok = ok && warp_wait(&k_full[ks], (n / kKStages) & 1, abort, A.err);
         if (!ok) break;
         tc_fence_after();
@@ -400,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        k != 0);
           mma_commit(smem_u32(&s_full[i]));
           mma_commit(smem_u32(&k_empty[ks]));
-          if (flags & kLast) mma_commit(smem_u32(&q_free[i]));
+          if (flags & kLast) mma_commit(smem_u32(&q_free[kSplit ? 0 : i]));
         }
         __syncwarp();
         if (flags & kEdge) {
@@ -409,20 +439,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll 1
         for (int half = 0; half < 2 && ok; ++half) {
-          ok = warp_wait(&v_full[half], n & 1, abort, A.err) && warp_wait(&p_full[i][half], n & 1, abort, A.err);
+          ok = warp_wait(&v_full[n % kVStages][half], (n / kVStages) & 1, abort, A.err) &&
+               warp_wait(&p_full[i][half], par, abort, A.err);
           if (!ok) break;
           tc_fence_after();
           if (issuer) {
-            const uint64_t vd = desc_add(dv, half * kVHalf);
+            const uint64_t vd = desc_add(dv, (n % kVStages * 2 + half) * kVHalf);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_f16_ts(col + kOCol, col + 64 * (1 - half) + 8 * k, desc_add(vd, k * 2048), idesc_o,
-                         (half | k) != 0 || !(flags & kFirst));
-            mma_commit(smem_u32(&v_empty[half]));
+                         (half | k) != 0 ? 1u : kept);
+            mma_commit(smem_u32(&v_empty[n % kVStages][half]));
             if (half == 1) mma_commit(smem_u32(&o_done[i]));
           }
           __syncwarp();
         }
+        kept = 1;
       }
       // Everything issued has finished before tensor and shared memory are given back.
       __syncwarp();
@@ -458,33 +490,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (x.flags & kEdge) {
           for (int i = 0; i < 2 && ok; ++i) {
-            ok = warp_wait(&v_full[i], n & 1, abort, A.err);
+            ok = warp_wait(&v_full[n % kVStages][i], (n / kVStages) & 1, abort, A.err);
             if (!ok) break;
-            uint4* atom = reinterpret_cast<uint4*>(v_buf + i * kVHalf + (fw >> 1) * (kVHalf / 2));
-            const int ch = 4 * (fw & 1) + (lane & 3);
-#pragma unroll 2
-            for (int row = lane >> 2; row < 64; row += 8) {
-              const int key = 64 * (1 - i) + row;
-              uint4* at = atom + row * 8 + (ch ^ (row & 7));
-              const uint4 v = *at;
-              const uint32_t o[4] = {v.x, v.y, v.z, v.w};
-              uint32_t keep[4];
-              bool bad = false;
+            uint4* atom = reinterpret_cast<uint4*>(v_buf + (n % kVStages * 2 + i) * kVHalf + (fw >> 1) * (kVHalf / 2));
+            const int ch = 4 * (fw & 1) + (lane & 3), key0 = 64 * (1 - i) + (lane >> 2);   // keys key0 + 8 k
+            auto chunk = [&](int k) { return atom + (8 * k + (lane >> 2)) * 8 + (ch ^ (lane >> 2)); };
+            // zero times a value is NaN exactly where the value is not finite
+            uint4 v[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                keep[e] = o[e];
-                if ((o[e] & 0x7F80u) == 0x7F80u) keep[e] &= 0xFFFF0000u;
-                if ((o[e] & 0x7F800000u) == 0x7F800000u) keep[e] &= 0xFFFFu;
-                bad |= keep[e] != o[e];
-              }
-              if (key > x.last) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else if (bad) {
-                *at = make_uint4(keep[0], keep[1], keep[2], keep[3]);
+            for (int k = 0; k < 8; ++k) v[k] = key0 + 8 * k <= x.last ? *chunk(k) : make_uint4(0, 0, 0, 0);
+            __nv_bfloat162 sum = __float2bfloat162_rn(0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t o[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&o[e]), __float2bfloat162_rn(0.f), sum);
+              if (key0 + 8 * k > x.last) *chunk(k) = v[k];
+            }
+            if (__low2float(sum) != 0.f || __high2float(sum) != 0.f) {
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) {
+                if (key0 + 8 * k > x.last) break;
+                const uint4 u = *chunk(k);
+                const uint32_t o[4] = {u.x, u.y, u.z, u.w};
+                uint32_t keep[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  keep[e] = o[e];
+                  if ((o[e] & 0x7F80u) == 0x7F80u) keep[e] &= 0xFFFF0000u;
+                  if ((o[e] & 0x7F800000u) == 0x7F800000u) keep[e] &= 0xFFFFu;
+                }
+                *chunk(k) = make_uint4(keep[0], keep[1], keep[2], keep[3]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                   if ((o[e >> 1] ^ keep[e >> 1]) >> (16 * (e & 1)) & 0xFFFFu)
-                    note_min(s_note[seg % kUnits], 32 * fw + 8 * (lane & 3) + e, key - x.rel);
+                    note_min(s_note[seg % kUnits], 32 * fw + 8 * (lane & 3) + e, key0 + 8 * k - x.rel);
               }
             }
           }
@@ -501,94 +541,155 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax: a thread per row
     const int i = warp >> 2;                       // tile
     const uint32_t tile = tmem + i * kTileCols + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int row = kTile * i + 32 * (warp & 3) + lane;
+    const int row = (kSplit ? 0 : kTile * i) + 32 * (warp & 3) + lane;
     const float f = fmaxf(A.scale_log2, 1.17549435e-38f);   // (a scale of 0 would make masked scores NaN)
     float M = kNone, l = 0.f;
     int seg = -1;
-    bool notes = false;                            // the segment had a unit with notes
+    bool notes = false, have = false;              // the segment had a unit with notes, one of this tile's
     for (int n = 0; n < count; ++n) {
       const int us = n % kUnits;
       if (!warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err)) break;
       const int flags = s_unit[us].flags;
       if (flags & kFirst) {
         ++seg;
-        M = kNone, l = 0.f, notes = false;
+        M = kNone, l = 0.f, notes = have = false;
       }
-      if (!warp_wait(&s_full[i], n & 1, abort, A.err)) break;
-      tc_fence_after();
-      // Keys 0 .. 63 are read for the maximum, then 64 .. 127, whose weights are formed first; then
-      // the others again (all 128 at once would not fit beside the rest in 128 registers).
       const bool edge = (flags & kEdge) != 0;
-      const int lim = !edge ? kKeys : (flags & kVoid) || row >= s_unit[us].rows ? -1 : s_unit[us].rel + row;
       notes |= edge;
-      float s[64];
-      auto read = [&](int key) {
-        tmem_ld64(tile + key, s);
-        tmem_ld_wait();
-        if (edge) {
+      const uint32_t par = (kSplit ? n >> 1 : n) & 1;
+      if (!kSplit || (n & 1) == i) {
+        if (!warp_wait(&s_full[i], par, abort, A.err)) break;
+        tc_fence_after();
+        // Keys 0 .. 63 are read for the maximum, then 64 .. 127, whose weights are formed first; then
+        // the others again (all 128 at once would not fit beside the rest in 128 registers).
+        const int lim = !edge ? kKeys : (flags & kVoid) || row >= s_unit[us].rows ? -1 : s_unit[us].rel + row;
+        float s[64];
+        auto read = [&](int key) {
+          tmem_ld64(tile + key, s);
+          tmem_ld_wait();
+          if (edge) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (key + k > lim) s[k] = -INFINITY;
-        }
-      };
-      auto most = [&]() {
-        float m4[4] = {s[0], s[1], s[2], s[3]};
+            for (int k = 0; k < 64; ++k)
+              if (key + k > lim) s[k] = -INFINITY;
+          }
+        };
+        auto most = [&]() {
+          float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int k = 4; k < 60; k += 8) {
+          for (int k = 4; k < 60; k += 8) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) m4[j] = max3(m4[j], s[k + 2 * j], s[k + 2 * j + 1]);
-        }
+            for (int j = 0; j < 4; ++j) m4[j] = max3(m4[j], s[k + 2 * j], s[k + 2 * j + 1]);
+          }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], s[60 + j]);
-        return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      };
-      read(0);
-      float top = most();
-      read(64);
-      top = fmaxf(top, most()) * f;
-      if (flags & kFirst) {
-        M = fmaxf(top, kNone);
-      } else if (__any_sync(0xffffffffu, top > M + kMove)) {
-        float keep = 1.f;
-        if (top > M + kMove) keep = ex2(M - top), M = top;
-        l *= keep;
+          for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], s[60 + j]);
+          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        };
+        read(0);
+        float top = most();
+        read(64);
+        top = fmaxf(top, most()) * f;
+        if (!have) {
+          M = fmaxf(top, kNone);
+        } else if (__any_sync(0xffffffffu, top > M + kMove)) {
+          float keep = 1.f;
+          if (top > M + kMove) keep = ex2(M - top), M = top;
+          l *= keep;
 #pragma unroll 1
-        for (int k = 0; k < kV; k += 16) {
-          float v[16];
-          tmem_ld16(tile + kOCol + k, v);
+          for (int k = 0; k < kV; k += 16) {
+            float v[16];
+            tmem_ld16(tile + kOCol + k, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] *= keep;
+            tmem_st16(tile + kOCol + k, v);
+          }
+          tmem_st_wait();
+        }
+        float a[4] = {};
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (half) read(0);
+          uint32_t p[32];
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            fma2(s[k], s[k + 1], f, -M);
+            fma2(s[k + 2], s[k + 3], f, -M);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[k + j] = ex2(s[k + j]);
+            add2(a[0], a[1], s[k], s[k + 1]);
+            add2(a[2], a[3], s[k + 2], s[k + 3]);
+            p[k / 2] = pack_bf16(s[k], s[k + 1]);
+            p[k / 2 + 1] = pack_bf16(s[k + 2], s[k + 3]);
+          }
+          tmem_st32(tile + 64 * (1 - half), p);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&p_full[i][half]));
+        }
+        l += (a[0] + a[1]) + (a[2] + a[3]);
+        have = true;
+      }
+      if (kSplit && (flags & kLast)) {
+        // ---- both places' maxima, sums and O are one; a place's warps take 64 of the columns
+        const bool mine = (n & 1) == i;
+        s_ml[kSplit ? i : 0][kSplit ? row : 0] = make_float2(M, have ? l : -1.f);
+        if (have && !warp_wait(&o_done[i], mine ? par : (n - 1) >> 1 & 1, abort, A.err)) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&x_full));
+        if (!warp_wait(&x_full, seg & 1, abort, A.err)) break;
+        tc_fence_after();
+        const ExpUnit x = s_unit[us];
+        const float2 other = s_ml[kSplit ? 1 - i : 0][kSplit ? row : 0];
+        const bool there = other.y != -1.f;       // (the same for all rows)
+        const float Mx = !there ? M : have ? fmaxf(M, other.x) : other.x;
+        const float fa = have ? ex2(M - Mx) : 0.f, fb = there ? ex2(other.x - Mx) : 0.f;
+        const float sum = (have ? l * fa : 0.f) + (there ? other.y * fb : 0.f);
+        const bool valid = row < x.rows, none = sum == 0.f;
+        const float inv = none ? 0.f : x.slot < 0 ? 1.f / sum : 1.f;
+        const int64_t at = (int64_t)(x.q0 + (valid ? row : 0)) * A.H + x.h;
+        const int64_t part = (int64_t)x.slot * kRows + row;
+        const uint32_t far = tmem + (1 - i) * kTileCols + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll 1
+        for (int k = 64 * i; k < 64 * i + 64; k += 16) {
+          float v[16], u[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = u[j] = 0.f;
+          if (have) tmem_ld16(tile + kOCol + k, v);
+          if (__any_sync(0xffffffffu, there)) tmem_ld16(far + kOCol + k, u);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] *= keep;
-          tmem_st16(tile + kOCol + k, v);
-        }
-        tmem_st_wait();
-      }
-      float a[4] = {};
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (half) read(0);
-        uint32_t p[32];
+          for (int j = 0; j < 16; ++j) {
+            v[j] = (v[j] * fa + u[j] * fb) * inv;
+            if (notes && !none && row >= (int)(int16_t)(s_note[seg % kUnits][(k + j) >> 1] >> (16 * (j & 1)))) v[j] = NAN;
+          }
+          if (!valid) {
+          } else if (x.slot < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(A.out + at * kV + k);
 #pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          fma2(s[k], s[k + 1], f, -M);
-          fma2(s[k + 2], s[k + 3], f, -M);
+            for (int j = 0; j < 16; j += 8)
+              dst[j / 8] = none ? make_uint4(0, 0, 0, 0)
+                                : make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]), pack_bf16(v[j + 4], v[j + 5]),
+                                             pack_bf16(v[j + 6], v[j + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(parts.o + part * kV + k);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[k + j] = ex2(s[k + j]);
-          add2(a[0], a[1], s[k], s[k + 1]);
-          add2(a[2], a[3], s[k + 2], s[k + 3]);
-          p[k / 2] = pack_bf16(s[k], s[k + 1]);
-          p[k / 2 + 1] = pack_bf16(s[k + 2], s[k + 3]);
+            for (int j = 0; j < 16; j += 4) dst[j / 4] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          }
+          __syncwarp();
         }
-        tmem_st32(tile + 64 * (1 - half), p);
-        tmem_st_wait();
+        if (valid && i == 0) {
+          if (x.slot >= 0) *reinterpret_cast<float2*>(parts.ml + part * 2) = make_float2(Mx, sum);
+          else if (A.lse) A.lse[at] = none ? -INFINITY : (Mx + log2f(sum)) * 0.6931471805599453f;
+        }
+        // (the next item's products overwrite both)
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[i][half]));
-      }
-      l += (a[0] + a[1]) + (a[2] + a[3]);
-      if (flags & kLast) {
+        if (lane == 0) mbar_arrive(smem_u32(&x_done));
+        if (!warp_wait(&x_done, seg & 1, abort, A.err)) break;
+      } else if (flags & kLast) {
         // ---- the segment's outputs, or its part
-        if (!warp_wait(&o_done[i], n & 1, abort, A.err)) break;
+        if (!warp_wait(&o_done[i], par, abort, A.err)) break;
         tc_fence_after();
         const ExpUnit x = s_unit[us];
         const bool valid = row < x.rows, none = l == 0.f;
@@ -640,17 +741,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-size_t latent_expanded_scratch_bytes(int num_sms) { return latent_parts_bytes(num_sms, kRows, kV); }
+// Tiles of an item: two (products of one while the other's softmax runs), but one where the mean
+// request has no more rows than that. (16 requests of 100 rows in the mean over 1500 keys, 16 heads:
+// FIGURE_ONE us with one tile, FIGURE_TWO with two.)
+static int exp_tiles(int B, int T) { return T <= (int64_t)B * kTile ? 1 : 2; }
+
+template <int TILES>
+static cudaError_t exp_launch(const LatentExpandedArgs& A, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& rope,
+                              const CUtensorMap& v, int num_sms, cudaStream_t st) {
+  using S = ExpShape<TILES>;
+  const LatentParts parts = latent_parts(A.scratch, num_sms, S::kRows, kV);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(latent_expanded_kernel<TILES>, S::kSmem, allowed);
+  if (e != cudaSuccess) return e;
+  latent_expanded_kernel<TILES><<<num_sms, kThreads, S::kSmem, st>>>(q, k, rope, v, A, parts);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : latent_merge_launch<kV>(parts, num_sms, A.out, A.lse, st);
+}
+
+// (of two tiles, which serve any batch)
+size_t latent_expanded_scratch_bytes(int num_sms) { return latent_parts_bytes(num_sms, ExpShape<2>::kRows, kV); }
 
 cudaError_t latent_expanded_launch(const LatentExpandedArgs& A, const CUtensorMap& q, const CUtensorMap& k,
                                    const CUtensorMap& rope, const CUtensorMap& v, int num_sms, cudaStream_t st) {
-  const LatentParts parts = latent_parts(A.scratch, num_sms, kRows, kV);
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(latent_expanded_kernel, kSmem, allowed);
-  if (e != cudaSuccess) return e;
-  latent_expanded_kernel<<<num_sms, kThreads, kSmem, st>>>(q, k, rope, v, A, parts);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : latent_merge_launch<kV>(parts, num_sms, A.out, A.lse, st);
+  return exp_tiles(A.B, A.T) == 1 ? exp_launch<1>(A, q, k, rope, v, num_sms, st) : exp_launch<2>(A, q, k, rope, v, num_sms, st);
 }
 
 }  // namespace dsa

@@ -189,3 +189,28 @@ def test_expanded_refusals_of_the_binding():
             b.attend(**bad)
     with pytest.raises(_lib.DsaError):
         b.attend(ws=_lib.workspace(256, DEV))
+
+
+@pytest.mark.parametrize("lens,new,H", [([1000], [1], 1), ([129, 128, 127], [3, 128, 1], 2), ([2000, 900, 40], [128, 100, 40], 16), ([600], [128], 3)])
+def test_expanded_few_rows(lens, new, H):
+    """At most 128 rows a request in the mean: units of an item alternate between two places; items
+    of one unit, cut items, items longer than the mean."""
+    b = Batch(lens, new, H, 21)
+    n = sum(new)
+    b.check(ts={0, n - 1, n // 2, n // 3})
+    b = Batch([700, 64, 64, 64], [300, 1, 1, 1], H, 22)
+    b.check(ts={0, 127, 128, 255, 256, 299, 300, 302})
+
+
+def test_expanded_few_rows_nan():
+    """A NaN among the first of many units, whose weight is nothing beside later ones, is still seen."""
+    b = Batch([1024, 1024], [2, 2], 2, 23)
+    b.q.zero_()
+    b.q[:, :, 128] = 8.0
+    b.rows[:, 512] = torch.arange(2048) % 1024 / 4
+    b.kv[5, 0, 128 + 9] = math.nan
+    b.upload()
+    out, lse = b.attend(1.0)
+    want = torch.zeros(4, 2, 128, dtype=torch.bool)
+    want[:2, 0, 9] = True
+    assert torch.equal(torch.isnan(out.float()).cpu(), want) and torch.isfinite(lse).all()
