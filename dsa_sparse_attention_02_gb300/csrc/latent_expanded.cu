@@ -39,6 +39,9 @@ constexpr int kKStages = 2;
 template <int TILES>
 struct ExpShape {
   static constexpr int kRows = TILES * kTile, kVStages = TILES == 1 ? 2 : 1;
+  // An item's cost beside its units'. (Ragged prompts of 100 rows in the mean over 1500 keys: 82 us
+  // with 0, 57 with 1, 54 with 2, 52 with 3 and with 4; a chunk of 2048 tokens: 476, 478 and 484 with 1, 2 and 3.)
+  static constexpr int kItemCost = TILES == 1 ? 3 : 2;
   static constexpr int kSmem = 1024 + TILES * kQTile + kKStages * kKBytes + kVStages * 2 * kVHalf;
 };
 constexpr int kUnits = 4;                      // units described ahead
@@ -74,6 +77,7 @@ __device__ __forceinline__ ExpReq exp_req(const LatentExpandedArgs& A, int b) {
   r.tiles = (r.n + kRows - 1) / kRows;
   return r;
 }
+struct ExpStart { ExpReq r; int b, h, ti, c; int64_t item; };   // unit c of tile ti of head h of request b, the item's number
 // Units that tile i's last token sees (at least one: empty rows are written too).
 template <int kRows>
 __device__ __forceinline__ int exp_units(const ExpReq& r, int i) {
@@ -131,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap map_rope, const __grid_constant__ CUtensorMap map_v,
                            const LatentExpandedArgs A, const LatentParts parts) {
   constexpr int kRows = ExpShape<TILES>::kRows, kVStages = ExpShape<TILES>::kVStages;
+  constexpr int kItemCost = ExpShape<TILES>::kItemCost;
   constexpr bool kSplit = TILES == 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -182,9 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&s_tmem), kTmem);
     tmem_relinquish();
   }
-  // The run [begin, end) of all units, the request it starts in and where that begins.
-  int64_t begin = 0, end = 0, base = 0, total = 0;
-  int req = 0, runs = 1;
+  // Runs are equal in cost: an item's units, and kItemCost for it (its queries, and its outputs, which
+  // no product hides). This block's run is the units [begin, end); it starts at `first`.
+  int64_t begin = 0, end = 0, total = 0;
+  int runs = 1;
+  ExpStart first{};
   if (warp == kLoadWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&map_q);
@@ -193,36 +200,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map_v);
       parts.cuts[blockIdx.x].follow = 0;
     }
-    for (int b0 = 0; b0 < A.B; b0 += 32) {
+    // (32 requests at most are read once: each look takes half a microsecond)
+    ExpReq front{};
+    int64_t front_head = 0;
+    auto look = [&](int b0) {
+      front = ExpReq{};
+      front_head = 0;
       if (b0 + lane < A.B) {
-        const ExpReq r = exp_req<kRows>(A, b0 + lane);
-        total += A.H * exp_head<kRows>(r);
-        if (r.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
+        front = exp_req<kRows>(A, b0 + lane);
+        front_head = exp_head<kRows>(front);
       }
+    };
+    auto weight = [&]() { return A.H * (front_head + (int64_t)kItemCost * front.tiles); };
+    for (int b0 = (A.B - 1) / 32 * 32; b0 >= 0; b0 -= 32) {      // (the first ones stay)
+      look(b0);
+      total += weight();
+      if (front.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     runs = (int)min((int64_t)gridDim.x, max(total, (int64_t)1));
-    if ((int)blockIdx.x < runs) {
-      begin = run_begin(blockIdx.x, total, runs);
-      end = run_begin(blockIdx.x + 1, total, runs);
-      for (int b0 = 0; b0 < A.B; b0 += 32) {
-        const int64_t w = b0 + lane < A.B ? A.H * exp_head<kRows>(exp_req<kRows>(A, b0 + lane)) : 0;
-        int64_t upto = w;
+    if ((int)blockIdx.x < runs && total > 0) {
+      const int64_t lo = run_begin(blockIdx.x, total, runs), hi = run_begin(blockIdx.x + 1, total, runs);
+      int64_t cost = 0, units = 0, items = 0;                    // of the requests before b0
+      bool found = false;
+      end = -1;
+      for (int b0 = 0; b0 < A.B && end < 0; b0 += 32) {
+        if (b0 > 0) look(b0);
+        int64_t up[3] = {weight(), A.H * front_head, (int64_t)A.H * front.tiles};
+        const int64_t own[3] = {up[0], up[1], up[2]};
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += v;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, up[i], o);
+            if (lane >= o) up[i] += v;
+          }
         }
-        const unsigned m = __ballot_sync(0xffffffffu, base + upto > begin);
-        if (m) {
-          const int l = __ffs(m) - 1;
-          req = b0 + l;
-          base += __shfl_sync(0xffffffffu, upto - w, l);
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, upto, 31);
+        // the unit at cost `at`, or the first behind it
+        auto locate = [&](int64_t at, int l, ExpStart& k) {
+          ExpReq& r = k.r;
+          r.q0 = __shfl_sync(0xffffffffu, front.q0, l), r.n = __shfl_sync(0xffffffffu, front.n, l);
+          r.k0 = __shfl_sync(0xffffffffu, front.k0, l), r.start = __shfl_sync(0xffffffffu, front.start, l);
+          r.tiles = __shfl_sync(0xffffffffu, front.tiles, l);
+          r.bad = __shfl_sync(0xffffffffu, front.bad, l), r.none = __shfl_sync(0xffffffffu, front.none, l);
+          const int64_t head = __shfl_sync(0xffffffffu, front_head, l), whole = head + (int64_t)kItemCost * r.tiles;
+          int64_t o = at - cost - __shfl_sync(0xffffffffu, up[0] - own[0], l), before = 0;
+          k.b = b0 + l;
+          k.h = (int)quotient(o, whole);
+          o -= k.h * whole;
+          k.ti = 0;
+          for (int n = exp_units<kRows>(r, 0); o >= n + kItemCost; n = exp_units<kRows>(r, ++k.ti)) o -= n + kItemCost, before += n;
+          k.c = max((int)o - kItemCost, 0);
+          k.item = items + __shfl_sync(0xffffffffu, up[2] - own[2], l) + (int64_t)k.h * r.tiles + k.ti;
+          return units + __shfl_sync(0xffffffffu, up[1] - own[1], l) + k.h * head + before + k.c;
+        };
+        const unsigned m_lo = __ballot_sync(0xffffffffu, cost + up[0] > lo), m_hi = __ballot_sync(0xffffffffu, cost + up[0] > hi);
+        if (!found && m_lo) begin = locate(lo, __ffs(m_lo) - 1, first), found = true;
+        ExpStart behind;
+        if (m_hi) end = locate(hi, __ffs(m_hi) - 1, behind);
+        cost += __shfl_sync(0xffffffffu, up[0], 31), units += __shfl_sync(0xffffffffu, up[1], 31);
+        items += __shfl_sync(0xffffffffu, up[2], 31);
       }
+      if (end < 0) end = units;                                  // (the last run)
     }
     if (lane == 0) s_count = (int)(end - begin);
   }
@@ -238,25 +278,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // nothing of this batch for this block
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- units, keys and queries
-      int b = req, h = 0, ti = 0, c = 0;
-      ExpReq r = exp_req<kRows>(A, b);
-      {
-        const int64_t per = exp_head<kRows>(r);
-        int64_t o = begin - base;
-        h = (int)(o / per);
-        o -= h * per;
-        while (o >= exp_units<kRows>(r, ti)) o -= exp_units<kRows>(r, ti++);
-        c = (int)o;
-      }
+      int b = first.b, h = first.h, ti = first.ti, c = first.c;
+      int64_t item = first.item;                  // the item's number among all
+      ExpReq r = first.r;
       ExpUnit x{};
       int cnt = 0, at = 0;
       // up to 32 units at a time, one per lane
       auto batch = [&](int64_t u) {
         cnt = (int)min((int64_t)32, end - u);
         int bb = b, hh = h, tt = ti, cc = c;
+        int64_t it = item;
         ExpReq rr = r;
         int units = exp_units<kRows>(rr, tt);
-        auto turn = [&](int& b_, int& h_, int& t_, ExpReq& r_) {      // the item behind this one
+        auto turn = [&](int& b_, int& h_, int& t_, int64_t& i_, ExpReq& r_) {   // the item behind this one
+          ++i_;
           if (++t_ < r_.tiles) return;
           t_ = 0;
           if (++h_ < A.H) return;
@@ -272,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           step -= left;
           cc = 0;
-          turn(bb, hh, tt, rr);
+          turn(bb, hh, tt, it, rr);
           units = exp_units<kRows>(rr, tt);
         }
         __syncwarp();
@@ -291,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           x.slot = !cut ? -1 : 2 * (int)blockIdx.x + (max(ib, begin) == begin ? 0 : 1);
           if (last && cut && ib >= begin) {
             LatentCut k{};
-            k.follow = (int)run_owner(ie - 1, total, runs) - (int)blockIdx.x;
+            // (the last unit's cost: the units before it, and its item and those before)
+            k.follow = (int)run_owner(ie - 1 + kItemCost * (it + 1), total, runs) - (int)blockIdx.x;
             k.slot = x.slot, k.rows = x.rows, k.step = A.H, k.out = (int64_t)x.q0 * A.H + hh;
             parts.cuts[blockIdx.x] = k;
           }
@@ -299,11 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the cursor behind the batch: its last lane's unit, one further
         const int l = cnt - 1;
         b = __shfl_sync(0xffffffffu, bb, l), h = __shfl_sync(0xffffffffu, hh, l);
-        ti = __shfl_sync(0xffffffffu, tt, l), c = __shfl_sync(0xffffffffu, cc, l) + 1;
+        ti = __shfl_sync(0xffffffffu, tt, l), c = __shfl_sync(0xffffffffu, cc, l) + 1, item = __shfl_sync(0xffffffffu, it, l);
         r = exp_req<kRows>(A, b);
         if (u + cnt < end && c == exp_units<kRows>(r, ti)) {
           c = 0;
-          turn(b, h, ti, r);
+          turn(b, h, ti, item, r);
         }
         at = 0;
       };
@@ -743,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Tiles of an item: two (products of one while the other's softmax runs), but one where the mean
 // request has no more rows than that. (16 requests of 100 rows in the mean over 1500 keys, 16 heads:
-// FIGURE_ONE us with one tile, FIGURE_TWO with two.)
+// 52 us with one tile, 79 with two.)
 static int exp_tiles(int B, int T) { return T <= (int64_t)B * kTile ? 1 : 2; }
 
 template <int TILES>
