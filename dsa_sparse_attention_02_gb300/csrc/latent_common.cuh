@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(32 * kLatentMergeWarps) latent_merge_kernel(co
     float4 v[kBatch][V];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int p = min(p0 + i, k.follow);
+      const int p = p0 + i;
+      if (p > k.follow) break;
       const int64_t at = (p == 0 ? (int64_t)k.slot : 2 * (int64_t)(blockIdx.x + p)) * s.rows + row;
       ml[i] = __ldcg(reinterpret_cast<const float2*>(s.ml + at * 2));
 #pragma unroll
