@@ -11,18 +11,26 @@
 // a page is read once for both products, and one 64-key page is what has to be whole: the rows
 // of N = 64 queries alone take 74 KB, and 128 keys would leave no room for the next ones.
 //
-//   warps 0-3  softmax: S has 16 rows in each lane quarter; a 16 x 256-bit load spreads them
-//              over all lanes, warp w has rows 16 w .. 16 w + 15 (those below N), a thread two of
-//              them with 16 keys each. P^T goes to shared memory as bf16. The reference
-//              maximum moves only when a score passes it by more than 2^8; then, and at an
-//              item's end, all four warps read their quarter of O^T's lanes (latent columns).
-//   warps 4, 5 issue the products, one the scores', one the values': an MMA costs its issuer some
-//              50 clocks, more than it costs the tensor cores at these shapes (32 and 40 to 48)
-//   warp 6     finds the units of this block's run, loads pages by TMA in pairs of 64-column atoms
-//   the rest   records: convert codes * scale to bf16 (as every reader of them does). Both:
-//              in a page that some row of the item does not see whole, zero the keys that no row
-//              sees and those with a NaN or infinity, which rows that do see them get as
-//              a NaN score (a weight of zero would not keep them out of the sum).
+//   warps 0-7   softmax: S has 16 rows in each lane quarter; a 16 x 256-bit load spreads them
+//               over all lanes, warp w has rows 16 (w % 4) on (those below N) and the keys of half
+//               w / 4, a thread two rows with 8 keys each. P^T goes to shared memory by matrix
+//               stores. The reference maximum moves only when a score passes it by more than 2^8;
+//               then, and at an item's end, all eight read O^T (a quarter's lanes, half the columns).
+//   then two issue scores and two (records: one) values: an MMA costs its issuer some 50 clocks,
+//               more than it costs the tensor cores at these shapes (32 and 40 to 48)
+//   one         finds the units of this block's run, loads pages by TMA in pairs of 64-column atoms
+//   the rest    bf16: in a page that some row of the item does not see whole, zero the keys that no
+//               row sees, and where rows see different keys those with a NaN or infinity, which rows
+//               that do see them get as a NaN score (a weight of zero would not keep them out of
+//               the sum). The scores do not wait for that.
+//               records: convert codes to f16, exact; scales are applied in fp32 to each scale's
+//               scores, and to the weights: P^T of each scale's 128 columns is its own. (With code *
+//               scale rounded to bf16 instead, log-sum-exps were off by 0.3%.) The queries' latent part
+//               is brought to f16 by an exact power of two a row.
+// What bounds it: bf16 rows HBM (decode of 16 heads: 376 MB in 72 us), and with 64 rows an item the
+// chain of a page, as two pages are all that fits beside the queries: loads (1900 clocks) -> scores
+// (2000) -> softmax (1200) -> values (1500). Records, 64 rows: the same chain with conversion
+// between, 6,300 clocks a page; issue slots 54%, tensor cores 26% busy.
 // All units are laid end to end and cut into equal runs, one per SM; cut items are merged.
 #include "latent_units.cuh"
 

@@ -495,8 +495,8 @@ size_t dsa_gqa_attend_blocks_workspace_size(const dsa_geom_t* geom, const dsa_gq
 /*
  * Dense latent attention: the layers, contexts and prompts that attend to every cached
  * row instead of a selection, over the same paged latent cache (kv_cache as for
- * dsa_sparse_mla_attend, in all three kv_dtypes; the value of a record is code*scale rounded
- * to bf16). Padding rows, tokens at negative positions, inconsistent requests and bad page
+ * dsa_sparse_mla_attend, in all three kv_dtypes; the value of a record is code*scale, which
+ * here is not rounded but where it leaves in bf16: dsa_latent_gather). Padding rows, tokens at negative positions, inconsistent requests and bad page
  * ids are treated as the grouped-query operators treat them.
  */
 
@@ -559,8 +559,9 @@ size_t dsa_latent_append_workspace_size(const dsa_geom_t* geom);
  *     latent row that a query does not see (NaN, infinities, pages of other requests) does not
  *     reach it; a NaN or infinity that it sees makes its outputs NaN (an infinity that meets
  *     queries of the other sign possibly in its own column only). out overlaps no input.
- *   Weights are rounded to bf16 before they meet the rows; all sums are fp32; out is
- *     rounded once more, to bf16.
+ *   Weights are rounded to bf16 before they meet the rows (records: weight times scale, to f16,
+ *     a row's largest being 2^7 at least); all sums are fp32; out is rounded once more, to bf16.
+ *     Over records the queries' first 512 values are exact down to 2^-31 of a row's largest.
  *   sm_scale >= 0, and sm_scale * log2(e) finite in fp32. T * H < 2^31.
  */
 dsa_status_t dsa_latent_attend(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, int32_t H, const void* q,
