@@ -556,6 +556,35 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     uint32_t seg = 0;
     int edges = 0;
     bool ok = true;
+    // Records: the rotated part's scores and the first scale's, of page n (both by the first issuer, so
+    // the second are behind the first; the scales are there, and as the conversion leaves them).
+    float early[kRecord ? 16 : 1];
+    bool ahead = false;                           // they have been read
+    auto front = [&](int n) {
+      if constexpr (kRecord) {
+        const int s0 = slot.at;
+        slot.step(1);
+        const int s1 = slot.at;
+        ok = ok && warp_wait(&s_full[s1], slot.ph, abort, A.err);
+        slot.step(1);
+        if (!ok) return;
+        float t[2][16], c[8];
+        tc_fence_after();
+        tmem_ld_16x32(quarter + S::kSCol + s0 * S::kSlotCols + 32 * half, t[0]);
+        tmem_ld_16x32(quarter + S::kSCol + s1 * S::kSlotCols + 32 * half, t[1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = scale_buf[((n % kScaleSlots) * kPage + key0 + 8 * (j >> 1) + (j & 1)) * 4];
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&s_empty[s0]));
+          mbar_arrive(smem_u32(&s_empty[s1]));
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) early[j] = fmaf(t[1][j], c[2 * (j >> 2) + (j & 1)], t[0][j] * up[j >> 1 & 1]);
+      }
+    };
     for (int n = 0;; ++n) {
       const int us = n % kUnits;
       ok = ok && warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
@@ -596,45 +625,42 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
         slot.step(1);
       } else {
-        // (the scales are there, and as the conversion leaves them: the first one's scores are behind it)
-        // the rotated part and the first scale's, the next two, the last (two at a time: it is the
-        // waits that take long)
+        if (!ahead) front(n);
+        // the next two scales', the last one's (two at a time: it is the waits that take long)
 #pragma unroll
-        for (int g = -1; g < 4; g += 2) {
-          constexpr int kLast2 = 3;
+        for (int g = 1; g < 4; g += 2) {
           float t[2][16];
           const int s0 = slot.at;
           ok = ok && warp_wait(&s_full[s0], slot.ph, abort, A.err);
           slot.step(1);
           const int s1 = slot.at;
-          if (g < kLast2) {
+          if (g < 3) {
             ok = ok && warp_wait(&s_full[s1], slot.ph, abort, A.err);
             slot.step(1);
           }
           if (ok) {
             tc_fence_after();
             tmem_ld_16x32(quarter + S::kSCol + s0 * S::kSlotCols + 32 * half, t[0]);
-            if (g < kLast2) tmem_ld_16x32(quarter + S::kSCol + s1 * S::kSlotCols + 32 * half, t[1]);
+            if (g < 3) tmem_ld_16x32(quarter + S::kSCol + s1 * S::kSlotCols + 32 * half, t[1]);
             float c[2][8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float* at = scales + 4 * (8 * (j >> 1) + (j & 1));
-              if (g < 0) c[1][j] = at[0];
-              else if (g < kLast2) c[0][j] = at[g], c[1][j] = at[g + 1];
-              else c[0][j] = at[g];
+              c[0][j] = at[g];
+              if (g < 3) c[1][j] = at[g + 1];
             }
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(smem_u32(&s_empty[s0]));
-              if (g < kLast2) mbar_arrive(smem_u32(&s_empty[s1]));
+              if (g < 3) mbar_arrive(smem_u32(&s_empty[s1]));
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const int k = 2 * (j >> 2) + (j & 1);
-              s[j] = g < 0 ? t[0][j] * up[j >> 1 & 1] : fmaf(t[0][j], c[0][k], s[j]);
-              if (g < kLast2) s[j] = fmaf(t[1][j], c[1][k], s[j]);
+              s[j] = fmaf(t[0][j], c[0][k], g == 1 ? early[j] : s[j]);
+              if (g < 3) s[j] = fmaf(t[1][j], c[1][k], s[j]);
               else s[j] *= qf[j >> 1 & 1];        // in powers of two
             }
           }
@@ -754,9 +780,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 4; g += 2) {          // each scale's codes get its weights
           const int p0 = ps.at;
-          ok = ok && warp_wait(&p_empty[p0], ps.ph ^ 1, abort, A.err);
           ps.step(1);
-          const int p1 = ps.at;
+          const int p1 = ps.at;                   // (its last values are behind the other place's)
           ok = ok && warp_wait(&p_empty[p1], ps.ph ^ 1, abort, A.err);
           ps.step(1);
           if (ok) {
@@ -783,6 +808,16 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             if (lane == 0) {
               mbar_arrive(smem_u32(&p_full[p0]));
               mbar_arrive(smem_u32(&p_full[p1]));
+            }
+          }
+          // While these weights' values are on their way: the next page's first scores, whose places
+          // its last ones need. (Not of another item, whose queries these warps have yet to convert.)
+          if (g == 0) {
+            ahead = false;
+            if (!(x.flags & kEnd)) {
+              ok = ok && warp_wait(&u_full[(n + 1) % kUnits], ((n + 1) / kUnits) & 1, abort, A.err);
+              ahead = ok && !(s_unit[(n + 1) % kUnits].flags & kFirst);
+              if (ahead) front(n + 1);
             }
           }
         }
