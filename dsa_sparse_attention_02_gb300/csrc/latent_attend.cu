@@ -39,6 +39,7 @@ namespace dsa {
 namespace {
 
 constexpr int kSoftWarps = 8, kScoreWarp0 = 8, kValueWarp0 = 10;
+constexpr uint32_t kSCol = 256;              // scores' first column in tensor memory
 constexpr float kMove = 8.f;                 // log2 of what a weight may pass the reference by
 
 template <int N, int KV>
@@ -46,13 +47,12 @@ struct LatentShape {
   static constexpr bool kRecord = KV != kKvBf16;
   // Rings as deep as shared memory allows.
   static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 64 ? 6 : 8);
-  static constexpr int kRopes = !kRecord && N == 16 ? 3 : 2;
+  static constexpr int kRopes = !kRecord && N == 16 ? 3 : kRecord && N == 64 ? 1 : 2;
   static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 2 : N == 32 ? 3 : 6;
-  // Scores: a page's of bf16 rows in one place, two pages at a time; of records in one place for
-  // each scale (and the rotated part), in a ring. P: one of a page, or a ring of one for each scale.
-  static constexpr int kSlots = !kRecord ? 2 : N == 64 ? 4 : 6;
-  static constexpr uint32_t kSCol = !kRecord || N == 64 ? 256 : 128, kSlotCols = kRecord ? kPage : 2 * kPage;
-  static constexpr int kPs = !kRecord ? 1 : N == 16 ? 4 : 2;
+  // Scores, from column 256 on. bf16 rows: a page's in one place (two, one of each issuer), two pages at a
+  // time. Records: the rotated part's and three of the scales' in a place each, the last scale's in the
+  // rotated part's. P: one of a page, or three, the last scale's in the first's place.
+  static constexpr int kPs = kRecord ? 3 : 1;
   // (20 and 16 warps: a whole number for each quarter of the SM, whose registers they share)
   static constexpr int kValueWarps = kRecord ? 1 : 2, kFixWarps = kRecord ? 8 : 3;
   static constexpr int kLoadWarp = kValueWarp0 + kValueWarps, kFixWarp0 = kLoadWarp + 1;
@@ -131,7 +131,10 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ uint64_t pair_full[S::kPairs], pair_empty[S::kPairs], rope_full[S::kRopes], rope_empty[S::kRopes];
   __shared__ uint64_t code_full[kRecord ? S::kCodes : 1], code_empty[kRecord ? S::kCodes : 1];
   __shared__ uint64_t scale_full[kRecord ? kScaleSlots : 1];
-  __shared__ uint64_t q_full, q_free, s_full[S::kSlots], s_empty[S::kSlots], p_full[S::kPs], p_empty[S::kPs];
+  __shared__ uint64_t q_full, q_free, s_full[2], s_empty[2], p_full;   // (bf16 rows)
+  // records, each once a page: the rotated part's and the first scale's scores are there, the next two's, the
+  // last's; the first two have been read, the others; three scales' weights are there, the last's; the first's have been used
+  __shared__ uint64_t f_front, f_mid, f_last, e_front, e_rest, p_front, p_last, p_used;
   __shared__ uint64_t q_ready;                            // records: the queries are in f16
   __shared__ uint64_t o_done[2], drain[4];                // o_done: of even and odd units
   __shared__ LatentUnit s_unit[kUnits];
@@ -167,14 +170,19 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     mbar_init(smem_u32(&q_full), 1);
     mbar_init(smem_u32(&q_free), 2);
     mbar_init(smem_u32(&q_ready), kSoftWarps);
-    for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(smem_u32(&s_full[i]), kRecord ? 1 : 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 2);
       mbar_init(smem_u32(&s_empty[i]), N / 8);
     }
-    for (int i = 0; i < S::kPs; ++i) {
-      mbar_init(smem_u32(&p_full[i]), kRecord ? N / 8 : kSoftWarps);
-      mbar_init(smem_u32(&p_empty[i]), 1);
-    }
+    mbar_init(smem_u32(&p_full), kSoftWarps);
+    mbar_init(smem_u32(&f_front), 1);
+    mbar_init(smem_u32(&f_mid), 2);
+    mbar_init(smem_u32(&f_last), 1);
+    mbar_init(smem_u32(&e_front), N / 8);
+    mbar_init(smem_u32(&e_rest), N / 8);
+    mbar_init(smem_u32(&p_front), N / 8);
+    mbar_init(smem_u32(&p_last), N / 8);
+    mbar_init(smem_u32(&p_used), 1);
     mbar_init(smem_u32(&o_done[0]), S::kValueWarps);
     mbar_init(smem_u32(&o_done[1]), S::kValueWarps);
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&drain[i]), 1);
@@ -223,19 +231,23 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&u_full[us]));
       const int pg = __shfl_sync(0xffffffffu, at.page, at.at++);
-      ok = warp_wait(&rope_empty[rope], rope_ph ^ 1, abort, A.err);
-      if (!ok) break;
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&rope_full[rope]);
-        if (pg >= 0) {
-          mbar_arrive_expect_tx(bar, kRopeBytes);
-          if (kRecord) tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, 0, pg);
-          else tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8);
-        } else {
-          mbar_arrive(bar);
+      auto load_rope = [&]() {
+        ok = warp_wait(&rope_empty[rope], rope_ph ^ 1, abort, A.err);
+        if (!ok) return;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&rope_full[rope]);
+          if (pg >= 0) {
+            mbar_arrive_expect_tx(bar, kRopeBytes);
+            if (kRecord) tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, 0, pg);
+            else tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8);
+          } else {
+            mbar_arrive(bar);
+          }
         }
-      }
-      if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
+        if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
+      };
+      if (!kRecord) load_rope();
+      if (!ok) break;
       if (kRecord && lane == 0) {                 // (the slot's last reader has given back its unit)
         const uint32_t bar = smem_u32(&scale_full[n % kScaleSlots]);
         if (pg >= 0) {
@@ -248,7 +260,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         if (kRecord) {
-          ok = warp_wait(&code_empty[code], code_ph ^ 1, abort, A.err);
+          // (the rotated part's one place is free later than the first codes')
+          if (j == 2) load_rope();
+          ok = ok && warp_wait(&code_empty[code], code_ph ^ 1, abort, A.err);
           if (!ok) break;
           if (lane == 0) {
             const uint32_t bar = smem_u32(&code_full[code]);
@@ -300,7 +314,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       const uint64_t dk = smem_desc(smem_u32(pair_buf), 0, 1024, kSwizzle128B);
       const uint64_t dr = smem_desc(smem_u32(rope_buf), 0, 1024, kSwizzle128B);
       Ring<S::kRopes> rope(0);
-      Ring<S::kSlots> slot(kRecord ? 2 * half : 0);   // records: places 0 (the rotated part's), 1 and 3, or 2 and 4 of a page's five
       uint32_t seg = 0;
       for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
@@ -322,8 +335,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           ok = ok && warp_wait(kRecord ? &q_ready : &q_full, seg & 1, abort, A.err);
           ++seg;
         }
-        if (!kRecord || half == 0) ok = ok && warp_wait(&s_empty[slot.at], slot.ph ^ 1, abort, A.err);
-        uint32_t d = S::kSCol + slot.at * S::kSlotCols + (kRecord ? 0 : half * kPage);
+        // the place (records: all but the first scale's, and that too) has been read
+        ok = ok && (kRecord ? warp_wait(&e_rest, (n & 1) ^ 1, abort, A.err) : warp_wait(&s_empty[n & 1], ((n >> 1) & 1) ^ 1, abort, A.err));
+        uint32_t d = kRecord ? kSCol : kSCol + (n & 1) * 2 * kPage + half * kPage;
         if (half == 0) {
           ok = ok && warp_wait(&rope_full[rope.at], rope.ph, abort, A.err);
           if (!ok) break;
@@ -333,18 +347,16 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc_rope, k != 0);
             mma_commit(smem_u32(&rope_empty[rope.at]));
-            if (kRecord) mma_commit(smem_u32(&s_full[slot.at]));
           }
           __syncwarp();
           rope.step(1);
-          if (kRecord) slot.step(1);
         }
 #pragma unroll 1
         for (int i = 0; i < 2 && ok; ++i) {
           const int j = half + 2 * i;
           if (kRecord) {                          // each scale's scores go to a place of their own
-            ok = warp_wait(&s_empty[slot.at], slot.ph ^ 1, abort, A.err);
-            d = S::kSCol + slot.at * S::kSlotCols;
+            d = kSCol + ((j + 1) & 3) * kPage;
+            if (j == 3) ok = warp_wait(&e_front, n & 1, abort, A.err);
           }
           ok = ok && warp_wait(&pair_full[pair.at], pair.ph, abort, A.err);
           if (!ok) break;
@@ -355,13 +367,12 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             for (int k = 0; k < 8; ++k)
               mma_f16_ss(d, desc_add(qd, (k >> 2) * N * 128 + (k & 3) * 32),
                          desc_add(kd, (k >> 2) * (kPage * 128) + (k & 3) * 32), idesc, kRecord || (half && i == 0) ? k != 0 : 1);
-            if (kRecord || i == 1) mma_commit(smem_u32(&s_full[slot.at]));
+            if (kRecord) mma_commit(smem_u32(j == 0 ? &f_front : j == 3 ? &f_last : &f_mid));
+            else if (i == 1) mma_commit(smem_u32(&s_full[n & 1]));
             if (i == 1 && (flags & kLast)) mma_commit(smem_u32(&q_free));
           }
           __syncwarp();
           pair.step(2);
-          if (kRecord) slot.step(i == 0 ? 2 : half ? 3 : 2);   // (to place 3 or 4, then to the next page's first)
-          else if (i == 1) slot.step(1);
         }
       }
     } else {
@@ -370,7 +381,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       const uint64_t dp = smem_desc(smem_u32(p_buf), 0, 1024, kSwizzle128B);
       constexpr int kStep = S::kValueWarps;       // a warp's pairs: half and every kStep-th from there
       Ring<S::kPairs> pair(half);
-      Ring<S::kPs> ps(kRecord ? half : 0);
       for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
         ok = warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
@@ -381,22 +391,21 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll 1
         for (int j = half; j < 4; j += kStep) {
           // (P is behind the scores, and so behind the pairs' arrival)
-          if (kRecord || j == half) ok = warp_wait(&p_full[ps.at], ps.ph, abort, A.err);
+          if (j == half) ok = warp_wait(kRecord ? &p_front : &p_full, n & 1, abort, A.err);
+          if (kRecord && j == 3) ok = warp_wait(&p_last, n & 1, abort, A.err);
           if (!ok) break;
           tc_fence_after();
           if (issuer) {
-            const uint64_t vd = desc_add(dv, pair.at * kPairBytes), pd = desc_add(dp, ps.at * S::kPBytes);
+            const uint64_t vd = desc_add(dv, pair.at * kPairBytes), pd = desc_add(dp, kRecord ? j % 3 * S::kPBytes : 0);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
             mma_commit(smem_u32(&pair_empty[pair.at]));
-            if (kRecord) mma_commit(smem_u32(&p_empty[ps.at]));
+            if (kRecord && j == 0) mma_commit(smem_u32(&p_used));
             if (j + kStep >= 4) mma_commit(smem_u32(&o_done[n & 1]));
           }
           __syncwarp();
           pair.step(kStep);
-          if (kRecord) ps.step(kStep);
-          else if (j + kStep >= 4) ps.step(1);
         }
       }
     }
@@ -550,8 +559,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     const int key0 = 32 * half + 2 * (lane & 3);  // and keys: key0 + 8 j and the next, j < 4
     const float f = fmaxf(A.scale_log2, 1.17549435e-38f);   // (a scale of 0 would make masked scores NaN)
     float M[2] = {kNone, kNone}, l[2] = {0.f, 0.f};
-    Ring<S::kSlots> slot(0);
-    Ring<S::kPs> ps(0);
     float qf[2], up[2];                           // records: factors of the rows' scores, and of the rotated part's to theirs
     uint32_t seg = 0;
     int edges = 0;
@@ -562,32 +569,25 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     bool ahead = false;                           // they have been read
     auto front = [&](int n) {
       if constexpr (kRecord) {
-        const int s0 = slot.at;
-        slot.step(1);
-        const int s1 = slot.at;
-        ok = ok && warp_wait(&s_full[s1], slot.ph, abort, A.err);
-        slot.step(1);
+        ok = ok && warp_wait(&f_front, n & 1, abort, A.err);
         if (!ok) return;
         float t[2][16], c[8];
         tc_fence_after();
-        tmem_ld_16x32(quarter + S::kSCol + s0 * S::kSlotCols + 32 * half, t[0]);
-        tmem_ld_16x32(quarter + S::kSCol + s1 * S::kSlotCols + 32 * half, t[1]);
+        tmem_ld_16x32(quarter + kSCol + 32 * half, t[0]);
+        tmem_ld_16x32(quarter + kSCol + kPage + 32 * half, t[1]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) c[j] = scale_buf[((n % kScaleSlots) * kPage + key0 + 8 * (j >> 1) + (j & 1)) * 4];
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&s_empty[s0]));
-          mbar_arrive(smem_u32(&s_empty[s1]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&e_front));
 #pragma unroll
         for (int j = 0; j < 16; ++j) early[j] = fmaf(t[1][j], c[2 * (j >> 2) + (j & 1)], t[0][j] * up[j >> 1 & 1]);
       }
     };
     for (int n = 0;; ++n) {
       const int us = n % kUnits;
-      ok = ok && warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err);
+      ok = ok && (ahead || warp_wait(&u_full[us], (n / kUnits) & 1, abort, A.err));
       LatentUnit x{};
       if (ok) x = s_unit[us];
       if (x.flags & kFirst) {
@@ -610,60 +610,48 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       // (warps without rows do not look at the scores' barriers, which may be two pages ahead of them)
       if (!active || (x.flags & kStop)) {
       } else if constexpr (!kRecord) {
-        ok = ok && warp_wait(&s_full[slot.at], slot.ph, abort, A.err);
+        ok = ok && warp_wait(&s_full[n & 1], (n >> 1) & 1, abort, A.err);
         if (ok) {
           float t[16];
           tc_fence_after();
-          tmem_ld_16x32(quarter + S::kSCol + slot.at * S::kSlotCols + 32 * half, s);
-          tmem_ld_16x32(quarter + S::kSCol + slot.at * S::kSlotCols + kPage + 32 * half, t);
+          tmem_ld_16x32(quarter + kSCol + (n & 1) * 2 * kPage + 32 * half, s);
+          tmem_ld_16x32(quarter + kSCol + (n & 1) * 2 * kPage + kPage + 32 * half, t);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s_empty[slot.at]));
+          if (lane == 0) mbar_arrive(smem_u32(&s_empty[n & 1]));
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] += t[j];
         }
-        slot.step(1);
       } else {
         if (!ahead) front(n);
-        // the next two scales', the last one's (two at a time: it is the waits that take long)
+        // the other scales', together: it is the waits that take long
+        ok = ok && warp_wait(&f_mid, n & 1, abort, A.err) && warp_wait(&f_last, n & 1, abort, A.err);
+        if (ok) {
+          float t[3][16];
+          tc_fence_after();
 #pragma unroll
-        for (int g = 1; g < 4; g += 2) {
-          float t[2][16];
-          const int s0 = slot.at;
-          ok = ok && warp_wait(&s_full[s0], slot.ph, abort, A.err);
-          slot.step(1);
-          const int s1 = slot.at;
-          if (g < 3) {
-            ok = ok && warp_wait(&s_full[s1], slot.ph, abort, A.err);
-            slot.step(1);
-          }
-          if (ok) {
-            tc_fence_after();
-            tmem_ld_16x32(quarter + S::kSCol + s0 * S::kSlotCols + 32 * half, t[0]);
-            if (g < 3) tmem_ld_16x32(quarter + S::kSCol + s1 * S::kSlotCols + 32 * half, t[1]);
-            float c[2][8];
+          for (int g = 0; g < 3; ++g) tmem_ld_16x32(quarter + kSCol + ((g + 2) & 3) * kPage + 32 * half, t[g]);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&e_rest));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float* at = scales + 4 * (8 * (j >> 1) + (j & 1));
-              c[0][j] = at[g];
-              if (g < 3) c[1][j] = at[g + 1];
-            }
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_u32(&s_empty[s0]));
-              if (g < 3) mbar_arrive(smem_u32(&s_empty[s1]));
-            }
+          for (int j = 0; j < 16; ++j) s[j] = early[j];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int k = 2 * (j >> 2) + (j & 1);
-              s[j] = fmaf(t[0][j], c[0][k], g == 1 ? early[j] : s[j]);
-              if (g < 3) s[j] = fmaf(t[1][j], c[1][k], s[j]);
-              else s[j] *= qf[j >> 1 & 1];        // in powers of two
+          for (int g = 0; g < 3; ++g) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float c = scales[4 * (8 * (k >> 1) + (k & 1)) + g + 1];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int j = 4 * (k >> 1) + 2 * i + (k & 1);
+                s[j] = fmaf(t[g][j], c, s[j]);
+              }
             }
           }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) s[j] *= qf[j >> 1 & 1];    // in powers of two
         }
       }
       bool need = false;
@@ -775,51 +763,50 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full[0]));
+        if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full));
       } else if (active) {
+        // each scale's codes get its weights: of the first three, once the last page's values have left their places
+        auto weights = [&](int g) {
+          float v[16];
 #pragma unroll
-        for (int g = 0; g < 4; g += 2) {          // each scale's codes get its weights
-          const int p0 = ps.at;
-          ps.step(1);
-          const int p1 = ps.at;                   // (its last values are behind the other place's)
-          ok = ok && warp_wait(&p_empty[p1], ps.ph ^ 1, abort, A.err);
-          ps.step(1);
-          if (ok) {
-            float c[2][8];
+          for (int k = 0; k < 8; ++k) {
+            const float c = scales[4 * (8 * (k >> 1) + (k & 1)) + g];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float* at = scales + 4 * (8 * (j >> 1) + (j & 1));
-              c[0][j] = at[g], c[1][j] = at[g + 1];
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float v[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = s[j] * c[h][2 * (j >> 2) + (j & 1)];
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                store_matrices(p_row + (h ? p1 : p0) * S::kPBytes + i * 1024, pack_weights(v[2 * i], v[2 * i + 1]),
-                               pack_weights(v[4 + 2 * i], v[5 + 2 * i]), pack_weights(v[8 + 2 * i], v[9 + 2 * i]),
-                               pack_weights(v[12 + 2 * i], v[13 + 2 * i]));
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_u32(&p_full[p0]));
-              mbar_arrive(smem_u32(&p_full[p1]));
+            for (int i = 0; i < 2; ++i) {
+              const int j = 4 * (k >> 1) + 2 * i + (k & 1);
+              v[j] = s[j] * c;
             }
           }
-          // While these weights' values are on their way: the next page's first scores, whose places
-          // its last ones need. (Not of another item, whose queries these warps have yet to convert.)
-          if (g == 0) {
-            ahead = false;
-            if (!(x.flags & kEnd)) {
-              ok = ok && warp_wait(&u_full[(n + 1) % kUnits], ((n + 1) / kUnits) & 1, abort, A.err);
-              ahead = ok && !(s_unit[(n + 1) % kUnits].flags & kFirst);
-              if (ahead) front(n + 1);
-            }
-          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            store_matrices(p_row + g % 3 * S::kPBytes + i * 1024, pack_weights(v[2 * i], v[2 * i + 1]),
+                           pack_weights(v[4 + 2 * i], v[5 + 2 * i]), pack_weights(v[8 + 2 * i], v[9 + 2 * i]),
+                           pack_weights(v[12 + 2 * i], v[13 + 2 * i]));
+        };
+        auto hand_over = [&](uint64_t* bar) {
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(bar));
+        };
+        if (n > 0) ok = ok && warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
+        if (ok) {
+#pragma unroll
+          for (int g = 0; g < 3; ++g) weights(g);
+          hand_over(&p_front);
+        }
+        // While their values are on the way: the next page's first scores, whose place its last ones
+        // need. (Not of another item, whose queries these warps have yet to convert.)
+        ahead = false;
+        if (!(x.flags & kEnd)) {
+          ok = ok && warp_wait(&u_full[(n + 1) % kUnits], ((n + 1) / kUnits) & 1, abort, A.err);
+          ahead = ok && !(s_unit[(n + 1) % kUnits].flags & kFirst);
+          if (ahead) front(n + 1);
+        }
+        ok = ok && warp_wait(&p_used, n & 1, abort, A.err);
+        if (ok) {
+          weights(3);
+          hand_over(&p_last);
         }
       }
       if (x.flags & kLast) {
