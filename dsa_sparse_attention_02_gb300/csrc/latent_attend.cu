@@ -133,8 +133,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ uint64_t scale_full[kRecord ? kScaleSlots : 1];
   __shared__ uint64_t q_full, q_free, s_full[2], s_empty[2], p_full;   // (bf16 rows)
   // records, each once a page: the rotated part's and the first scale's scores are there, the next two's, the
-  // last's; the first two have been read, the others; three scales' weights are there, the last's; the first's have been used
-  __shared__ uint64_t f_front, f_mid, f_last, e_front, e_rest, p_front, p_last, p_used;
+  // last's; the first two have been read, the others; the first
+  // scale's weights are there, the next two's, the last's; the first's have been used
+  __shared__ uint64_t f_front, f_mid, f_last, e_front, e_rest, p_front, p_mid, p_last, p_used;
   __shared__ uint64_t q_ready;                            // records: the queries are in f16
   __shared__ uint64_t o_done[2], drain[4];                // o_done: of even and odd units
   __shared__ LatentUnit s_unit[kUnits];
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     mbar_init(smem_u32(&e_front), N / 8);
     mbar_init(smem_u32(&e_rest), N / 8);
     mbar_init(smem_u32(&p_front), N / 8);
+    mbar_init(smem_u32(&p_mid), N / 8);
     mbar_init(smem_u32(&p_last), N / 8);
     mbar_init(smem_u32(&p_used), 1);
     mbar_init(smem_u32(&o_done[0]), S::kValueWarps);
@@ -388,24 +390,34 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         flags = s_unit[us].flags;
         if (flags & kStop) break;
         const uint32_t kept = flags & kFirst ? 0u : 1u;
-#pragma unroll 1
-        for (int j = half; j < 4; j += kStep) {
-          // (P is behind the scores, and so behind the pairs' arrival)
-          if (j == half) ok = warp_wait(kRecord ? &p_front : &p_full, n & 1, abort, A.err);
-          if (kRecord && j == 3) ok = warp_wait(&p_last, n & 1, abort, A.err);
-          if (!ok) break;
+        // pairs j, j + kStep, .. below `to` (P is behind the scores, and so behind the pairs' arrival)
+        auto values = [&](int j, int to, uint64_t* bar) {
+          ok = ok && warp_wait(bar, n & 1, abort, A.err);
+          if (!ok) return;
           tc_fence_after();
-          if (issuer) {
-            const uint64_t vd = desc_add(dv, pair.at * kPairBytes), pd = desc_add(dp, kRecord ? j % 3 * S::kPBytes : 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_ss(j * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
-            mma_commit(smem_u32(&pair_empty[pair.at]));
-            if (kRecord && j == 0) mma_commit(smem_u32(&p_used));
-            if (j + kStep >= 4) mma_commit(smem_u32(&o_done[n & 1]));
+          for (int i = 0; i < 2; ++i) {
+            if (j + i * kStep >= to) break;
+            if (issuer) {
+              const int jj = j + i * kStep;
+              const uint64_t vd = desc_add(dv, pair.at * kPairBytes), pd = desc_add(dp, kRecord ? jj % 3 * S::kPBytes : 0);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_f16_ss(jj * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
+              mma_commit(smem_u32(&pair_empty[pair.at]));
+              if (kRecord && jj == 0) mma_commit(smem_u32(&p_used));
+              if (jj + kStep >= 4) mma_commit(smem_u32(&o_done[n & 1]));
+            }
+            pair.step(kStep);
           }
           __syncwarp();
-          pair.step(kStep);
+        };
+        if constexpr (kRecord) {
+          values(0, 1, &p_front);
+          values(1, 3, &p_mid);
+          values(3, 4, &p_last);
+        } else {
+          values(half, 4, &p_full);
         }
       }
     }
@@ -605,7 +617,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           }
         }
       }
-      float s[16];
+      float s[16], lg[8] = {};                    // lg: records, logarithms of the keys' largest scales
       const float* scales = scale_buf + ((n % kScaleSlots) * kPage + key0) * 4;   // of this thread's keys
       // (warps without rows do not look at the scores' barriers, which may be two pages ahead of them)
       if (!active || (x.flags & kStop)) {
@@ -625,31 +637,46 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
       } else {
         if (!ahead) front(n);
-        // the other scales', together: it is the waits that take long
-        ok = ok && warp_wait(&f_mid, n & 1, abort, A.err) && warp_wait(&f_last, n & 1, abort, A.err);
-        if (ok) {
-          float t[3][16];
-          tc_fence_after();
+        // the next two scales', then the last one's, before whose arrival the rest is at hand: the chain of
+        // a page is values -> conversion of its last pairs -> their scores -> from here to the weights
+        auto more = [&](int g, const float (&t)[16], const float (&c)[8]) {
 #pragma unroll
-          for (int g = 0; g < 3; ++g) tmem_ld_16x32(quarter + kSCol + ((g + 2) & 3) * kPage + 32 * half, t[g]);
+          for (int j = 0; j < 16; ++j) s[j] = fmaf(t[j], c[2 * (j >> 2) + (j & 1)], g == 1 ? early[j] : s[j]);
+        };
+        auto scale = [&](int g, float (&c)[8]) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) c[j] = scales[4 * (8 * (j >> 1) + (j & 1)) + g];
+        };
+        float t[16], c[8];
+        ok = ok && warp_wait(&f_mid, n & 1, abort, A.err);
+        if (ok) {
+          float u[16], d[8];
+          tc_fence_after();
+          tmem_ld_16x32(quarter + kSCol + 2 * kPage + 32 * half, t);
+          tmem_ld_16x32(quarter + kSCol + 3 * kPage + 32 * half, u);
+          scale(1, c);
+          scale(2, d);
+          tmem_ld_wait();
+          more(1, t, c);
+          more(2, u, d);
+          scale(3, c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = *reinterpret_cast<const float2*>(&s_lg[us][key0 + 8 * j]);
+            lg[2 * j] = v.x, lg[2 * j + 1] = v.y;
+          }
+          // (the last page's values have left P's places)
+          if (n > 0) ok = warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
+        }
+        ok = ok && warp_wait(&f_last, n & 1, abort, A.err);
+        if (ok) {
+          tc_fence_after();
+          tmem_ld_16x32(quarter + kSCol + 32 * half, t);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&e_rest));
-#pragma unroll
-          for (int j = 0; j < 16; ++j) s[j] = early[j];
-#pragma unroll
-          for (int g = 0; g < 3; ++g) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float c = scales[4 * (8 * (k >> 1) + (k & 1)) + g + 1];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int j = 4 * (k >> 1) + 2 * i + (k & 1);
-                s[j] = fmaf(t[g][j], c, s[j]);
-              }
-            }
-          }
+          more(3, t, c);
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] *= qf[j >> 1 & 1];    // in powers of two
         }
@@ -675,14 +702,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
                 else if (bad >> key & 1) v = NAN;
               }
             }
-          }
-        }
-        float lg[8] = {};
-        if constexpr (kRecord) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 v = *reinterpret_cast<const float2*>(&s_lg[us][key0 + 8 * j]);
-            lg[2 * j] = v.x, lg[2 * j + 1] = v.y;
           }
         }
 #pragma unroll
@@ -765,7 +784,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(smem_u32(&p_full));
       } else if (active) {
-        // each scale's codes get its weights: of the first three, once the last page's values have left their places
+        // each scale's codes get its weights
         auto weights = [&](int g) {
           float v[16];
 #pragma unroll
@@ -789,11 +808,12 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(bar));
         };
-        if (n > 0) ok = ok && warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
         if (ok) {
-#pragma unroll
-          for (int g = 0; g < 3; ++g) weights(g);
+          weights(0);
           hand_over(&p_front);
+          weights(1);
+          weights(2);
+          hand_over(&p_mid);
         }
         // While their values are on the way: the next page's first scores, whose place its last ones
         // need. (Not of another item, whose queries these warps have yet to convert.)
