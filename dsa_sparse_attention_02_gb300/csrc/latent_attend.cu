@@ -132,9 +132,10 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ uint64_t code_full[kRecord ? S::kCodes : 1], code_empty[kRecord ? S::kCodes : 1];
   __shared__ uint64_t scale_full[kRecord ? kScaleSlots : 1];
   __shared__ uint64_t q_full, q_free, s_full[2], s_empty[2], p_full;   // (bf16 rows)
-  // records, each once a page: the rotated part's and the first scale's scores are there, the next two's, the
-  // last's; the first two have been read, the others; the first
-  // scale's weights are there, the next two's, the last's; the first's have been used
+  // records, each once a page: the rotated part's and the first scale's scores are there (and the last
+  // page's first weights used), the next two's, the last's (and the last page's last weights used); the
+  // first two have been read, the others; the first scale's weights are there, the next two's, the
+  // last's; the first's have been used
   __shared__ uint64_t f_front, f_mid, f_last, e_front, e_rest, p_front, p_mid, p_last, p_used;
   __shared__ uint64_t q_ready;                            // records: the queries are in f16
   __shared__ uint64_t o_done[2], drain[4];                // o_done: of even and odd units
@@ -176,9 +177,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       mbar_init(smem_u32(&s_empty[i]), N / 8);
     }
     mbar_init(smem_u32(&p_full), kSoftWarps);
-    mbar_init(smem_u32(&f_front), 1);
+    mbar_init(smem_u32(&f_front), 2);
     mbar_init(smem_u32(&f_mid), 2);
-    mbar_init(smem_u32(&f_last), 1);
+    mbar_init(smem_u32(&f_last), 2);
     mbar_init(smem_u32(&e_front), N / 8);
     mbar_init(smem_u32(&e_rest), N / 8);
     mbar_init(smem_u32(&p_front), N / 8);
@@ -405,14 +406,19 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
               for (int k = 0; k < 4; ++k)
                 mma_f16_ss(jj * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
               mma_commit(smem_u32(&pair_empty[pair.at]));
-              if (kRecord && jj == 0) mma_commit(smem_u32(&p_used));
+              if (kRecord && jj == 0) mma_commit(smem_u32(&p_used)), mma_commit(smem_u32(&f_front));
               if (jj + kStep >= 4) mma_commit(smem_u32(&o_done[n & 1]));
+              if (kRecord && jj == 3) mma_commit(smem_u32(&f_last));
             }
             pair.step(kStep);
           }
           __syncwarp();
         };
         if constexpr (kRecord) {
+          if (n == 0 && lane == 0) {              // (no page before it)
+            mbar_arrive(smem_u32(&f_front));
+            mbar_arrive(smem_u32(&f_last));
+          }
           values(0, 1, &p_front);
           values(1, 3, &p_mid);
           values(3, 4, &p_last);
@@ -665,8 +671,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             const float2 v = *reinterpret_cast<const float2*>(&s_lg[us][key0 + 8 * j]);
             lg[2 * j] = v.x, lg[2 * j + 1] = v.y;
           }
-          // (the last page's values have left P's places)
-          if (n > 0) ok = warp_wait(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, A.err);
         }
         ok = ok && warp_wait(&f_last, n & 1, abort, A.err);
         if (ok) {
@@ -817,13 +821,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
         // While their values are on the way: the next page's first scores, whose place its last ones
         // need. (Not of another item, whose queries these warps have yet to convert.)
-        ahead = false;
-        if (!(x.flags & kEnd)) {
-          ok = ok && warp_wait(&u_full[(n + 1) % kUnits], ((n + 1) / kUnits) & 1, abort, A.err);
-          ahead = ok && !(s_unit[(n + 1) % kUnits].flags & kFirst);
-          if (ahead) front(n + 1);
-        }
-        ok = ok && warp_wait(&p_used, n & 1, abort, A.err);
+        ahead = ok && !(x.flags & kLast);
+        if (ahead) front(n + 1);                  // (which waits for the first weights' use as well)
+        else ok = ok && warp_wait(&p_used, n & 1, abort, A.err);
         if (ok) {
           weights(3);
           hand_over(&p_last);
