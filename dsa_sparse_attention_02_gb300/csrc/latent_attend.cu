@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kSoftWarps = 8, kScoreWarp0 = 8, kValueWarp0 = 10;
 constexpr uint32_t kSCol = 256;              // scores' first column in tensor memory
+constexpr int kAhead = 1;                    // pages
 constexpr float kMove = 8.f;                 // log2 of what a weight may pass the reference by
 
 template <int N, int KV>
@@ -224,6 +225,11 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     bool ok = true;
     for (int n = 0; n < count && ok; ++n) {
       if (at.at == at.cnt) at.batch(at.begin + n);
+      if constexpr (kRecord) {
+        // pages into L2 ahead of their loads, of which too few are under way for HBM's latency
+        const bool mine = at.at == 0 ? lane <= kAhead : lane == at.at + kAhead;
+        if (mine && lane < at.cnt && at.page >= 0) bulk_prefetch_l2(A.kv + (int64_t)at.page * kRecPageBytes, kRecPageBytes);
+      }
       const int us = n % kUnits;
       ok = warp_wait(&u_empty[us], ((n / kUnits) & 1) ^ 1, abort, A.err);
       if (!ok) break;
