@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       mbar_init(smem_u32(&e_full[i]), S::kFixWarps);
     }
     for (int i = 0; i < S::kPairs; ++i) {
-      mbar_init(smem_u32(&pair_full[i]), kRecord ? S::kFixWarps : 1);
+      mbar_init(smem_u32(&pair_full[i]), kRecord ? S::kFixWarps / 2 : 1);
       mbar_init(smem_u32(&pair_empty[i]), 1);
     }
     for (int i = 0; i < S::kRopes; ++i) {
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&scale_full[i]), 1);
       for (int i = 0; i < S::kCodes; ++i) {
         mbar_init(smem_u32(&code_full[i]), 1);
-        mbar_init(smem_u32(&code_empty[i]), S::kFixWarps);
+        mbar_init(smem_u32(&code_empty[i]), S::kFixWarps / 2);
       }
     }
     mbar_init(smem_u32(&q_full), 1);
@@ -452,8 +452,10 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     const int ct = tid - 32 * kFixWarp0;
     if constexpr (kRecord) {
       // ---------------------------------------------------------- conversion
-      int pair = 0, code = 0;
-      uint32_t pair_ph = 0, code_ph = 0;
+      // (half of the warps take every other pair: what a pair waits for is not what the next does)
+      const int group = ct / (16 * S::kFixWarps), gt = ct % (16 * S::kFixWarps);
+      Ring<S::kPairs> pair(group);
+      Ring<S::kCodes> code(group);
       bool ok = true;
       for (int n = 0, flags = 0; ok && !(flags & kEnd); ++n) {
         const int us = n % kUnits;
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         // row sees become 0, and so do those of a key with a NaN or infinity, which is noted.
         ok = warp_wait(&scale_full[n % kScaleSlots], (n / kScaleSlots) & 1, abort, A.err);
         if (!ok) break;
-        if (ct < kPage) {
+        if (ct < kPage) {                         // (of the first group, before its first pair is there)
           float4* at = reinterpret_cast<float4*>(scale_buf) + (n % kScaleSlots) * kPage + ct;
           const float4 c = *at;
           const float top = fmaxf(max3(fabsf(c.x), fabsf(c.y), fabsf(c.z)), fabsf(c.w));
@@ -479,16 +481,16 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           s_lg[us][ct] = lg2(fmaxf(top, 7.8886091e-31f));   // (2^-100: all four may be 0)
         }
         // eight codes a thread and round: half a warp reads a row's 128, and eight threads write a row of an atom
-        constexpr int kRounds = kPage * 16 / (32 * S::kFixWarps), kRows = 2 * S::kFixWarps;
-        const int row = ct >> 4, ch = ct & 15;
+        constexpr int kRounds = kPage * 16 / (16 * S::kFixWarps), kRows = S::kFixWarps;
+        const int row = gt >> 4, ch = gt & 15;
         const int from = row * 128 + ch * 8, to = (ch >> 3) * (kPage * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
         static_assert(kRows % 8 == 0, "rows of a round have the swizzle of the first");
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          ok = warp_wait(&code_full[code], code_ph, abort, A.err) && warp_wait(&pair_empty[pair], pair_ph ^ 1, abort, A.err);
+        for (int j = group; j < 4; j += 2) {
+          ok = warp_wait(&code_full[code.at], code.ph, abort, A.err) && warp_wait(&pair_empty[pair.at], pair.ph ^ 1, abort, A.err);
           if (!ok) break;
-          const uint8_t* src = code_buf + code * kCodeStage + from;
-          uint8_t* dst = pair_buf + pair * kPairBytes + to;
+          const uint8_t* src = code_buf + code.at * kCodeStage + from;
+          uint8_t* dst = pair_buf + pair.at * kPairBytes + to;
           uint2 w[kRounds];
 #pragma unroll
           for (int i = 0; i < kRounds; ++i) w[i] = *reinterpret_cast<const uint2*>(src + i * kRows * 128);
@@ -511,12 +513,12 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_u32(&pair_full[pair]));
-            mbar_arrive(smem_u32(&code_empty[code]));
-            if (j == 3) mbar_arrive(smem_u32(&u_empty[us]));
+            mbar_arrive(smem_u32(&pair_full[pair.at]));
+            mbar_arrive(smem_u32(&code_empty[code.at]));
+            if (j >= 2) mbar_arrive(smem_u32(&u_empty[us]));
           }
-          if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
-          if (++code == S::kCodes) code = 0, code_ph ^= 1u;
+          pair.step(2);
+          code.step(2);
         }
       }
     } else {
