@@ -58,6 +58,9 @@ struct LatentShape {
   static constexpr int kValueWarps = kRecord ? 1 : 2, kFixWarps = kRecord ? 8 : 3;
   static constexpr int kLoadWarp = kValueWarp0 + kValueWarps, kFixWarp0 = kLoadWarp + 1;
   static constexpr int kThreads = 32 * (kFixWarp0 + kFixWarps);
+  // An item's cost beside its units'. (0, 1, 2, 3, 4, 6: decode of 16 heads 71.1, 70.3, 70.6, 70.9, 71.4, 72.6 us; of
+  // 128 heads 149, 149, 147, 147, 145, 143; verification int8, 64 rows, 107, 106, 103, 103, 103, 105)
+  static constexpr int kItemCost = N == 64 ? 4 : N == 32 ? 2 : 1;
   static constexpr int kQBytes = 9 * N * 128, kPBytes = N * 128;   // of one P
   static constexpr int kSmem = 1024 + kQBytes + kPs * kPBytes + kRopes * kRopeBytes + kPairs * kPairBytes + kCodes * kCodeStage +
                                (kRecord ? kScaleSlots * 1024 : 0);
@@ -197,14 +200,14 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     tmem_alloc(smem_u32(&s_tmem), kTmem);
     tmem_relinquish();
   }
-  LatentCursor<N> at(A, parts, blockIdx.x, true);
+  LatentCursor<N, S::kItemCost> at(A, parts);
   if (warp == kLoadWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&map_q);
       tma_prefetch_desc(&map_pair);
       tma_prefetch_desc(&map_rope);
     }
-    at.find(gridDim.x);
+    at.find();
     if (at.begin < at.end) at.batch(at.begin);
   }
   tc_fence_before();
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 16; j += 2) {
                 const float s0 = s_sum[0][row + j] + s_sum[1][row + j], s1 = s_sum[0][row + j + 1] + s_sum[1][row + j + 1];
-                const float a = s0 == 0.f ? 0.f : v[j] / s0, b = s1 == 0.f ? 0.f : v[j + 1] / s1;
+                const float a = s0 == 0.f ? 0.f : v[j] * rcp(s0), b = s1 == 0.f ? 0.f : v[j + 1] * rcp(s1);
                 const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
                 if (row + j + (lane & 1) < x.rows)
                   *reinterpret_cast<uint32_t*>(dst + (int64_t)j * kDimLatent) = lane & 1 ? pack_bf16(other, b) : pack_bf16(a, other);

@@ -59,118 +59,130 @@ __device__ __forceinline__ int64_t latent_before(const LatentAttendArgs& A, cons
   return s;
 }
 
-// Finds the units of run `id` of `grid`; whole warp, which keeps up to 32 units at a time, one a lane.
-template <int N>
+// Finds the units of this block's run; whole warp, which keeps up to 32 units at a time, one a lane.
+// Runs are equal in cost: an item's units, and COST for it (its queries, and its outputs, which no
+// product hides).
+template <int N, int COST>
 struct LatentCursor {
   const LatentAttendArgs& A;
   const LatentParts& parts;
-  const int id;
-  const bool writer;                         // notes the run's cut item
-  int64_t begin = 0, end = 0, base = 0, total = 0;
+  int64_t begin = 0, end = 0, total = 0;     // the run's units; the cost of all
   int runs = 1;
-  int b = 0, ti = 0, c = 0;                  // request, tile and page of the next batch's first unit
-  LatentReq r{};
+  // Of the next batch's first unit: request, tile and page, and the item's number among all.
+  struct Place {
+    LatentReq r;
+    int b, ti, c;
+    int64_t item;
+  } p{};
   LatentUnit x{};                            // the batch: this lane's unit and its page
   int page = -1, cnt = 0, at = 0;
 
-  __device__ __forceinline__ LatentCursor(const LatentAttendArgs& args, const LatentParts& p, int id_, bool writer_)
-      : A(args), parts(p), id(id_), writer(writer_) {}
+  __device__ __forceinline__ LatentCursor(const LatentAttendArgs& args, const LatentParts& parts_) : A(args), parts(parts_) {}
 
   // Finds the run. (What the requests say is read once where there are 32 at most: each look takes
   // half a microsecond, before which no load of a page can begin.)
-  __device__ __forceinline__ void find(int grid) {
+  __device__ __forceinline__ void find() {
     const int lane = threadIdx.x & 31;
-    LatentReq front{};                       // of request `lane`
-    int64_t w_front = 0;
-    for (int b0 = 0; b0 < A.g.B; b0 += 32) {
+    LatentReq front{};                       // of request b0 + lane
+    int64_t units_of = 0;
+    auto look = [&](int b0) {
+      front = LatentReq{};
+      units_of = 0;
       if (b0 + lane < A.g.B) {
-        const LatentReq q = latent_req<N>(A, b0 + lane);
-        const int64_t w = latent_before<N>(A, q, q.tiles);
-        if (b0 == 0) front = q, w_front = w;
-        total += w;
-        if (q.bad && id == 0 && writer) record_error(A.err, kDevBadIndex);
+        front = latent_req<N>(A, b0 + lane);
+        units_of = latent_before<N>(A, front, front.tiles);
       }
+    };
+    for (int b0 = (A.g.B - 1) / 32 * 32; b0 >= 0; b0 -= 32) {      // (the first ones stay)
+      look(b0);
+      total += units_of + (int64_t)COST * front.tiles;
+      if (front.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
     }
-    if (lane == 0 && writer) parts.cuts[id].follow = 0;
+    if (lane == 0) parts.cuts[blockIdx.x].follow = 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    runs = (int)min((int64_t)grid, max(total, (int64_t)1));
-    if (id >= runs || total == 0) return;
-    begin = run_begin(id, total, runs);
-    end = run_begin(id + 1, total, runs);
-    for (int b0 = 0; b0 < A.g.B; b0 += 32) {
-      int64_t w = w_front;
-      if (b0 > 0) {
-        w = 0;
-        if (b0 + lane < A.g.B) {
-          front = latent_req<N>(A, b0 + lane);
-          w = latent_before<N>(A, front, front.tiles);
-        }
-      }
-      int64_t upto = w;
+    runs = (int)min((int64_t)gridDim.x, max(total, (int64_t)1));
+    if ((int)blockIdx.x >= runs || total == 0) return;
+    const int64_t lo = run_begin(blockIdx.x, total, runs), hi = run_begin(blockIdx.x + 1, total, runs);
+    int64_t units = 0, items = 0;                                  // of the requests before b0
+    bool found = false;
+    end = -1;
+    for (int b0 = 0; b0 < A.g.B && end < 0; b0 += 32) {
+      if (b0 > 0) look(b0);
+      int64_t up = units_of;
+      int it = front.tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
+        const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
+        const int i = __shfl_up_sync(0xffffffffu, it, o);
+        if (lane >= o) up += v, it += i;
       }
-      const unsigned m = __ballot_sync(0xffffffffu, base + upto > begin);
-      if (m) {
-        const int l = __ffs(m) - 1;
-        b = b0 + l;
-        base += __shfl_sync(0xffffffffu, upto - w, l);
+      const int64_t cost = units + up + COST * (items + it);       // up to this lane's request, with it
+      // the unit at cost `to`, or the first behind it: its number, and where it is
+      auto locate = [&](int64_t to, int l, Place& k) {
+        LatentReq& r = k.r;
         r.q0 = __shfl_sync(0xffffffffu, front.q0, l), r.n = __shfl_sync(0xffffffffu, front.n, l);
         r.start = __shfl_sync(0xffffffffu, front.start, l), r.tiles = __shfl_sync(0xffffffffu, front.tiles, l);
         r.bad = __shfl_sync(0xffffffffu, front.bad, l), r.none = __shfl_sync(0xffffffffu, front.none, l);
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, upto, 31);
+        const int64_t u0 = units + __shfl_sync(0xffffffffu, up - units_of, l);
+        const int64_t i0 = items + __shfl_sync(0xffffffffu, it - front.tiles, l);
+        const int64_t o = to - u0 - COST * i0;
+        int lo = 0, hi = r.tiles - 1;                              // the last tile that begins at `to` or before it
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (latent_before<N>(A, r, mid) + (int64_t)COST * mid <= o) lo = mid; else hi = mid - 1;
+        }
+        const int64_t before = latent_before<N>(A, r, lo);
+        k.b = b0 + l;
+        k.ti = lo;
+        k.c = (int)max(o - before - (int64_t)COST * (lo + 1), (int64_t)0);
+        k.item = i0 + lo;
+        return u0 + before + k.c;
+      };
+      const unsigned m_lo = __ballot_sync(0xffffffffu, cost > lo), m_hi = __ballot_sync(0xffffffffu, cost > hi);
+      if (!found && m_lo) begin = locate(lo, __ffs(m_lo) - 1, p), found = true;
+      Place behind;
+      if (m_hi) end = locate(hi, __ffs(m_hi) - 1, behind);
+      units += __shfl_sync(0xffffffffu, up, 31), items += __shfl_sync(0xffffffffu, it, 31);
     }
-    // the last tile that begins at or before unit `begin`
-    const int64_t o = begin - base;
-    int lo = 0, hi = r.tiles - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (latent_before<N>(A, r, mid) <= o) lo = mid; else hi = mid - 1;
-    }
-    ti = lo;
-    c = (int)(o - latent_before<N>(A, r, lo));
+    if (end < 0) end = units;                                      // (the last run)
   }
 
-  __device__ __forceinline__ void turn(int& b_, int& t_, LatentReq& r_) const {   // the item behind this one
-    if (++t_ < r_.tiles) return;
-    t_ = 0;
-    do r_ = latent_req<N>(A, ++b_);
-    while (r_.tiles == 0 && b_ + 1 < A.g.B);
+  __device__ __forceinline__ void turn(Place& k) const {   // to the item behind this one
+    ++k.item;
+    if (++k.ti < k.r.tiles) return;
+    k.ti = 0;
+    do k.r = latent_req<N>(A, ++k.b);
+    while (k.r.tiles == 0 && k.b + 1 < A.g.B);
   }
 
   __device__ __forceinline__ void batch(int64_t u) {
     const int lane = threadIdx.x & 31;
     cnt = (int)min((int64_t)32, end - u);
-    int bb = b, tt = ti, cc = c;
-    LatentReq rr = r;
-    int units = latent_units<N>(A, rr, tt);
+    Place k = p;
+    int units = latent_units<N>(A, k.r, k.ti);
     for (int step = lane; step > 0 && lane < cnt;) {            // forward by `lane` units
-      const int left = units - cc;
+      const int left = units - k.c;
       if (step < left) {
-        cc += step;
+        k.c += step;
         break;
       }
       step -= left;
-      cc = 0;
-      turn(bb, tt, rr);
-      units = latent_units<N>(A, rr, tt);
+      k.c = 0;
+      turn(k);
+      units = latent_units<N>(A, k.r, k.ti);
     }
     __syncwarp();
     if (lane < cnt) {
-      const int64_t me = u + lane, ib = me - cc, ie = ib + units;
-      x.row0 = tt * N;
-      x.rows = min(N, rr.n * A.H - x.row0);
-      x.out = (int64_t)rr.q0 * A.H + x.row0;
-      x.rel = rr.start - cc * kPage;
+      const int64_t me = u + lane, ib = me - k.c, ie = ib + units;
+      x.row0 = k.ti * N;
+      x.rows = min(N, k.r.n * A.H - x.row0);
+      x.out = (int64_t)k.r.q0 * A.H + x.row0;
+      x.rel = k.r.start - k.c * kPage;
       const int lo = (uint32_t)x.row0 / (uint32_t)A.H, hi = (uint32_t)(x.row0 + x.rows - 1) / (uint32_t)A.H;
       page = -1;
-      if (!rr.none && x.rel + hi >= 0) {
-        page = gqa_page(A.g, bb, cc);
+      if (!k.r.none && x.rel + hi >= 0) {
+        page = gqa_page(A.g, k.b, k.c);
         if (page < 0) record_error(A.err, kDevBadIndex);
       }
       x.last = page >= 0 ? min(x.rel + hi, kPage - 1) : -1;
@@ -179,23 +191,25 @@ struct LatentCursor {
                 (page < 0 || x.rel + lo < kPage - 1 ? kEdge : 0) | (page >= 0 && max(x.rel + lo, -1) < x.last ? kMixed : 0) |
                 (me + 1 == end ? kEnd : 0);
       const bool cut = ib < begin || ie > end;
-      x.slot = !cut ? -1 : 2 * id + (max(ib, begin) == begin ? 0 : 1);
-      if (last && cut && ib >= begin && writer) {
-        LatentCut k{};
-        k.follow = (int)run_owner(ie - 1, total, runs) - id;
-        k.slot = x.slot, k.rows = x.rows, k.step = 1, k.out = x.out;
-        parts.cuts[id] = k;
+      x.slot = !cut ? -1 : 2 * (int)blockIdx.x + (max(ib, begin) == begin ? 0 : 1);
+      if (last && cut && ib >= begin) {
+        LatentCut w{};
+        // (the last unit's cost: the units before it, and its item and those before)
+        w.follow = (int)run_owner(ie - 1 + COST * (k.item + 1), total, runs) - (int)blockIdx.x;
+        w.slot = x.slot, w.rows = x.rows, w.step = 1, w.out = x.out;
+        parts.cuts[blockIdx.x] = w;
       }
     }
     at = 0;
     if (u + cnt == end) return;
     // the cursor behind the batch: its last lane's unit, one further
     const int l = cnt - 1;
-    b = __shfl_sync(0xffffffffu, bb, l), ti = __shfl_sync(0xffffffffu, tt, l), c = __shfl_sync(0xffffffffu, cc, l) + 1;
-    r = latent_req<N>(A, b);
-    if (c == latent_units<N>(A, r, ti)) {
-      c = 0;
-      turn(b, ti, r);
+    p.b = __shfl_sync(0xffffffffu, k.b, l), p.ti = __shfl_sync(0xffffffffu, k.ti, l);
+    p.c = __shfl_sync(0xffffffffu, k.c, l) + 1, p.item = __shfl_sync(0xffffffffu, k.item, l);
+    p.r = latent_req<N>(A, p.b);
+    if (p.c == latent_units<N>(A, p.r, p.ti)) {
+      p.c = 0;
+      turn(p);
     }
   }
 };
