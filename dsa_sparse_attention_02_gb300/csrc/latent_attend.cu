@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   __shared__ uint64_t o_done[2], drain[4];                // o_done: of even and odd units
   __shared__ LatentUnit s_unit[kUnits];
   __shared__ uint32_t s_bad[kUnits][2];                   // keys with a value that is not finite
-  __shared__ float s_keep[N], s_top[2][N], s_sum[2][N], s_qf[kRecord ? N : 1], s_lg[kRecord ? kUnits : 1][kPage];
+  __shared__ __align__(16) float s_keep[N], s_top[2][N], s_sum[2][N], s_qf[kRecord ? N : 1], s_lg[kRecord ? kUnits : 1][kPage];
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -853,6 +853,11 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           }
         }
         if (!bar_all(1, 32 * kSoftWarps, ok)) break;
+        if (tid < N) {                            // (keep is for the next rescaling: now the sums' reciprocals)
+          const float sum = s_sum[0][tid] + s_sum[1][tid];
+          s_keep[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        }
+        if (!bar_all(1, 32 * kSoftWarps, ok)) break;
         // (two barriers, for a warp may come here before unit n - 1's values are done or after unit n's)
         ok = warp_wait(&o_done[n & 1], (n >> 1) & 1, abort, A.err);
         if (ok) {
@@ -884,8 +889,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
               __nv_bfloat16* dst = A.out + (x.out + row + (lane & 1)) * kDimLatent + (dim & ~1);
 #pragma unroll
               for (int j = 0; j < 16; j += 2) {
-                const float s0 = s_sum[0][row + j] + s_sum[1][row + j], s1 = s_sum[0][row + j + 1] + s_sum[1][row + j + 1];
-                const float a = s0 == 0.f ? 0.f : v[j] * rcp(s0), b = s1 == 0.f ? 0.f : v[j + 1] * rcp(s1);
+                // (a row that saw nothing has zeros in O as well: all its weights were 0)
+                const float a = v[j] * s_keep[row + j], b = v[j + 1] * s_keep[row + j + 1];
                 const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
                 if (row + j + (lane & 1) < x.rows)
                   *reinterpret_cast<uint32_t*>(dst + (int64_t)j * kDimLatent) = lane & 1 ? pack_bf16(other, b) : pack_bf16(a, other);
