@@ -27,11 +27,14 @@
 //               scores, and to the weights: P^T of each scale's 128 columns is its own. (With code *
 //               scale rounded to bf16 instead, log-sum-exps were off by 0.3%.) The queries' latent part
 //               is brought to f16 by an exact power of two a row.
-// What bounds it: bf16 rows HBM (decode of 16 heads: 376 MB in 72 us), and with 64 rows an item the
-// chain of a page, as two pages are all that fits beside the queries: loads (1900 clocks) -> scores
-// (2000) -> softmax (1200) -> values (1500). Records, 64 rows: the same chain with conversion
-// between, 6,300 clocks a page; issue slots 54%, tensor cores 26% busy.
-// All units are laid end to end and cut into equal runs, one per SM; cut items are merged.
+// What bounds it. bf16 rows, 16 heads: HBM (376 MB in 71 us, of which 60 at 6.0 TB/s). 64 rows an item:
+// the chain of a page, as two pages are all that fits beside the queries: loads (1900 clocks) ->
+// scores (2000) -> softmax (1200) -> values (1500), 3,000 clocks a page (128 heads: 145 us, pages read
+// twice, 5.0 TB/s). Records, 64 rows: values -> conversion of the next page's last two pairs ->
+// their scores -> softmax -> weights, and the softmax warps' own steps (each wait 200 clocks), which
+// are as long: 4,700 clocks a page (8 contexts of 131072 in e4m3: 269 us, 2.6 TB/s). Issue slots 54%,
+// tensor cores 26% busy (when it took 370 us).
+// All units are laid end to end and cut into runs of equal cost, one per SM; cut items are merged.
 #include "latent_units.cuh"
 
 namespace dsa {

@@ -1,7 +1,8 @@
 // Rows of the paged latent cache, in and out (the definitions are at dsa_latent_append and
 // dsa_latent_gather in include/dsa.h).
 //
-// Append: HBM bounds it where a chunk's queries are many, lookups and launch where they are few.
+// Append: HBM bounds it where a chunk's queries are many, lookups and launch where they are few (2048
+// tokens, 64 heads, e4m3 records and bf16 rows: 40 MB in 10.2 us, 3.9 TB/s; a token of two requests 2.9).
 // A token's work is cut into warps: one norms, rotates and stores the row, the others rotate
 // kWarpHeads query heads each (two rounds of eight heads by four threads, whose loads are all
 // issued before the lookups that give the position). Angles are counted in turns, as fractions
@@ -12,7 +13,7 @@
 // reciprocal root is corrected from that pair, so that stored codes do not depend on the
 // order of the sum: it is the exact sum's but where that lies at a rounding's border.
 //
-// Gather: HBM bounds it. A warp takes kGatherRows rows, lane i the lookups of row i, with all
+// Gather: HBM bounds it (143 MB of e4m3 records and rows in 24.7 us, 5.8 TB/s). A warp takes kGatherRows rows, lane i the lookups of row i, with all
 // rows' loads in flight together.
 #include "latent_common.cuh"
 
