@@ -29,8 +29,8 @@
 //               is brought to f16 by an exact power of two a row.
 // What bounds it. bf16 rows, 16 heads: HBM (376 MB in 71 us, of which 60 at 6.0 TB/s). 64 rows an item:
 // the chain of a page, as two pages are all that fits beside the queries: loads (1900 clocks) ->
-// scores (2000) -> softmax (1200) -> values (1500), 3,000 clocks a page (128 heads: 145 us, pages read
-// twice, 5.0 TB/s). Records, 64 rows: values -> conversion of the next page's last two pairs ->
+// scores (2000) -> softmax (1200) -> values (1500), 3,000 clocks a page, 2,700 in clusters (128 heads: 130 us, pages read
+// once for two items by a cluster's two CTAs, 3.0 TB/s). Records, 64 rows: values -> conversion of the next page's last two pairs ->
 // their scores -> softmax -> weights, and the softmax warps' own steps (each wait 200 clocks), which
 // are as long: 4,700 clocks a page (8 contexts of 131072 in e4m3: 269 us, 2.6 TB/s). Issue slots 54%,
 // tensor cores 26% busy (when it took 370 us).
@@ -116,7 +116,9 @@ struct Ring {
   }
 };
 
-template <int N, int KV>
+// CL: CTAs of a cluster, which have neighbouring items of N rows each over the same pages, each loading
+// half of every page for both.
+template <int N, int KV, int CL>
 __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     latent_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_pair,
                          const __grid_constant__ CUtensorMap map_rope, const LatentAttendArgs A, const LatentParts parts) {
@@ -124,6 +126,10 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   constexpr bool kRecord = S::kRecord;
   constexpr int kLoadWarp = S::kLoadWarp, kFixWarp0 = S::kFixWarp0;
   constexpr uint32_t kFmt = kRecord ? kFmtF16 : kFmtBF16;   // of latents, and of weights
+  static_assert(CL == 1 || !kRecord, "records have no cluster form");
+  constexpr int R = CL * N;                     // rows of an item as the units and the parts see it
+  constexpr uint16_t kAll = (1 << CL) - 1;
+  const int rank = CL == 1 ? 0 : (int)cluster_ctarank();
   // Weights in f16 use its range upwards as well: 2^7 at the reference, and so below 2^16.
   constexpr float kLift = kRecord ? 7.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
@@ -163,11 +169,11 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     }
     for (int i = 0; i < S::kPairs; ++i) {
       mbar_init(smem_u32(&pair_full[i]), kRecord ? S::kFixWarps / 2 : 1);
-      mbar_init(smem_u32(&pair_empty[i]), 1);
+      mbar_init(smem_u32(&pair_empty[i]), CL);
     }
     for (int i = 0; i < S::kRopes; ++i) {
       mbar_init(smem_u32(&rope_full[i]), 1);
-      mbar_init(smem_u32(&rope_empty[i]), 1);
+      mbar_init(smem_u32(&rope_empty[i]), CL);
     }
     if (kRecord) {
       for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&scale_full[i]), 1);
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     tmem_alloc(smem_u32(&s_tmem), kTmem);
     tmem_relinquish();
   }
-  LatentCursor<N, S::kItemCost> at(A, parts);
+  LatentCursor<R, S::kItemCost> at(A, parts, blockIdx.x / CL, gridDim.x / CL, rank == 0);
   if (warp == kLoadWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&map_q);
@@ -215,6 +221,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (CL > 1) cluster_sync();                   // (the other's barriers are set up)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort = &s_abort;
@@ -236,13 +243,15 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         // (records: 304 us without, 284, 286, 288 and 305 with 1, 2, 3 and 6; bf16 rows gain 1%)
         constexpr uint32_t kPageBytes = kRecord ? kRecPageBytes : kPage * kDimQK * 2;
         const bool mine = at.at == 0 ? lane <= kAhead : lane == at.at + kAhead;
-        if (mine && lane < at.cnt && at.page >= 0) bulk_prefetch_l2(A.kv + (int64_t)at.page * kPageBytes, kPageBytes);
+        if (mine && lane < at.cnt && at.page >= 0 && rank == 0) bulk_prefetch_l2(A.kv + (int64_t)at.page * kPageBytes, kPageBytes);
       }
       const int us = n % kUnits;
       ok = warp_wait(&u_empty[us], ((n / kUnits) & 1) ^ 1, abort, A.err);
       if (!ok) break;
       if (lane == at.at) {
-        s_unit[us] = at.x;
+        LatentUnit x = at.x;
+        if (CL > 1) x.row0 += N * rank, x.out += N * rank, x.rows = min(max(x.rows - N * rank, 0), N);
+        s_unit[us] = x;
         s_bad[us][0] = s_bad[us][1] = 0;
       }
       __syncwarp();
@@ -256,7 +265,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           if (pg >= 0) {
             mbar_arrive_expect_tx(bar, kRopeBytes);
             if (kRecord) tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, 0, pg);
-            else tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8);
+            else if (CL == 1) tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8);
+            else if ((n & 1) == rank) tma_load_3d_multicast(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8, kAll);
           } else {
             mbar_arrive(bar);
           }
@@ -298,7 +308,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             const uint32_t bar = smem_u32(&pair_full[pair]);
             if (pg >= 0) {
               mbar_arrive_expect_tx(bar, kPairBytes);
-              tma_load_3d(smem_u32(pair_buf + pair * kPairBytes), &map_pair, bar, 0, pg * kPage, 2 * j);
+              const uint32_t dst = smem_u32(pair_buf + pair * kPairBytes);
+              if (CL == 1) tma_load_3d(dst, &map_pair, bar, 0, pg * kPage, 2 * j);
+              else if ((j & 1) == rank) tma_load_3d_multicast(dst, &map_pair, bar, 0, pg * kPage, 2 * j, kAll);
             } else {
               mbar_arrive(bar);
             }
@@ -363,7 +375,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             const uint64_t kd = desc_add(dr, rope.at * kRopeBytes), qd = desc_add(dq, 8 * N * 128);
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc_rope, k != 0);
-            mma_commit(smem_u32(&rope_empty[rope.at]));
+            if (CL == 1) mma_commit(smem_u32(&rope_empty[rope.at]));
+            else mma_commit_multicast(smem_u32(&rope_empty[rope.at]), kAll);
           }
           __syncwarp();
           rope.step(1);
@@ -419,7 +432,8 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_f16_ss(jj * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
-              mma_commit(smem_u32(&pair_empty[pair.at]));
+              if (CL == 1) mma_commit(smem_u32(&pair_empty[pair.at]));
+              else mma_commit_multicast(smem_u32(&pair_empty[pair.at]), kAll);
               if (kRecord && jj == 0) mma_commit(smem_u32(&p_used)), mma_commit(smem_u32(&f_front));
               if (jj + kStep >= 4) mma_commit(smem_u32(&o_done[n & 1]));
               if (kRecord && jj == 3) mma_commit(smem_u32(&f_last));
@@ -872,7 +886,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
               const int row = r0 + 8 * i;
               const float sum = s_sum[0][row] + s_sum[1][row];
               if (row >= x.rows) continue;
-              if (x.slot >= 0) *reinterpret_cast<float2*>(parts.ml + ((int64_t)x.slot * N + row) * 2) = make_float2(M[i], sum);
+              if (x.slot >= 0) *reinterpret_cast<float2*>(parts.ml + ((int64_t)x.slot * R + N * rank + row) * 2) = make_float2(M[i], sum);
               else if (A.lse) A.lse[x.out + row] = sum == 0.f ? -INFINITY : (M[i] + log2f(sum)) * 0.6931471805599453f;
             }
           }
@@ -883,7 +897,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             tmem_ld_wait();
             const int dim = k / N * 128 + t, row = k % N;
             if (x.slot >= 0) {
-              float* dst = parts.o + ((int64_t)x.slot * N + row) * kDimLatent + dim;
+              float* dst = parts.o + ((int64_t)x.slot * R + N * rank + row) * kDimLatent + dim;
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 if (row + j < x.rows) dst[(int64_t)j * kDimLatent] = v[j];
@@ -911,6 +925,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (CL > 1) cluster_sync();                   // (nothing arrives here any more)
   if (warp == kScoreWarp0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmem);
@@ -923,24 +938,46 @@ int latent_rows(const GeomDev& g, int H) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-template <int N, int KV>
+// Whether two items of a request go to the two CTAs of a cluster: where it has just two in the mean. (64 requests
+// of 128 rows over 5000 keys 130 us, without 144; 32 over 3000 54 and 56. More items find their pages in L2, and
+// an odd one leaves half of a cluster idle: 256 rows 34.8 and 33.9, 192 rows 202 and 167, 4800 rows 97 and 94.)
+bool latent_pairs(const GeomDev& g, int H) {
+  const int64_t rows = ((int64_t)g.T + g.B - 1) / g.B * H;
+  return rows > 64 && rows <= 128;
+}
+
+template <int N, int KV, int CL>
 cudaError_t launch(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st) {
   using S = LatentShape<N, KV>;
-  const LatentParts parts = latent_parts(A.scratch, num_sms, N, kDimLatent);
-  auto kern = latent_attend_kernel<N, KV>;
+  const int runs = num_sms / CL;
+  const LatentParts parts = latent_parts(A.scratch, runs, CL * N, kDimLatent);
+  auto kern = latent_attend_kernel<N, KV, CL>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(kern, S::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  kern<<<num_sms, S::kThreads, S::kSmem, st>>>(m.q, m.pair, m.rope, A, parts);
-  e = cudaGetLastError();
-  return e != cudaSuccess ? e : latent_merge_launch<kDimLatent>(parts, num_sms, A.out, A.lse, st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(runs * CL);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, m.q, m.pair, m.rope, A, parts);
+  return e != cudaSuccess ? e : latent_merge_launch<kDimLatent>(parts, runs, A.out, A.lse, st);
 }
 template <int KV>
 cudaError_t launch_rows(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st) {
   switch (latent_rows(A.g, A.H)) {
-    case 16: return launch<16, KV>(A, m, num_sms, st);
-    case 32: return launch<32, KV>(A, m, num_sms, st);
-    default: return launch<64, KV>(A, m, num_sms, st);
+    case 16: return launch<16, KV, 1>(A, m, num_sms, st);
+    case 32: return launch<32, KV, 1>(A, m, num_sms, st);
+    default:
+      if constexpr (KV == kKvBf16) {
+        if (latent_pairs(A.g, A.H) && num_sms > 1) return launch<64, KV, 2>(A, m, num_sms, st);
+      }
+      return launch<64, KV, 1>(A, m, num_sms, st);
   }
 }
 

@@ -59,13 +59,15 @@ __device__ __forceinline__ int64_t latent_before(const LatentAttendArgs& A, cons
   return s;
 }
 
-// Finds the units of this block's run; whole warp, which keeps up to 32 units at a time, one a lane.
+// Finds the units of run `id` of `grid` (a block's, or a cluster's); whole warp, which keeps up to 32 units at a time, one a lane.
 // Runs are equal in cost: an item's units, and COST for it (its queries, and its outputs, which no
 // product hides).
 template <int N, int COST>
 struct LatentCursor {
   const LatentAttendArgs& A;
   const LatentParts& parts;
+  const int id, grid;
+  const bool writer;                         // reports, and notes the run's cut item
   int64_t begin = 0, end = 0, total = 0;     // the run's units; the cost of all
   int runs = 1;
   // Of the next batch's first unit: request, tile and page, and the item's number among all.
@@ -77,7 +79,8 @@ struct LatentCursor {
   LatentUnit x{};                            // the batch: this lane's unit and its page
   int page = -1, cnt = 0, at = 0;
 
-  __device__ __forceinline__ LatentCursor(const LatentAttendArgs& args, const LatentParts& parts_) : A(args), parts(parts_) {}
+  __device__ __forceinline__ LatentCursor(const LatentAttendArgs& args, const LatentParts& parts_, int id_, int grid_, bool writer_)
+      : A(args), parts(parts_), id(id_), grid(grid_), writer(writer_) {}
 
   // Finds the run. (What the requests say is read once where there are 32 at most: each look takes
   // half a microsecond, before which no load of a page can begin.)
@@ -96,14 +99,14 @@ struct LatentCursor {
     for (int b0 = (A.g.B - 1) / 32 * 32; b0 >= 0; b0 -= 32) {      // (the first ones stay)
       look(b0);
       total += units_of + (int64_t)COST * front.tiles;
-      if (front.bad && blockIdx.x == 0) record_error(A.err, kDevBadIndex);
+      if (front.bad && id == 0 && writer) record_error(A.err, kDevBadIndex);
     }
-    if (lane == 0) parts.cuts[blockIdx.x].follow = 0;
+    if (lane == 0 && writer) parts.cuts[id].follow = 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    runs = (int)min((int64_t)gridDim.x, max(total, (int64_t)1));
-    if ((int)blockIdx.x >= runs || total == 0) return;
-    const int64_t lo = run_begin(blockIdx.x, total, runs), hi = run_begin(blockIdx.x + 1, total, runs);
+    runs = (int)min((int64_t)grid, max(total, (int64_t)1));
+    if (id >= runs || total == 0) return;
+    const int64_t lo = run_begin(id, total, runs), hi = run_begin(id + 1, total, runs);
     int64_t units = 0, items = 0;                                  // of the requests before b0
     bool found = false;
     end = -1;
@@ -191,13 +194,13 @@ struct LatentCursor {
                 (page < 0 || x.rel + lo < kPage - 1 ? kEdge : 0) | (page >= 0 && max(x.rel + lo, -1) < x.last ? kMixed : 0) |
                 (me + 1 == end ? kEnd : 0);
       const bool cut = ib < begin || ie > end;
-      x.slot = !cut ? -1 : 2 * (int)blockIdx.x + (max(ib, begin) == begin ? 0 : 1);
-      if (last && cut && ib >= begin) {
+      x.slot = !cut ? -1 : 2 * id + (max(ib, begin) == begin ? 0 : 1);
+      if (last && cut && ib >= begin && writer) {
         LatentCut w{};
         // (the last unit's cost: the units before it, and its item and those before)
-        w.follow = (int)run_owner(ie - 1 + COST * (k.item + 1), total, runs) - (int)blockIdx.x;
+        w.follow = (int)run_owner(ie - 1 + COST * (k.item + 1), total, runs) - id;
         w.slot = x.slot, w.rows = x.rows, w.step = 1, w.out = x.out;
-        parts.cuts[blockIdx.x] = w;
+        parts.cuts[id] = w;
       }
     }
     at = 0;

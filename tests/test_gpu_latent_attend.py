@@ -245,3 +245,17 @@ def test_refusals_of_the_binding():
     with pytest.raises(_lib.DsaError):
         call(ws=_lib.workspace(256, DEV))
     call()
+
+
+@pytest.mark.parametrize("lens,new,H", [([700, 64, 129], [1, 1, 1], 100), ([300, 1, 0], [8, 1, 3], 16), ([90, 5000], [5, 3], 24), ([200, 77], [1, 1], 65),
+                                        ([130, 130, 130], [3, 1, 0], 64)])
+def test_pairs_of_items(lens, new, H):
+    """65 to 128 rows a request in the mean: two items of 64 rows share their pages' loads; requests with
+    fewer rows, with more, and without any; NaN behind the last token and in a page seen in part."""
+    c = ref.Case(lens, new, H, "bf16", seed=31 + H)
+    for b, n in enumerate(lens):
+        for s in range(n % 64, 64 if n % 64 else 0):
+            spoil(c, int(c.block_table[b, n // 64]), s, "nan")
+    check(c)
+    c.block_table[0, 0] = -3
+    check(c, error=_lib.DSA_ERR_BAD_INDEX)
