@@ -78,52 +78,74 @@ __device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32
                : "memory");
 }
 
-// Merges the parts of cut items in the order of the runs: block (c, y) looks whether run c holds
-// an item's first part, and if so merges eight of its rows, one a warp.
-constexpr int kLatentMergeWarps = 8;
+// Merges the parts of cut items in the order of the runs: blocks (c, y) look whether run c holds an
+// item's first part, and if so merge rows of it, a warp one of 512 columns or four of 128 at a time.
+// (128 columns: with one row a warp two short prompts took 11.6 us instead of 10.4. 512: with one, two or four
+// rows of 128 columns a warp long contexts took 286 to 299 us instead of 280, two short requests 10.8 to 11.1 instead of 10.4.)
+constexpr int kLatentMergeWarps = 8, kLatentMergeBlocks = 8;   // blocks of a run at most
+template <int WIDTH>
+constexpr int kLatentMergeRows = WIDTH == 128 ? 4 : 1;
 
 template <int WIDTH>
 __global__ void __launch_bounds__(32 * kLatentMergeWarps) latent_merge_kernel(const LatentParts s, __nv_bfloat16* out,
                                                                               float* lse) {
   constexpr int V = WIDTH / 128;                   // float4 pieces a lane has, 128 values apart
-  constexpr int kBatch = V == 1 ? 8 : 4;           // parts whose loads are in flight together
+  constexpr int kRows = kLatentMergeRows<WIDTH>;
+  constexpr int kBatch = V == 1 ? 2 : 4;           // parts whose loads are in flight together
   griddep_wait();
   const LatentCut k = s.cuts[blockIdx.x];
-  const int row = blockIdx.y * kLatentMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (k.follow <= 0 || row >= k.rows) return;
-  float M = kNone, l = 0.f, o[4 * V] = {};
-  for (int p0 = 0; p0 <= k.follow; p0 += kBatch) {
-    float2 ml[kBatch];
-    float4 v[kBatch][V];
+  if (k.follow <= 0) return;
+  const int lane = threadIdx.x & 31;
+  for (int row0 = (blockIdx.y * kLatentMergeWarps + (threadIdx.x >> 5)) * kRows; row0 < k.rows;
+       row0 += gridDim.y * kLatentMergeWarps * kRows) {
+    float M[kRows], l[kRows] = {};
+    float4 o[kRows][V] = {};
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int p = p0 + i;
-      if (p > k.follow) break;
-      const int64_t at = (p == 0 ? (int64_t)k.slot : 2 * (int64_t)(blockIdx.x + p)) * s.rows + row;
-      ml[i] = __ldcg(reinterpret_cast<const float2*>(s.ml + at * 2));
+    for (int r = 0; r < kRows; ++r) M[r] = kNone;
+    for (int p0 = 0; p0 <= k.follow; p0 += kBatch) {
+      float2 ml[kBatch][kRows];
+      float4 v[kBatch][kRows][V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[i][j] = __ldcg(reinterpret_cast<const float4*>(s.o + at * WIDTH) + 32 * j + lane);
-    }
+      for (int i = 0; i < kBatch; ++i) {
+        const int p = p0 + i;
+        if (p > k.follow) break;
+        const int64_t part = (p == 0 ? (int64_t)k.slot : 2 * (int64_t)(blockIdx.x + p)) * s.rows;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (p0 + i > k.follow) break;
-      const float Mn = fmaxf(M, ml[i].x), a = ex2(M - Mn), b = ex2(ml[i].x - Mn);
-      M = Mn;
-      l = l * a + ml[i].y * b;
+        for (int r = 0; r < kRows; ++r) {
+          const int64_t at = part + min(row0 + r, k.rows - 1);
+          ml[i][r] = __ldcg(reinterpret_cast<const float2*>(s.ml + at * 2));
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        o[4 * j] = o[4 * j] * a + v[i][j].x * b, o[4 * j + 1] = o[4 * j + 1] * a + v[i][j].y * b;
-        o[4 * j + 2] = o[4 * j + 2] * a + v[i][j].z * b, o[4 * j + 3] = o[4 * j + 3] * a + v[i][j].w * b;
+          for (int j = 0; j < V; ++j) v[i][r][j] = __ldcg(reinterpret_cast<const float4*>(s.o + at * WIDTH) + 32 * j + lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (p0 + i > k.follow) break;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float Mn = fmaxf(M[r], ml[i][r].x), a = ex2(M[r] - Mn), b = ex2(ml[i][r].x - Mn);
+          M[r] = Mn;
+          l[r] = l[r] * a + ml[i][r].y * b;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            o[r][j].x = o[r][j].x * a + v[i][r][j].x * b, o[r][j].y = o[r][j].y * a + v[i][r][j].y * b;
+            o[r][j].z = o[r][j].z * a + v[i][r][j].z * b, o[r][j].w = o[r][j].w * a + v[i][r][j].w * b;
+          }
+        }
       }
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t at = k.out + (int64_t)row * k.step;
-  uint2* dst = reinterpret_cast<uint2*>(out + at * WIDTH) + lane;
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    dst[32 * j] = make_uint2(pack_bf16(o[4 * j] * inv, o[4 * j + 1] * inv), pack_bf16(o[4 * j + 2] * inv, o[4 * j + 3] * inv));
-  if (lse && lane == 0) lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+    for (int r = 0; r < kRows; ++r) {
+      if (row0 + r >= k.rows) break;
+      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+      const int64_t at = k.out + (int64_t)(row0 + r) * k.step;
+      uint2* dst = reinterpret_cast<uint2*>(out + at * WIDTH) + lane;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        dst[32 * j] = make_uint2(pack_bf16(o[r][j].x * inv, o[r][j].y * inv), pack_bf16(o[r][j].z * inv, o[r][j].w * inv));
+      if (lse && lane == 0) lse[at] = l[r] == 0.f ? -INFINITY : (M[r] + log2f(l[r])) * 0.6931471805599453f;
+    }
+  }
 }
 
 template <int WIDTH>
@@ -141,7 +163,7 @@ inline cudaError_t latent_merge_launch(const LatentParts& s, int runs, __nv_bflo
     if (dev < 64) set.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(runs, s.rows / kLatentMergeWarps);
+  cfg.gridDim = dim3(runs, min(s.rows / (kLatentMergeWarps * kLatentMergeRows<WIDTH>), kLatentMergeBlocks));
   cfg.blockDim = dim3(32 * kLatentMergeWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
