@@ -73,32 +73,35 @@ struct LatentShape {
 // Queries of records: the latent part of N rows in shared memory, bf16 to f16, each row by a power of
 // two that brings its largest magnitude into [2^13, 2^14) (what lies 2^31 below that may round; the
 // rest is exact). factor[row] undoes it. For 256 threads.
+// (Eight lanes have a row's 128 bytes of an atom, so that no two meet in a bank; each value is read once.)
 template <int N>
 __device__ __forceinline__ void queries_f16(uint8_t* q_buf, int tid, float* factor) {
-  constexpr int kPer = 32 * kSoftWarps / N, kChunks = 64 / kPer;   // threads of a row, its 16-byte chunks a thread has
-  const int row = tid / kPer, c0 = tid % kPer;
-  auto chunk = [&](int i) {
-    const int c = c0 + i * kPer;
-    return reinterpret_cast<uint4*>(q_buf + (c >> 3) * (N * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-  };
-  uint32_t top = 0;                              // largest magnitude, as bf16 bits
-#pragma unroll 4
-  for (int i = 0; i < kChunks; ++i) {
-    const uint4 v = *chunk(i);
-    const uint32_t o[4] = {v.x, v.y, v.z, v.w};
+  constexpr int kWarpRows = N / kSoftWarps;                      // 8, 4 or 2
+  constexpr int kLanes = kWarpRows == 2 ? 16 : 8, kAtoms = 64 / kLanes, kAtomStep = kLanes / 8;
+  const int lane = tid & 31;
+#pragma unroll 1
+  for (int r = 0; r < kWarpRows; r += 32 / kLanes) {
+    const int row = (tid >> 5) * kWarpRows + r + lane / kLanes;
+    uint8_t* at = q_buf + (lane >> 3) % kAtomStep * (N * 128) + row * 128 + (((lane ^ row) & 7) << 4);
+    uint4 v[kAtoms];
+    uint32_t top = 0;                            // largest magnitude, as bf16 bits
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(o[e] & 0x7FFFu, o[e] >> 16 & 0x7FFFu));
-  }
+    for (int i = 0; i < kAtoms; ++i) {
+      v[i] = *reinterpret_cast<const uint4*>(at + i * kAtomStep * (N * 128));
+      const uint32_t o[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-  for (int o = 1; o < kPer; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const int e = min(max((int)(top >> 7) - 127, -60), 127);
-  const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-  if (c0 == 0) factor[row] = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
-#pragma unroll 4
-  for (int i = 0; i < kChunks; ++i) {
-    const uint4 v = *chunk(i);
-    *chunk(i) = make_uint4(pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                           pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+      for (int e = 0; e < 4; ++e) top = max(top, max(o[e] & 0x7FFFu, o[e] >> 16 & 0x7FFFu));
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = min(max((int)(top >> 7) - 127, -60), 127);
+    const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+    if (lane % kLanes == 0) factor[row] = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < kAtoms; ++i)
+      *reinterpret_cast<uint4*>(at + i * kAtomStep * (N * 128)) =
+          make_uint4(pack_f16(bf16_lo(v[i].x) * up, bf16_hi(v[i].x) * up), pack_f16(bf16_lo(v[i].y) * up, bf16_hi(v[i].y) * up),
+                     pack_f16(bf16_lo(v[i].z) * up, bf16_hi(v[i].z) * up), pack_f16(bf16_lo(v[i].w) * up, bf16_hi(v[i].w) * up));
   }
 }
 
@@ -890,29 +893,42 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
               else if (A.lse) A.lse[x.out + row] = sum == 0.f ? -INFINITY : (M[i] + log2f(sum)) * 0.6931471805599453f;
             }
           }
+          constexpr int kCols = N == 16 ? 16 : 32;  // at a time: each look at tensor memory is waited for
 #pragma unroll 1
-          for (int k = 2 * N * half; k < 2 * N * (half + 1); k += 16) {
-            float v[16];
-            tmem_ld16(quarter + k, v);
+          for (int k = 2 * N * half; k < 2 * N * (half + 1); k += kCols) {
+            float v[kCols];
+            if constexpr (kCols == 16) tmem_ld16(quarter + k, v);
+            else tmem_ld32(quarter + k, v);
             tmem_ld_wait();
             const int dim = k / N * 128 + t, row = k % N;
-            if (x.slot >= 0) {
+            // (rows all in use as a case of its own: 16 branches a look at tensor memory otherwise)
+            auto part = [&](auto used) {
               float* dst = parts.o + ((int64_t)x.slot * R + N * rank + row) * kDimLatent + dim;
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (row + j < x.rows) dst[(int64_t)j * kDimLatent] = v[j];
-            } else {
+              for (int j = 0; j < kCols; ++j)
+                if (used(j)) dst[(int64_t)j * kDimLatent] = v[j];
+            };
+            auto output = [&](auto used) {
               // neighbouring lanes share two rows: the even one writes both columns of the first
               __nv_bfloat16* dst = A.out + (x.out + row + (lane & 1)) * kDimLatent + (dim & ~1);
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
+              for (int j = 0; j < kCols; j += 4) {
                 // (a row that saw nothing has zeros in O as well: all its weights were 0)
-                const float a = v[j] * s_keep[row + j], b = v[j + 1] * s_keep[row + j + 1];
-                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-                if (row + j + (lane & 1) < x.rows)
-                  *reinterpret_cast<uint32_t*>(dst + (int64_t)j * kDimLatent) = lane & 1 ? pack_bf16(other, b) : pack_bf16(a, other);
+                const float4 inv = *reinterpret_cast<const float4*>(&s_keep[row + j]);
+                const float w[4] = {v[j] * inv.x, v[j + 1] * inv.y, v[j + 2] * inv.z, v[j + 3] * inv.w};
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                  const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? w[i] : w[i + 1], 1);
+                  const uint32_t two = lane & 1 ? pack_bf16(other, w[i + 1]) : pack_bf16(w[i], other);
+                  if (used(j + i + (lane & 1))) *reinterpret_cast<uint32_t*>(dst + (int64_t)(j + i) * kDimLatent) = two;
+                }
               }
-            }
+            };
+            auto some = [&](int j) { return row + j < x.rows; };
+            auto all = [](int) { return true; };
+            const bool whole = row + kCols <= x.rows;
+            if (x.slot >= 0) whole ? part(all) : part(some);
+            else whole ? output(all) : output(some);
           }
           tc_fence_before();
         }
