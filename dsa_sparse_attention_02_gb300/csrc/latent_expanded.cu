@@ -8,7 +8,7 @@
 // 2,560 clocks of an SM's tensor cores for two tiles, which bound prompts (2048 tokens over
 // 16384, 32 heads: 470 to 490 us, 1.35 PFLOP/s); both products read as many operand bytes from
 // shared memory as 128 bytes a clock allow in that time. Few rows over many keys are bound by HBM
-// (16 requests of 100 rows over 1500 keys in the mean, 16 heads: 52 us, 4.3 TB/s).
+// (16 requests of 100 rows over 1500 keys in the mean, 16 heads: 51 us, 4.4 TB/s).
 //
 //   * tensor memory holds S (128 columns; P, packed bf16, takes its place) and O (128) in each of
 //     two places: all 512. A tile goes through scores, softmax and values one after the other;
