@@ -52,7 +52,11 @@ struct LatentShape {
   // Rings as deep as shared memory allows.
   static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 64 ? 6 : 8);
   static constexpr int kRopes = !kRecord && N == 16 ? 3 : kRecord && N == 64 ? 1 : 2;
-  static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 2 : N == 32 ? 3 : 6;
+  static constexpr int kCodes = !kRecord ? 0 : N == 16 ? 6 : 2;
+  // (Records: the two groups of converting warps, and the two that issue scores, take every other place. In
+  // an odd ring one would come to a place that the other's load has not reached yet, and take the phase
+  // before that for the one it waits for.)
+  static_assert(!kRecord || (kPairs % 2 == 0 && kCodes % 2 == 0), "a place has one user");
   // Scores, from column 256 on. bf16 rows: a page's in one place (two, one of each issuer), two pages at a
   // time. Records: the rotated part's and three of the scales' in a place each, the last scale's in the
   // rotated part's. P: one of a page, or three, the last scale's in the first's place.

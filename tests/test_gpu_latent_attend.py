@@ -259,3 +259,22 @@ def test_pairs_of_items(lens, new, H):
     check(c)
     c.block_table[0, 0] = -3
     check(c, error=_lib.DSA_ERR_BAD_INDEX)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,n,new,H", [(22, 5500, 2, 12), (7, 9000, 1, 32), (60, 1300, 1, 20), (8, 4000, 1, 16), (10, 4000, 3, 16), (3, 9000, 1, 128)])
+def test_long_runs_of_each_row_count(B, n, new, H, kind):
+    """Runs of tens of pages with 16, 17 to 32 and up to 64 rows an item, many times over: rings come
+    round many times, and nothing depends on which load is first."""
+    lens = [n - 37 * b for b in range(B)]
+    c = ref.Case([64 * 40], [1], H, kind, seed=B, spare=0)          # a small cache whose pages repeat
+    c.lens, c.new, c.T, c.max_len = lens, [new] * B, new * B, n
+    c.seq_lens = torch.tensor(lens, dtype=torch.int32)
+    c.cu_q = torch.arange(B + 1, dtype=torch.int32) * new
+    c.block_table = torch.randint(0, c.P, (B, -(-n // 64)), generator=c.gen, dtype=torch.int32)
+    c.q = torch.randn(c.T, H, 576, generator=c.gen).bfloat16()
+    d, out, lse = check(c, ts={0, c.T - 1, c.T // 2})
+    for _ in range(30):
+        again = d.attend()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert _lib.dsa_get_error(d.ws) == 0
