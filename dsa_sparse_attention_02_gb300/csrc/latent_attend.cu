@@ -327,6 +327,18 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       }
       if (ok && lane == 0) mbar_arrive(smem_u32(&u_loaded[us]));
     }
+    // In a cluster the other block's products arrive here too when they have read a place: the last of
+    // them as well, before this block may leave.
+    if (CL > 1) {
+      for (int i = 0; i < S::kPairs && ok; ++i) {
+        ok = warp_wait(&pair_empty[pair], pair_ph ^ 1, abort, A.err);
+        if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
+      }
+      for (int i = 0; i < S::kRopes && ok; ++i) {
+        ok = warp_wait(&rope_empty[rope], rope_ph ^ 1, abort, A.err);
+        if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
+      }
+    }
     // Copies in flight land before shared memory is given back: every slot's last copy is waited
     // for by its reader, or, when the run was given up, here.
     if (!ok) {
