@@ -50,9 +50,9 @@ template <int N, int KV>
 struct LatentShape {
   static constexpr bool kRecord = KV != kKvBf16;
   // Rings as deep as shared memory allows.
-  static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 64 ? 6 : 8);
+  static constexpr int kPairs = !kRecord ? (N == 16 ? 11 : N == 32 ? 10 : 8) : (N == 16 ? 8 : 6);
   static constexpr int kRopes = !kRecord && N == 16 ? 3 : kRecord && N == 64 ? 1 : 2;
-  static constexpr int kCodes = !kRecord ? 0 : N == 16 ? 6 : 2;
+  static constexpr int kCodes = !kRecord ? 0 : N == 64 ? 2 : 6;
   // (Records: the two groups of converting warps, and the two that issue scores, take every other place. In
   // an odd ring one would come to a place that the other's load has not reached yet, and take the phase
   // before that for the one it waits for.)
