@@ -207,10 +207,7 @@ class Geometry:
         self.c = dsa_geom_t(self.B, self.T, self.max_seq_len, self.num_pages, 64,
                             int(block_table.shape[1]) if block_table.dim() == 2 else 0,
                             _dptr(seq_lens), _dptr(cu_q), _dptr(block_table))
-
-    @property
-    def ref(self):
-        return C.byref(self.c)
+        self.ref = C.byref(self.c)
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -359,6 +356,7 @@ class GqaCache:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
@@ -504,7 +502,7 @@ def _latent_call(ws, stream, index):
     """Checks common to the latent calls; the raw stream to enqueue on."""
     if ws is None or not ws.is_contiguous():      # (its size goes by its elements)
         raise TypeError("ws must be a contiguous tensor, as workspace() makes it")
-    if ws.get_device() != index or index < 0 or torch.cuda.current_device() != index:
+    if index < 0 or ws.get_device() != index or _current_device() != index:
         raise ValueError("tensors, geometry and workspace must be on the current device, "
                          f"cuda:{torch.cuda.current_device()}" if torch.cuda.is_available() else "tensors must be CUDA tensors")
     if stream is not None:
@@ -530,14 +528,16 @@ def _tensor(name, t, dtype, shape, index, inner=1):
     """Address of a tensor of this type and shape whose innermost `inner` dimensions lie side by
     side, and its other strides."""
     # (on the way of a call that fits, nothing is looked at twice: some of these calls take microseconds)
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape:
-        if inner == len(shape):
-            if t.is_contiguous():
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+            if inner == 1:
+                st = t.stride()
+                if st[-1] == 1 and 1 not in shape:
+                    return (t.data_ptr(),) + st[:-1]
+            elif inner == len(shape) and t.is_contiguous():
                 return (t.data_ptr(),)
-        elif inner == 1 and 1 not in shape:
-            *outer, last = t.stride()
-            if last == 1:
-                return (t.data_ptr(), *outer)
+    except AttributeError:                        # (no tensor: told below)
+        pass
     if t is None:
         raise TypeError(f"{name} is missing")
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
@@ -637,7 +637,7 @@ def dsa_latent_attend_expanded(cu_q, cu_k, q, k, v, k_rope, sm_scale: float, out
     [T, H, 128] bf16 and lse [T, H] fp32 (or None). q, k, v and k_rope may be strided views."""
     index = cu_q.get_device()
     st = _latent_call(ws, stream, index)
-    B, (T, H), S = cu_q.shape[0] - 1, q.shape[:2], k.shape[0]
+    B, T, H, S = cu_q.shape[0] - 1, q.shape[0], q.shape[1], k.shape[0]
     cq, = _tensor("cu_q", cu_q, _I32, (B + 1,), index)
     ck, = _tensor("cu_k", cu_k, _I32, (B + 1,), index)
     qp, qt, qh = _tensor("q", q, _BF16, (T, H, 192), index)
