@@ -1,6 +1,6 @@
-// Units of the dense absorbed attention (latent_attend.cu, latent_cluster.cu): an item is (request,
-// N of its tokens x heads), a unit a page of 64 keys that some row of the item sees. All units are
-// laid end to end and cut into equal runs.
+// Units of the dense absorbed attention (latent_attend.cu): an item is (request, N of its tokens x
+// heads), a unit a page of 64 keys that some row of the item sees. All units are laid end to end
+// and cut into runs of equal cost.
 #pragma once
 #include "latent_common.cuh"
 
