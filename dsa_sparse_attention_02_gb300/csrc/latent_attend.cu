@@ -29,8 +29,8 @@
 //               is brought to f16 by an exact power of two a row.
 // What bounds it. bf16 rows, 16 heads: HBM (376 MB in 71 us, of which 60 at 6.0 TB/s). 64 rows an item:
 // the chain of a page, as two pages are all that fits beside the queries: loads (1900 clocks) ->
-// scores (2000) -> softmax (1200) -> values (1500), 3,000 clocks a page, 2,700 in clusters (128 heads: 130 us, pages read
-// once for two items by a cluster's two CTAs, 3.0 TB/s). Records, 64 rows: values -> conversion of the next page's last two pairs ->
+// scores (2000) -> softmax (1200) -> values (1500), 3,000 clocks a page (128 heads: 129.5 us, pages read
+// from HBM once for two items in neighbouring blocks, 3.0 TB/s). Records, 64 rows: values -> conversion of the next page's last two pairs ->
 // their scores -> softmax -> weights, and the softmax warps' own steps (each wait 200 clocks), which
 // are as long: 4,700 clocks a page (8 contexts of 131072 in e4m3: 269 us, 2.6 TB/s). Issue slots 54%,
 // tensor cores 26% busy (when it took 370 us).
@@ -123,9 +123,9 @@ struct Ring {
   }
 };
 
-// CL: CTAs of a cluster, which have neighbouring items of N rows each over the same pages, each loading
-// half of every page for both.
-template <int N, int KV, int CL>
+// BL: blocks of a run, which have neighbouring items of N rows each over the same pages at about the same
+// time, so that a page is read from HBM by the first and found in L2 by the other.
+template <int N, int KV, int BL>
 __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     latent_attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_pair,
                          const __grid_constant__ CUtensorMap map_rope, const LatentAttendArgs A, const LatentParts parts) {
@@ -133,10 +133,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   constexpr bool kRecord = S::kRecord;
   constexpr int kLoadWarp = S::kLoadWarp, kFixWarp0 = S::kFixWarp0;
   constexpr uint32_t kFmt = kRecord ? kFmtF16 : kFmtBF16;   // of latents, and of weights
-  static_assert(CL == 1 || !kRecord, "records have no cluster form");
-  constexpr int R = CL * N;                     // rows of an item as the units and the parts see it
-  constexpr uint16_t kAll = (1 << CL) - 1;
-  const int rank = CL == 1 ? 0 : (int)cluster_ctarank();
+  static_assert(BL == 1 || !kRecord, "records have no form of two blocks");
+  constexpr int R = BL * N;                     // rows of an item as the units and the parts see it
+  const int rank = BL == 1 ? 0 : (int)blockIdx.x % BL;
   // Weights in f16 use its range upwards as well: 2^7 at the reference, and so below 2^16.
   constexpr float kLift = kRecord ? 7.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
@@ -176,11 +175,11 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     }
     for (int i = 0; i < S::kPairs; ++i) {
       mbar_init(smem_u32(&pair_full[i]), kRecord ? S::kFixWarps / 2 : 1);
-      mbar_init(smem_u32(&pair_empty[i]), CL);
+      mbar_init(smem_u32(&pair_empty[i]), 1);
     }
     for (int i = 0; i < S::kRopes; ++i) {
       mbar_init(smem_u32(&rope_full[i]), 1);
-      mbar_init(smem_u32(&rope_empty[i]), CL);
+      mbar_init(smem_u32(&rope_empty[i]), 1);
     }
     if (kRecord) {
       for (int i = 0; i < kScaleSlots; ++i) mbar_init(smem_u32(&scale_full[i]), 1);
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
     tmem_alloc(smem_u32(&s_tmem), kTmem);
     tmem_relinquish();
   }
-  LatentCursor<R, S::kItemCost> at(A, parts, blockIdx.x / CL, gridDim.x / CL, rank == 0);
+  LatentCursor<R, S::kItemCost> at(A, parts, blockIdx.x / BL, gridDim.x / BL, rank == 0);
   if (warp == kLoadWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&map_q);
@@ -228,7 +227,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CL > 1) cluster_sync();                   // (the other's barriers are set up)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort = &s_abort;
@@ -257,7 +255,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
       if (!ok) break;
       if (lane == at.at) {
         LatentUnit x = at.x;
-        if (CL > 1) x.row0 += N * rank, x.out += N * rank, x.rows = min(max(x.rows - N * rank, 0), N);
+        if (BL > 1) x.row0 += N * rank, x.out += N * rank, x.rows = min(max(x.rows - N * rank, 0), N);
         s_unit[us] = x;
         s_bad[us][0] = s_bad[us][1] = 0;
       }
@@ -272,8 +270,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
           if (pg >= 0) {
             mbar_arrive_expect_tx(bar, kRopeBytes);
             if (kRecord) tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, 0, pg);
-            else if (CL == 1) tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8);
-            else if ((n & 1) == rank) tma_load_3d_multicast(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8, kAll);
+            else tma_load_3d(smem_u32(rope_buf + rope * kRopeBytes), &map_rope, bar, 0, pg * kPage, 8);
           } else {
             mbar_arrive(bar);
           }
@@ -315,9 +312,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             const uint32_t bar = smem_u32(&pair_full[pair]);
             if (pg >= 0) {
               mbar_arrive_expect_tx(bar, kPairBytes);
-              const uint32_t dst = smem_u32(pair_buf + pair * kPairBytes);
-              if (CL == 1) tma_load_3d(dst, &map_pair, bar, 0, pg * kPage, 2 * j);
-              else if ((j & 1) == rank) tma_load_3d_multicast(dst, &map_pair, bar, 0, pg * kPage, 2 * j, kAll);
+              tma_load_3d(smem_u32(pair_buf + pair * kPairBytes), &map_pair, bar, 0, pg * kPage, 2 * j);
             } else {
               mbar_arrive(bar);
             }
@@ -326,18 +321,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
         }
       }
       if (ok && lane == 0) mbar_arrive(smem_u32(&u_loaded[us]));
-    }
-    // In a cluster the other block's products arrive here too when they have read a place: the last of
-    // them as well, before this block may leave.
-    if (CL > 1) {
-      for (int i = 0; i < S::kPairs && ok; ++i) {
-        ok = warp_wait(&pair_empty[pair], pair_ph ^ 1, abort, A.err);
-        if (++pair == S::kPairs) pair = 0, pair_ph ^= 1u;
-      }
-      for (int i = 0; i < S::kRopes && ok; ++i) {
-        ok = warp_wait(&rope_empty[rope], rope_ph ^ 1, abort, A.err);
-        if (++rope == S::kRopes) rope = 0, rope_ph ^= 1u;
-      }
     }
     // Copies in flight land before shared memory is given back: every slot's last copy is waited
     // for by its reader, or, when the run was given up, here.
@@ -394,8 +377,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             const uint64_t kd = desc_add(dr, rope.at * kRopeBytes), qd = desc_add(dq, 8 * N * 128);
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_f16_ss(d, desc_add(qd, k * 32), desc_add(kd, k * 32), idesc_rope, k != 0);
-            if (CL == 1) mma_commit(smem_u32(&rope_empty[rope.at]));
-            else mma_commit_multicast(smem_u32(&rope_empty[rope.at]), kAll);
+            mma_commit(smem_u32(&rope_empty[rope.at]));
           }
           __syncwarp();
           rope.step(1);
@@ -451,8 +433,7 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_f16_ss(jj * N, desc_add(vd, k * 2048), desc_add(pd, k * 32), idesc, k != 0 ? 1u : kept);
-              if (CL == 1) mma_commit(smem_u32(&pair_empty[pair.at]));
-              else mma_commit_multicast(smem_u32(&pair_empty[pair.at]), kAll);
+              mma_commit(smem_u32(&pair_empty[pair.at]));
               if (kRecord && jj == 0) mma_commit(smem_u32(&p_used)), mma_commit(smem_u32(&f_front));
               if (jj + kStep >= 4) mma_commit(smem_u32(&o_done[n & 1]));
               if (kRecord && jj == 3) mma_commit(smem_u32(&f_last));
@@ -957,7 +938,6 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CL > 1) cluster_sync();                   // (nothing arrives here any more)
   if (warp == kScoreWarp0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmem);
@@ -970,34 +950,25 @@ int latent_rows(const GeomDev& g, int H) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-// Whether two items of a request go to the two CTAs of a cluster: where it has just two in the mean. (64 requests
-// of 128 rows over 5000 keys 130 us, without 144; 32 over 3000 54 and 56. More items find their pages in L2, and
-// an odd one leaves half of a cluster idle: 256 rows 34.8 and 33.9, 192 rows 202 and 167, 4800 rows 97 and 94.)
+// Whether two items of a request go to two neighbouring blocks: where it has just two in the mean. (64 requests
+// of 128 rows over 5000 keys 129.5 us, without 143; 40 of 80 rows over 6750 108 and 118; 32 of 128 over 2250 43 and
+// 44; 8 over 3000 28 and 27; a single one over 30000 50 and 39.5, for its parts are merged by fewer blocks.)
 bool latent_pairs(const GeomDev& g, int H) {
   const int64_t rows = ((int64_t)g.T + g.B - 1) / g.B * H;
   return rows > 64 && rows <= 128;
 }
 
-template <int N, int KV, int CL>
+template <int N, int KV, int BL>
 cudaError_t launch(const LatentAttendArgs& A, const LatentMaps& m, int num_sms, cudaStream_t st) {
   using S = LatentShape<N, KV>;
-  const int runs = num_sms / CL;
-  const LatentParts parts = latent_parts(A.scratch, runs, CL * N, kDimLatent);
-  auto kern = latent_attend_kernel<N, KV, CL>;
+  const int runs = num_sms / BL;
+  const LatentParts parts = latent_parts(A.scratch, runs, BL * N, kDimLatent);
+  auto kern = latent_attend_kernel<N, KV, BL>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(kern, S::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(runs * CL);
-  cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CL, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CL > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, m.q, m.pair, m.rope, A, parts);
+  kern<<<runs * BL, S::kThreads, S::kSmem, st>>>(m.q, m.pair, m.rope, A, parts);
+  e = cudaGetLastError();
   return e != cudaSuccess ? e : latent_merge_launch<kDimLatent>(parts, runs, A.out, A.lse, st);
 }
 template <int KV>

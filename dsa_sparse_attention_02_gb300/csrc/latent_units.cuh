@@ -59,7 +59,7 @@ __device__ __forceinline__ int64_t latent_before(const LatentAttendArgs& A, cons
   return s;
 }
 
-// Finds the units of run `id` of `grid` (a block's, or a cluster's); whole warp, which keeps up to 32 units at a time, one a lane.
+// Finds the units of run `id` of `grid` (a block's, or that of two neighbours); whole warp, which keeps up to 32 units at a time, one a lane.
 // Runs are equal in cost: an item's units, and COST for it (its queries, and its outputs, which no
 // product hides).
 template <int N, int COST>
