@@ -142,8 +142,8 @@ dsa_status_t dsa_latent_attend(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, int
   if (!format_of(kv_dtype, &A.kv_format) || H < 1 || H > kMaxHeads) return DSA_ERR_INVALID_ARG;
   const float scale_log2 = sm_scale * 1.4426950408889634f;   // scores in powers of two
   if (!std::isfinite(scale_log2) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
-  if ((int64_t)geom->T * H > INT32_MAX) {
-    set_last_error("dsa_latent_attend", "T * H above 2^31 - 1");
+  if ((int64_t)geom->T * H > INT32_MAX - 127) {        // (rounded up to items, of 128 rows at most, in 32 bits)
+    set_last_error("dsa_latent_attend", "T * H above 2^31 - 128");
     return DSA_ERR_UNSUPPORTED;
   }
   if (!ws_ok(ws, ws_bytes, attend_ws(geom, H))) return DSA_ERR_WORKSPACE;

@@ -38,7 +38,7 @@ __device__ __forceinline__ LatentReq latent_req(const LatentAttendArgs& A, int b
   r.n = max(min(c1, A.g.T) - r.q0, 0);
   r.none = r.bad || len <= 0;
   r.start = len - r.n;
-  r.tiles = (r.n * A.H + N - 1) / N;      // (T * H stays below 2^31)
+  r.tiles = (r.n * A.H + N - 1) / N;      // (T * H <= 2^31 - 128)
   return r;
 }
 // Pages that tile i's last token sees; at least one unit, so that empty rows are written too.

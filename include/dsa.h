@@ -562,7 +562,7 @@ size_t dsa_latent_append_workspace_size(const dsa_geom_t* geom);
  *   Weights are rounded to bf16 before they meet the rows (records: weight times scale, to f16,
  *     a row's largest being 2^7 at least); all sums are fp32; out is rounded once more, to bf16.
  *     Over records the queries' first 512 values are exact down to 2^-31 of a row's largest.
- *   sm_scale >= 0, and sm_scale * log2(e) finite in fp32. T * H < 2^31.
+ *   sm_scale >= 0, and sm_scale * log2(e) finite in fp32. T * H <= 2^31 - 128.
  */
 dsa_status_t dsa_latent_attend(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, int32_t H, const void* q,
                                const void* kv_cache, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
