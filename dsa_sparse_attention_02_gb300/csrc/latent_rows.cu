@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) latent_gather_kernel(const La
   // lane i: output row s0 + i; -2 where it is none of a request's, -1 where it has no row in the cache
   int64_t mine = -2;
   const int64_t s = s0 + lane;
-  if (lane < kGatherRows && s < A.S && s < __ldg(A.cu_k + A.g.B)) {
+  if (lane < kGatherRows && s < A.S && s >= __ldg(A.cu_k) && s < __ldg(A.cu_k + A.g.B)) {
     int lo = 0, hi = A.g.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;

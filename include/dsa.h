@@ -576,8 +576,8 @@ size_t dsa_latent_attend_workspace_size(const dsa_geom_t* geom, int32_t H);
  *   cu_k [B+1] int32 (device): request b's rows are out's cu_k[b] .. cu_k[b+1]-1, its positions
  *     first[b] + 0, 1, ... (first [B] int32, or NULL for 0). geom->cu_q and T are not used.
  *   out: row s at s*out_stride (in elements, a multiple of 8, >= 576), 576 bf16, for s < S; rows
- *     from cu_k[B] on are left as they were. A position outside the request's seq_lens or
- *     a bad page id gives a row of zeros and sets DSA_ERR_BAD_INDEX.
+ *     before cu_k[0] and from cu_k[B] on are left as they were. A position outside the request's
+ *     seq_lens or a bad page id gives a row of zeros and sets DSA_ERR_BAD_INDEX.
  *   ws: 256 bytes (the header).
  */
 dsa_status_t dsa_latent_gather(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, const void* kv_cache, const int32_t* first,
