@@ -500,7 +500,9 @@ __global__ void __launch_bounds__(LatentShape<N, KV>::kThreads, 1)
             if (bad && ct <= last) atomicOr(&s_bad[us][ct >> 5], 1u << (ct & 31));
             if (bad || ct > last) *at = make_float4(0.f, 0.f, 0.f, 0.f);
           }
-          s_lg[us][ct] = lg2(fmaxf(top, 7.8886091e-31f));   // (2^-100: all four may be 0)
+          // (2^-88 at least: all four may be 0. A weight is then below 2^(88 + kLift + kMove) = 2^103, and
+          // 2^25 of them in a run's sum below 2^128.)
+          s_lg[us][ct] = lg2(fmaxf(top, 3.2311743e-27f));
         }
         // eight codes a thread and round: half a warp reads a row's 128, and eight threads write a row of an atom
         constexpr int kRounds = kPage * 16 / (16 * S::kFixWarps), kRows = S::kFixWarps;

@@ -1,10 +1,14 @@
-"""Ends of the dense latent operators' ranges on the GPU: offsets that do not begin at 0."""
+"""Ends of the dense latent operators' ranges on the GPU: offsets that do not begin at 0, scales too
+small to matter over long contexts."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
 import latent_reference as ref
 from dsa_sparse_attention_02_gb300 import _lib
-from test_gpu_latent_attend import DEV, KINDS, Dev
+from test_gpu_latent_attend import DEV, KINDS, Dev, compare
 from test_gpu_latent_rows import gathered
 
 pytestmark = pytest.mark.gpu
@@ -23,3 +27,38 @@ def test_gather_leaves_rows_before_the_first_request(kind, at):
     assert _lib.dsa_get_error(ws) == 0
     assert (out[:at] == 7.0).all() and (out[at + 230:] == 7.0).all()
     assert torch.equal(out[at:at + 230].cpu(), gathered(c, [0, 0, 0], [100, 0, 130]))
+
+
+def repeated(lens, new, H, kind, seed, pages):
+    """Requests whose block tables repeat a few pages."""
+    c = ref.Case([64 * pages], [1], H, kind, seed=seed, spare=0)
+    B, n = len(lens), max(lens)
+    c.lens, c.new, c.T, c.max_len = list(lens), list(new), sum(new), n
+    c.seq_lens = torch.tensor(c.lens, dtype=torch.int32)
+    c.cu_q = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32)
+    c.block_table = torch.randint(0, c.P, (B, -(-n // 64)), generator=c.gen, dtype=torch.int32)
+    c.q = torch.randn(c.T, H, 576, generator=c.gen).bfloat16()
+    return c
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+def test_small_scales_over_long_runs(kind):
+    """Scales of 2^-100 and scores that rise by e^5 behind the first page: the weights' sum, 40000 keys
+    in one run, stays finite."""
+    B, n = torch.cuda.get_device_properties(0).multi_processor_count, 40000
+    c = repeated([n] * B, [1] * B, 16, kind, 22, 2)
+    c.block_table[:, 0], c.block_table[:, 1:] = 0, 1
+    _, scale, rope = ref.planes(c.cache)
+    scale[...] = 2.0 ** -100
+    rope.zero_()
+    rope[1, :, 0] = 5.0
+    c.q[..., 512] = 1.0
+    d = Dev(c)
+    out, lse = d.attend(1.0)
+    assert _lib.dsa_get_error(d.ws) == 0
+    res = ref.attend(c, 1.0, {0, B - 1})
+    for r in res.values():
+        r[2][...] -= 1e-30                        # (an absolute term, as large as these values)
+    compare(res, out, lse)
+    want = math.log(64 + (n - 64) * math.exp(5.0))
+    assert (lse.double() - want).abs().max() < 1e-4
