@@ -1,5 +1,5 @@
 """Ends of the dense latent operators' ranges on the GPU: offsets that do not begin at 0, scales too
-small to matter over long contexts."""
+small to matter over long contexts, runs of many pages."""
 import math
 
 import numpy as np
@@ -8,7 +8,7 @@ import torch
 
 import latent_reference as ref
 from dsa_sparse_attention_02_gb300 import _lib
-from test_gpu_latent_attend import DEV, KINDS, Dev, compare
+from test_gpu_latent_attend import DEV, KINDS, Dev, check, compare
 from test_gpu_latent_rows import gathered
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +62,25 @@ def test_small_scales_over_long_runs(kind):
     compare(res, out, lse)
     want = math.log(64 + (n - 64) * math.exp(5.0))
     assert (lse.double() - want).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("H,new,tile,blocks", [(16, 1, 16, 1), (5, 3, 16, 1), (20, 1, 32, 1), (12, 2, 32, 1), (64, 1, 64, 1), (20, 3, 64, 1),
+                                               (128, 1, 64, 2), (24, 4, 64, 2), (128, 2, 64, 1)])
+def test_runs_of_thirty_pages_and_more(kind, H, new, tile, blocks):
+    """Every row count and form: each run has 30 pages at least, so that rings of places come round
+    seven times or more; 30 repeats give the same bits."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    runs = sms // blocks if kind == "bf16" else sms
+    rows = tile * blocks if kind == "bf16" else tile
+    B, items = 24, -(-H * new // rows)
+    n = 64 * (-(-36 * runs // (B * items)))
+    lens = [n - 37 * (b % 8) for b in range(B)]
+    assert min(lens) > new and sum(items * -(-x // 64) for x in lens) >= 30 * runs
+    c = repeated(lens, [new] * B, H, kind, H + new, 40)
+    d, out, lse = check(c, ts={0, c.T - 1, c.T // 2})
+    assert torch.isfinite(lse).all()
+    for _ in range(30):
+        again = d.attend()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert _lib.dsa_get_error(d.ws) == 0
