@@ -524,6 +524,13 @@ def _latent_cache(kv_dtype, kv_cache, geom, index):
                     "geometry's device")
 
 
+def _shape(name, t, dims):
+    """Shape of a tensor whose sizes a call goes by."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise TypeError(f"{name} must be a tensor of {dims} dimension{'s'[:dims > 1]}")
+    return t.shape
+
+
 def _tensor(name, t, dtype, shape, index, inner=1):
     """Address of a tensor of this type and shape whose innermost `inner` dimensions lie side by
     side, and its other strides."""
@@ -570,6 +577,8 @@ def dsa_latent_append(geom: Geometry, kv_dtype: int, kv_in, kv_cache, rope: Rope
         raise TypeError("kv_cache and kv_out go with kv_in")
     index = geom.seq_lens.get_device()
     st = _latent_call(ws, stream, index)
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
     T = geom.T
     kv = cache = gm = ko = qi = qo = None
     ks = H = qit = qih = qot = qoh = 0
@@ -581,7 +590,7 @@ def dsa_latent_append(geom: Geometry, kv_dtype: int, kv_in, kv_cache, rope: Rope
         if kv_out is not None:
             ko, = _tensor("kv_out", kv_out, _BF16, (T, 576), index, 2)
     if q_in is not None:
-        H = q_in.shape[1]
+        H = _shape("q_in", q_in, 3)[1]
         qi, qit, qih = _tensor("q_in", q_in, _BF16, (T, H, 64), index)
         qo, qot, qoh = _tensor("q_out", q_out, _BF16, (T, H, 64), index)
     s = load().dsa_latent_append(geom.ref, kv_dtype, kv, ks, gm, eps, rope.ref, cache, ko, H, qi, qit, qih, qo, qot, qoh,
@@ -599,7 +608,7 @@ def dsa_latent_attend(geom: Geometry, kv_dtype: int, q, kv_cache, sm_scale: floa
     [T, H, 512] bf16 and lse [T, H] fp32 (or None)."""
     index = geom.seq_lens.get_device()
     st = _latent_call(ws, stream, index)
-    T, H = geom.T, q.shape[1]
+    T, H = geom.T, _shape("q", q, 3)[1]
     qp, = _tensor("q", q, _BF16, (T, H, 576), index, 3)
     cache = _latent_cache(kv_dtype, kv_cache, geom, index)
     op, = _tensor("out", out, _BF16, (T, H, 512), index, 3)
@@ -618,11 +627,12 @@ def dsa_latent_gather(geom: Geometry, kv_dtype: int, kv_cache, first, cu_k, out,
     first[b] (None: 0) on, records dequantised."""
     index = geom.seq_lens.get_device()
     st = _latent_call(ws, stream, index)
+    S = _shape("out", out, 2)[0]
     cache = _latent_cache(kv_dtype, kv_cache, geom, index)
     fp = None if first is None else _tensor("first", first, _I32, (geom.B,), index)[0]
     cp, = _tensor("cu_k", cu_k, _I32, (geom.B + 1,), index)
-    op, os_ = _tensor("out", out, _BF16, (out.shape[0], 576), index)
-    s = load().dsa_latent_gather(geom.ref, kv_dtype, cache, fp, cp, out.shape[0], op, os_, ws.data_ptr(), ws.numel(), st)
+    op, os_ = _tensor("out", out, _BF16, (S, 576), index)
+    s = load().dsa_latent_gather(geom.ref, kv_dtype, cache, fp, cp, S, op, os_, ws.data_ptr(), ws.numel(), st)
     if s:
         raise DsaError(s, "dsa_latent_gather")
 
@@ -635,9 +645,10 @@ def dsa_latent_attend_expanded(cu_q, cu_k, q, k, v, k_rope, sm_scale: float, out
     """Causal attention of q [T, H, 192] over expanded keys k [S, H, 128] with the rotated parts
     k_rope [S, 64] of all heads and values v [S, H, 128], ragged by cu_q and cu_k [B+1], into out
     [T, H, 128] bf16 and lse [T, H] fp32 (or None). q, k, v and k_rope may be strided views."""
+    B = _shape("cu_q", cu_q, 1)[0] - 1
     index = cu_q.get_device()
     st = _latent_call(ws, stream, index)
-    B, T, H, S = cu_q.shape[0] - 1, q.shape[0], q.shape[1], k.shape[0]
+    (T, H, _), S = _shape("q", q, 3), _shape("k", k, 3)[0]
     cq, = _tensor("cu_q", cu_q, _I32, (B + 1,), index)
     ck, = _tensor("cu_k", cu_k, _I32, (B + 1,), index)
     qp, qt, qh = _tensor("q", q, _BF16, (T, H, 192), index)

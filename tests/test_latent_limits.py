@@ -4,6 +4,7 @@ import glob
 import os
 
 import pytest
+import torch
 
 from dsa_sparse_attention_02_gb300 import _lib, build
 from test_gqa_abi import UNS, WSP, geom, lib, ref  # noqa: F401
@@ -28,3 +29,33 @@ def test_attend_refuses_rows_that_do_not_round_up_to_items(lib, H, least):  # no
     for T in (least, least + 1, (1 << 31) - 1):
         assert call(T) == UNS
         assert b"2^31" in lib.dsa_last_error()
+
+
+def test_binding_names_a_tensor_that_is_missing_or_has_other_dimensions(monkeypatch):
+    """Also those whose sizes the calls go by: a TypeError with their name, not one about an attribute or index."""
+    class Handle:                                    # a geometry without a device
+        T, B, num_pages, max_seq_len = 3, 1, 2, 128
+        seq_lens = torch.zeros(1, dtype=torch.int32)
+
+    monkeypatch.setattr(_lib, "_latent_call", lambda ws, stream, index: 0)
+    g, ws, cu = Handle(), torch.zeros(256, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+    x = torch.zeros(3, 2, 576, dtype=torch.bfloat16)
+    cache, part = torch.zeros(2, 64, 576, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    for bad in (None, 3, torch.zeros(3, dtype=torch.bfloat16), torch.zeros(3, 2, 1, 64, dtype=torch.bfloat16)):
+        with pytest.raises(TypeError, match="^q must"):
+            _lib.dsa_latent_attend(g, _lib.DSA_BF16, bad, cache, 0.1, x, None, ws)
+        with pytest.raises(TypeError, match="^out must"):
+            _lib.dsa_latent_gather(g, _lib.DSA_BF16, cache, None, cu, bad, ws)
+        with pytest.raises(TypeError, match="^q must"):
+            _lib.dsa_latent_attend_expanded(cu, cu, bad, x, x, x, 0.1, x, None, ws)
+        with pytest.raises(TypeError, match="^k must"):
+            _lib.dsa_latent_attend_expanded(cu, cu, x, bad, x, x, 0.1, x, None, ws)
+        if bad is not None:
+            with pytest.raises(TypeError, match="^q_in must"):
+                _lib.dsa_latent_append(g, _lib.DSA_BF16, None, None, _lib.Rope(), q_in=bad, q_out=part, ws=ws)
+    for bad in (None, 3, torch.zeros(2, 2, dtype=torch.int32), torch.tensor(2, dtype=torch.int32)):
+        with pytest.raises(TypeError, match="^cu_q must"):
+            _lib.dsa_latent_attend_expanded(bad, cu, x, x, x, x, 0.1, x, None, ws)
+    for bad in (None, _lib.dsa_rope_t(), 64):
+        with pytest.raises(TypeError, match="^rope must"):
+            _lib.dsa_latent_append(g, _lib.DSA_BF16, None, None, bad, q_in=part, q_out=part, ws=ws)
