@@ -557,7 +557,7 @@ def _tensor(name, t, dtype, shape, index, inner=1):
     # (a stride over a single element says nothing: the least that fits)
     outer, least = [], width
     for i in range(len(shape) - inner - 1, -1, -1):
-        outer.append(st[i] if shape[i] > 1 else max(least, st[i]))
+        outer.append(st[i] if shape[i] > 1 else least)
         least = outer[-1] * shape[i] if shape[i] > 1 else outer[-1]
     return (t.data_ptr(), *reversed(outer))
 

@@ -59,3 +59,11 @@ def test_binding_names_a_tensor_that_is_missing_or_has_other_dimensions(monkeypa
     for bad in (None, _lib.dsa_rope_t(), 64):
         with pytest.raises(TypeError, match="^rope must"):
             _lib.dsa_latent_append(g, _lib.DSA_BF16, None, None, bad, q_in=part, q_out=part, ws=ws)
+
+
+@pytest.mark.parametrize("shape,strides,want", [((1, 2, 64), (130, 64, 1), (128, 64)), ((1, 1, 64), (577, 577, 1), (64, 64)), ((3, 1, 64), (72, 5, 1), (72, 64)),
+                                                ((1, 576), (577, 1), (576,)), ((1, 1, 192), (1 << 40, 3, 1), (192, 192)), ((2, 1, 64), (0, 9, 1), (0, 64))])
+def test_strides_over_a_single_element_say_nothing(shape, strides, want):
+    """A single token, or head, may lie at any stride in its tensor: 577 or 130 is no multiple of 8, but never taken."""
+    t = torch.zeros(4096, dtype=torch.bfloat16).as_strided(shape, strides)
+    assert _lib._tensor("x", t, torch.bfloat16, shape, -1)[1:] == want
