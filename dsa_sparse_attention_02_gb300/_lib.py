@@ -207,7 +207,10 @@ class Geometry:
         self.c = dsa_geom_t(self.B, self.T, self.max_seq_len, self.num_pages, 64,
                             int(block_table.shape[1]) if block_table.dim() == 2 else 0,
                             _dptr(seq_lens), _dptr(cu_q), _dptr(block_table))
-        self.ref = C.byref(self.c)
+
+    @property
+    def ref(self):
+        return C.byref(self.c)
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:

@@ -67,3 +67,12 @@ def test_strides_over_a_single_element_say_nothing(shape, strides, want):
     """A single token, or head, may lie at any stride in its tensor: 577 or 130 is no multiple of 8, but never taken."""
     t = torch.zeros(4096, dtype=torch.bfloat16).as_strided(shape, strides)
     assert _lib._tensor("x", t, torch.bfloat16, shape, -1)[1:] == want
+
+
+def test_a_geometry_passes_the_sizes_it_has_now():
+    """`ref` follows `c`: a program that gives a geometry other sizes or tables by a new `c` is understood."""
+    g = _lib.Geometry.__new__(_lib.Geometry)
+    g.c = geom()
+    assert g.ref._obj is g.c
+    g.c = geom(T=7)
+    assert g.ref._obj is g.c and g.ref._obj.T == 7
