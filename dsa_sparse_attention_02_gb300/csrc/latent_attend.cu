@@ -57,6 +57,9 @@ struct LatentShape {
   // an odd ring one would come to a place that the other's load has not reached yet, and take the phase
   // before that for the one it waits for.)
   static_assert(!kRecord || (kPairs % 2 == 0 && kCodes % 2 == 0), "a place has one user");
+  // (bf16 rows: the ring may be odd. An issuer of scores comes to pair 4 n + j only when those of page n - 2 have been
+  // read, for which all its pairs, up to 4 n - 5, had arrived: the load before in that place, 4 n + j - kPairs, as well.)
+  static_assert(kRecord || kPairs >= 8, "the place's last load is behind the issuer");
   // Scores, from column 256 on. bf16 rows: a page's in one place (two, one of each issuer), two pages at a
   // time. Records: the rotated part's and three of the scales' in a place each, the last scale's in the
   // rotated part's. P: one of a page, or three, the last scale's in the first's place.
