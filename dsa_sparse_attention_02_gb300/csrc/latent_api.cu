@@ -74,11 +74,11 @@ dsa_status_t dsa_latent_append(const dsa_geom_t* geom, dsa_dtype_t kv_dtype, con
   LatentAppendArgs A{};
   if (!format_of(kv_dtype, &A.kv_format) || !rope_ok(rope)) return DSA_ERR_INVALID_ARG;
   if (!(eps >= 0.f) || !std::isfinite(eps)) return DSA_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, kHeaderBytes)) return DSA_ERR_WORKSPACE;
+  if (geom->T == 0) return DSA_OK;                 // (tensors without elements have no address)
   if ((q_in == nullptr) != (q_out == nullptr)) return DSA_ERR_INVALID_ARG;
   if (q_in && (H < 1 || H > kMaxHeads)) return DSA_ERR_INVALID_ARG;
   if (!kv_in && (kv_cache || kv_out)) return DSA_ERR_INVALID_ARG;
-  if (!ws_ok(ws, ws_bytes, kHeaderBytes)) return DSA_ERR_WORKSPACE;
-  if (geom->T == 0) return DSA_OK;
   if (!kv_in && !q_in) return DSA_ERR_INVALID_ARG;
   if (kv_in && (!kv_cache || !aligned16(kv_in) || !aligned16(kv_cache) || !stride_ok(kv_stride, 576) ||
                 (gamma && !aligned16(gamma)) || (kv_out && !aligned16(kv_out))))

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from dsa_sparse_attention_02_gb300 import _lib, build
-from test_gqa_abi import UNS, WSP, geom, lib, ref  # noqa: F401
+from test_gqa_abi import INV, OK, UNS, WSP, geom, lib, ref  # noqa: F401
 
 
 def test_loads_go_to_the_own_block_alone():
@@ -76,3 +76,17 @@ def test_a_geometry_passes_the_sizes_it_has_now():
     assert g.ref._obj is g.c
     g.c = geom(T=7)
     assert g.ref._obj is g.c and g.ref._obj.T == 7
+
+
+def test_an_empty_batch_is_no_error(lib):  # noqa: F811
+    """Tensors without elements have no address, the cache has one."""
+    rope = _lib.Rope().c
+
+    def append(T, kv=None, cache=16, ko=None, H=4, q=None, qo=None):
+        return lib.dsa_latent_append(ref(geom(T=T)), _lib.DSA_BF16, kv, 576, 16, 1e-6, ref(rope), cache, ko, H, q, 256, 64, qo, 256, 64, 256, 256, None)
+    assert append(0) == OK and append(0, q=16) == OK and append(0, H=0) == OK
+    assert append(1) == INV and append(1, kv=16, q=16) == INV
+    assert lib.dsa_latent_attend(ref(geom(T=0)), _lib.DSA_BF16, 16, None, 16, 0.1, None, None, 256, 256, None) == OK
+    assert lib.dsa_latent_gather(ref(geom()), _lib.DSA_BF16, 16, None, 16, 0, None, 576, 256, 256, None) == OK
+    assert lib.dsa_latent_attend_expanded(1, 0, 0, 16, 16, 4, None, 768, 192, None, 512, 128, None, 512, 128, None, 64, 0.1, None, None, 256, 256,
+                                          None) == OK
