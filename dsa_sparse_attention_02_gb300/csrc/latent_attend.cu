@@ -27,13 +27,18 @@
 //               scores, and to the weights: P^T of each scale's 128 columns is its own. (With code *
 //               scale rounded to bf16 instead, log-sum-exps were off by 0.3%.) The queries' latent part
 //               is brought to f16 by an exact power of two a row.
-// What bounds it. bf16 rows, 16 heads: HBM (376 MB in 71 us, of which 60 at 6.0 TB/s). 64 rows an item:
+//
+// Weights meet bf16 rows in bf16, as both operands of a product are of one type; their sum is of the fp32
+// weights. (Against 64 bits outputs are off by 0.0019 to 0.0021 of their norm, with fp32 weights 0.0017, which is the
+// output's own rounding.) Weights times scales meet records in f16, where that is not to be seen.
+//
+// What bounds it. bf16 rows, 16 heads: HBM (376 MB in 71 us, of which 57 at 6.6 TB/s). 64 rows an item:
 // the chain of a page, as two pages are all that fits beside the queries: loads (1900 clocks) ->
-// scores (2000) -> softmax (1200) -> values (1500), 3,000 clocks a page (128 heads: 129.5 us, pages read
+// scores (2000) -> softmax (1200) -> values (1500), 3,030 clocks a page (128 heads: 129.5 us, pages read
 // from HBM once for two items in neighbouring blocks, 3.0 TB/s). Records, 64 rows: values -> conversion of the next page's last two pairs ->
 // their scores -> softmax -> weights, and the softmax warps' own steps (each wait 200 clocks), which
-// are as long: 4,700 clocks a page (8 contexts of 131072 in e4m3: 269 us, 2.6 TB/s). Issue slots 54%,
-// tensor cores 26% busy (when it took 370 us).
+// are as long: 4,500 to 4,700 clocks a page, with fewer rows too (8 contexts of 131072 in e4m3, 64 rows: 269 us,
+// 2.6 TB/s; issue slots 51%, tensor pipe 35% busy).
 // All units are laid end to end and cut into runs of equal cost, one per SM; cut items are merged.
 #include "latent_units.cuh"
 
@@ -957,7 +962,9 @@ int latent_rows(const GeomDev& g, int H) {
 
 // Whether two items of a request go to two neighbouring blocks: where it has just two in the mean. (64 requests
 // of 128 rows over 5000 keys 129.5 us, without 143; 40 of 80 rows over 6750 108 and 118; 32 of 128 over 2250 43 and
-// 44; 8 over 3000 28 and 27; a single one over 30000 50 and 39.5, for its parts are merged by fewer blocks.)
+// 44; 8 over 3000 28 and 27; a single one over 30000 50 and 39.5, for its parts are merged by fewer blocks. With more
+// rows the other items are mostly found in L2, and an odd one leaves half of a run idle: 40 of 192 rows over 6750 200
+// and 167.5; 16 of 192 over 3000 51 and 44.5; 8 of 256 over 3000 35 and 34; but 64 of 256 over 6100 279 and 302.)
 bool latent_pairs(const GeomDev& g, int H) {
   const int64_t rows = ((int64_t)g.T + g.B - 1) / g.B * H;
   return rows > 64 && rows <= 128;

@@ -561,7 +561,7 @@ size_t dsa_latent_append_workspace_size(const dsa_geom_t* geom);
  *     queries of the other sign possibly in its own column only). out overlaps no input.
  *   Weights are rounded to bf16 before they meet the rows (records: weight times scale, to f16,
  *     a row's largest being 2^7 at least, or below that by what its key's largest scale is below
- *     2^-88; scales below 2^100); all sums are fp32; out is rounded once more, to bf16.
+ *     2^-88; scales below 2^90); all sums are fp32; out is rounded once more, to bf16.
  *     Over records the queries' first 512 values are exact down to 2^-31 of a row's largest.
  *   sm_scale >= 0, and sm_scale * log2(e) finite in fp32. T * H <= 2^31 - 128.
  */
